@@ -158,6 +158,10 @@ int hip_status(hipError_t err) {
 
 }  // namespace
 
+namespace moe {
+int report_hip(hipError_t err) { return hip_status(err); }
+}  // namespace moe
+
 extern "C" {
 
 int moe_w4a16_workspace_size(const moe_w4a16_problem* p, size_t* bytes) {

@@ -1,0 +1,240 @@
+// ffn_api.cpp -- host side of include/moe_ffn.h: argument checks, workspace
+// layout and launch sequences. Every check runs before the first launch.
+#include "../../include/moe_ffn.h"
+#include "ffn_internal.h"
+#include "internal.h"
+
+namespace {
+
+using ffn::Product;
+
+constexpr int32_t kMaxWidth = 1 << 20;
+constexpr int64_t kMaxRows = 0x7fffffff;
+
+size_t region(int64_t bytes) { return ((size_t)bytes + 255) / 256 * 256; }
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+int check_problem(const moe_ffn_problem* p, int32_t multiple) {
+  if (!p) return MOE_ERR_NULL;
+  if (p->num_tokens < 0 || p->num_tokens > kMaxRows || p->hidden <= 0 || p->inter <= 0 ||
+      p->hidden > kMaxWidth || p->inter > kMaxWidth || p->hidden % multiple ||
+      p->inter % multiple)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+int check_rows(int64_t rows, int32_t width) {
+  if (rows < 0 || rows > kMaxRows || width <= 0 || width > kMaxWidth || width % 32)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+// every pointer given, then every one aligned
+int check_pointers(const void* const* ptrs, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!ptrs[i]) return MOE_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!aligned16(ptrs[i])) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need == 0) return MOE_OK;
+  if (!ws) return MOE_ERR_NULL;
+  if (!aligned16(ws)) return MOE_ERR_ALIGNMENT;
+  return have < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+int done(hipError_t e) { return e == hipSuccess ? MOE_OK : moe::report_hip(e); }
+
+// MXFP4 [rows, width] in a workspace: codes, then scales
+struct MxRegion {
+  size_t codes, scales;
+  MxRegion(int64_t rows, int32_t width)
+      : codes(region(rows * (width / 2))), scales(region(rows * (width / 32))) {}
+  size_t bytes() const { return codes + scales; }
+};
+
+size_t workspace_of(const moe_ffn_problem* p, int pass) {
+  const int64_t T = p->num_tokens, I = p->inter;
+  if (T == 0) return 0;
+  if (pass == MOE_FFN_FORWARD) return region(2 * T * I);
+  if (pass == MOE_FFN_BACKWARD) return region(4 * T * I) + region(2 * T * I);
+  return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes();
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_ffn_workspace_size(const moe_ffn_problem* p, int pass, size_t* bytes) {
+  if (!p || !bytes) return MOE_ERR_NULL;
+  if (pass < MOE_FFN_FORWARD || pass > MOE_FFN_FORWARD_MXFP4) return MOE_ERR_UNSUPPORTED;
+  const int st = check_problem(p, pass == MOE_FFN_FORWARD_MXFP4 ? 32 : 8);
+  if (st != MOE_OK) return st;
+  *bytes = workspace_of(p, pass);
+  return MOE_OK;
+}
+
+int moe_ffn_forward(const void* x, const void* w13, const void* w2, void* out, float* gate_up,
+                    const moe_ffn_problem* p, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  int st = check_problem(p, 8);
+  if (st != MOE_OK || p->num_tokens == 0) return st;
+  const void* ptrs[] = {x, w13, w2, out};
+  if ((st = check_pointers(ptrs, 4)) != MOE_OK) return st;
+  if (gate_up && !aligned16(gate_up)) return MOE_ERR_ALIGNMENT;
+  st = check_workspace(workspace, workspace_bytes, workspace_of(p, MOE_FFN_FORWARD));
+  if (st != MOE_OK) return st;
+  const int64_t T = p->num_tokens, H = p->hidden, I = p->inter;
+  hipStream_t s = (hipStream_t)stream;
+  Product up{x, w13, nullptr, nullptr, 2 * H, 2 * H, T, p->inter, H};
+  up.out = workspace;
+  up.aux = gate_up;
+  hipError_t e = ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, s);
+  if (e != hipSuccess) return done(e);
+  Product down{workspace, w2, nullptr, nullptr, 2 * I, 2 * I, T, p->hidden, I};
+  down.out = out;
+  return done(ffn::launch_product(ffn::kNT, ffn::kStoreBf16, down, s));
+}
+
+int moe_ffn_backward(const void* dout, const void* x, const float* gate_up, const void* w13,
+                     const void* w2, void* dx, void* dw13, void* dw2, const moe_ffn_problem* p,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  int st = check_problem(p, 8);
+  if (st != MOE_OK) return st;
+  if (!dw13 != !dw2 || (!dx && !dw13)) return MOE_ERR_NULL;
+  if (!aligned16(dx) || !aligned16(dw13) || !aligned16(dw2)) return MOE_ERR_ALIGNMENT;
+  const int64_t T = p->num_tokens, H = p->hidden, I = p->inter;
+  if (T > 0) {
+    const void* ptrs[] = {dout, x, gate_up, w13, w2};
+    if ((st = check_pointers(ptrs, 5)) != MOE_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, workspace_of(p, MOE_FFN_BACKWARD));
+    if (st != MOE_OK) return st;
+  }
+  hipStream_t s = (hipStream_t)stream;
+  char* dgu = (char*)workspace;                      // bf16 [T, 2I]
+  char* h = T > 0 ? dgu + region(4 * T * I) : dgu;   // bf16 [T, I]
+  hipError_t e = hipSuccess;
+  if (T > 0) {
+    Product dh{dout, w2, nullptr, nullptr, 2 * H, 2 * I, T, p->inter, H};
+    dh.out = dgu;
+    dh.out2 = h;
+    dh.aux = const_cast<float*>(gate_up);
+    e = ffn::launch_product(ffn::kNN, ffn::kSwigluGrad, dh, s);
+    if (e == hipSuccess && dx) {
+      Product d{dgu, w13, nullptr, nullptr, 4 * I, 2 * H, T, p->hidden, 2 * I};
+      d.out = dx;
+      e = ffn::launch_product(ffn::kNN, ffn::kStoreBf16, d, s);
+    }
+  }
+  if (e == hipSuccess && dw13) {
+    Product d13{dgu, x, nullptr, nullptr, 4 * I, 2 * H, 2 * I, p->hidden, T};
+    d13.out = dw13;
+    e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d13, s);
+    if (e == hipSuccess) {
+      Product d2{dout, h, nullptr, nullptr, 2 * H, 2 * I, H, p->inter, T};
+      d2.out = dw2;
+      e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d2, s);
+    }
+  }
+  return done(e);
+}
+
+int moe_mxfp4_quantize(const void* x, int32_t type, int64_t rows, int32_t width, uint8_t* codes,
+                       uint8_t* scales, void* stream) {
+  int st = check_rows(rows, width);
+  if (st != MOE_OK) return st;
+  if (type < MOE_TYPE_BF16 || type > MOE_TYPE_FP32) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const void* ptrs[] = {x, codes};
+  if (!scales) return MOE_ERR_NULL;
+  if ((st = check_pointers(ptrs, 2)) != MOE_OK) return st;
+  return done(ffn::launch_mx_quantize(x, type, rows, width, codes, scales, (hipStream_t)stream));
+}
+
+int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t width,
+                         int32_t type, void* out, void* stream) {
+  int st = check_rows(rows, width);
+  if (st != MOE_OK) return st;
+  if (type < MOE_TYPE_BF16 || type > MOE_TYPE_FP32) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const void* ptrs[] = {codes, out};
+  if (!scales) return MOE_ERR_NULL;
+  if ((st = check_pointers(ptrs, 2)) != MOE_OK) return st;
+  return done(
+      ffn::launch_mx_dequantize(codes, scales, rows, width, type, out, (hipStream_t)stream));
+}
+
+int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, int quantize,
+                                    size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL;
+  const int st = check_rows(rows, width);
+  if (st != MOE_OK) return st;
+  if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
+  *bytes = quantize && rows ? MxRegion(rows, width).bytes() : 0;
+  return MOE_OK;
+}
+
+int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
+                     const uint8_t* b_scales, int64_t rows, int32_t cols, int32_t width,
+                     int32_t out_type, void* out, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  size_t need = 0;
+  int st = moe_mxfp4_matmul_workspace_size(rows, cols, width, !a_scales, &need);
+  if (st != MOE_OK) return st;
+  if (out_type != MOE_TYPE_BF16 && out_type != MOE_TYPE_FP32) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  const void* ptrs[] = {a, b, out};
+  if (!b_scales) return MOE_ERR_NULL;
+  if ((st = check_pointers(ptrs, 3)) != MOE_OK) return st;
+  if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (!a_scales) {
+    uint8_t* codes = (uint8_t*)workspace;
+    uint8_t* scales = codes + MxRegion(rows, width).codes;
+    const hipError_t e =
+        ffn::launch_mx_quantize(a, MOE_TYPE_BF16, rows, width, codes, scales, s);
+    if (e != hipSuccess) return done(e);
+    a = codes;
+    a_scales = scales;
+  }
+  Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
+  d.out = out;
+  return done(ffn::launch_product_mx(
+      out_type == MOE_TYPE_FP32 ? ffn::kStoreF32 : ffn::kStoreBf16, d, s));
+}
+
+int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_scales,
+                          const uint8_t* w2, const uint8_t* w2_scales, void* out,
+                          const moe_ffn_problem* p, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+  int st = check_problem(p, 32);
+  if (st != MOE_OK || p->num_tokens == 0) return st;
+  const void* ptrs[] = {x, w13, w2, out};
+  if (!w13_scales || !w2_scales) return MOE_ERR_NULL;
+  if ((st = check_pointers(ptrs, 4)) != MOE_OK) return st;
+  st = check_workspace(workspace, workspace_bytes, workspace_of(p, MOE_FFN_FORWARD_MXFP4));
+  if (st != MOE_OK) return st;
+  const int64_t T = p->num_tokens;
+  const int32_t H = p->hidden, I = p->inter;
+  hipStream_t s = (hipStream_t)stream;
+  const MxRegion rx(T, H), rh(T, I);
+  uint8_t* xc = (uint8_t*)workspace;
+  uint8_t* xs = xc + rx.codes;
+  uint8_t* hc = xc + rx.bytes();
+  uint8_t* hs = hc + rh.codes;
+  hipError_t e = ffn::launch_mx_quantize(x, MOE_TYPE_BF16, T, H, xc, xs, s);
+  if (e != hipSuccess) return done(e);
+  Product up{xc, w13, xs, w13_scales, H / 2, H / 2, T, I, H};
+  up.out = hc;
+  up.aux = hs;
+  e = ffn::launch_product_mx(ffn::kSwigluMx, up, s);
+  if (e != hipSuccess) return done(e);
+  Product down{hc, w2, hs, w2_scales, I / 2, I / 2, T, H, I};
+  down.out = out;
+  return done(ffn::launch_product_mx(ffn::kStoreBf16, down, s));
+}
+
+}  // extern "C"

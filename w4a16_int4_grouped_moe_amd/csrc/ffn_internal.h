@@ -1,0 +1,50 @@
+// ffn_internal.h -- what the feed-forward and MXFP4 entry points share.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ffn {
+
+// What a product's epilogue does with its tile. "N" below is the product's
+// column count (gate_up: the intermediate width, each column being a gate and
+// an up column of the weight matrix).
+enum Epilogue {
+  kStoreBf16 = 0,   // out bf16 [M, N]
+  kStoreF32 = 1,    // out fp32 [M, N]
+  kSwiglu = 2,      // out bf16 h [M, N]; aux fp32 [M, 2N] pre-activations or NULL
+  kSwigluMx = 3,    // out e2m1 codes of h [M, N/2], aux its scale bytes [M, N/32]
+  kSwigluGrad = 4,  // the product is dh: aux fp32 [M, 2N] pre-activations (read),
+                    // out bf16 [M, 2N] their gradients, out2 bf16 h [M, N]
+};
+
+// D[m, n] = sum_k A(m, k) B(n, k). An operand is "K contiguous" (element
+// (r, k) at r * ld + k) or "row contiguous" (at k * ld + r); which one is a
+// template parameter of the kernel (see Layout).
+enum Layout { kNT = 0, kNN = 1, kTN = 2 };  // A/B: KC/KC, KC/RC, RC/RC
+
+struct Product {
+  const void* a;
+  const void* b;
+  const uint8_t* a_scales = nullptr;  // MXFP4: e8m0 bytes [M, K/32], [rows of b, K/32]
+  const uint8_t* b_scales = nullptr;
+  int64_t lda, ldb;  // bytes from one row (KC) or one k (RC) to the next
+  int64_t M;
+  int32_t N;
+  int64_t K;
+  void* out = nullptr;
+  void* out2 = nullptr;
+  void* aux = nullptr;
+};
+
+// bf16 operands
+hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, hipStream_t stream);
+// MXFP4 operands, both K contiguous; K a multiple of 32
+hipError_t launch_product_mx(Epilogue epilogue, const Product& p, hipStream_t stream);
+
+// x [rows, width] (type: MOE_TYPE_*) -> e2m1 codes [rows, width/2], scales [rows, width/32]
+hipError_t launch_mx_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
+                              uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                int32_t width, int32_t type, void* out, hipStream_t stream);
+
+}  // namespace ffn

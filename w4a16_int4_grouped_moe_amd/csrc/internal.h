@@ -166,4 +166,8 @@ hipError_t launch_combine(const float* y, const float* s, const int32_t* topk_id
                           const float* topk_weights, uint16_t* out, int64_t T, int32_t H,
                           int32_t k, int32_t E, int32_t base, hipStream_t stream);
 
+// The status of a failed HIP call (MOE_ERR_HIP), its message kept for
+// moe_w4a16_status_string.
+int report_hip(hipError_t err);
+
 }  // namespace moe
