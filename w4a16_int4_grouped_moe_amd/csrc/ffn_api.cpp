@@ -48,20 +48,31 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 
 int done(hipError_t e) { return e == hipSuccess ? MOE_OK : moe::report_hip(e); }
 
-// MXFP4 [rows, width] in a workspace: codes, then scales
+// MXFP4 [rows, width] in a workspace: codes, then padded scales
 struct MxRegion {
   size_t codes, scales;
   MxRegion(int64_t rows, int32_t width)
-      : codes(region(rows * (width / 2))), scales(region(rows * (width / 32))) {}
+      : codes(region(rows * (width / 2))), scales(region(rows * ffn::scale_stride(width))) {}
   size_t bytes() const { return codes + scales; }
 };
+
+// Widths that are not whole stages: the given scales are copied into padded rows
+bool needs_padding(int32_t width) { return width % 256 != 0; }
+size_t padded(int64_t rows, int32_t width) {
+  return needs_padding(width) ? region(rows * ffn::scale_stride(width)) : 0;
+}
+// Given scales of whole stages are read in place, eight bytes at a time
+bool scales_aligned(const uint8_t* s, int32_t width) {
+  return needs_padding(width) || ((uintptr_t)s & 7u) == 0;
+}
 
 size_t workspace_of(const moe_ffn_problem* p, int pass) {
   const int64_t T = p->num_tokens, I = p->inter;
   if (T == 0) return 0;
   if (pass == MOE_FFN_FORWARD) return region(2 * T * I);
   if (pass == MOE_FFN_BACKWARD) return region(4 * T * I) + region(2 * T * I);
-  return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes();
+  return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes() +
+         padded(2 * I, p->hidden) + padded(p->hidden, p->inter);
 }
 
 }  // namespace
@@ -151,7 +162,8 @@ int moe_mxfp4_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
   const void* ptrs[] = {x, codes};
   if (!scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 2)) != MOE_OK) return st;
-  return done(ffn::launch_mx_quantize(x, type, rows, width, codes, scales, (hipStream_t)stream));
+  return done(
+      ffn::launch_mx_quantize(x, type, rows, width, codes, scales, false, (hipStream_t)stream));
 }
 
 int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t width,
@@ -173,7 +185,9 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   const int st = check_rows(rows, width);
   if (st != MOE_OK) return st;
   if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
-  *bytes = quantize && rows ? MxRegion(rows, width).bytes() : 0;
+  *bytes = rows == 0 ? 0
+                     : (quantize ? MxRegion(rows, width).bytes() : padded(rows, width)) +
+                           padded(cols, width);
   return MOE_OK;
 }
 
@@ -189,17 +203,28 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
   const void* ptrs[] = {a, b, out};
   if (!b_scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 3)) != MOE_OK) return st;
+  if ((a_scales && !scales_aligned(a_scales, width)) || !scales_aligned(b_scales, width))
+    return MOE_ERR_ALIGNMENT;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   hipStream_t s = (hipStream_t)stream;
+  uint8_t* ws = (uint8_t*)workspace;
+  const uint8_t* a_given = a_scales;
+  hipError_t e = hipSuccess;
   if (!a_scales) {
-    uint8_t* codes = (uint8_t*)workspace;
-    uint8_t* scales = codes + MxRegion(rows, width).codes;
-    const hipError_t e =
-        ffn::launch_mx_quantize(a, MOE_TYPE_BF16, rows, width, codes, scales, s);
-    if (e != hipSuccess) return done(e);
-    a = codes;
-    a_scales = scales;
+    const MxRegion r(rows, width);
+    e = ffn::launch_mx_quantize(a, MOE_TYPE_BF16, rows, width, ws, ws + r.codes, true, s);
+    a = ws;
+    a_scales = ws + r.codes;
+    ws += r.bytes();
   }
+  if (e == hipSuccess && needs_padding(width)) {
+    uint8_t* pa = ws;
+    uint8_t* pb = a_given ? pa + padded(rows, width) : ws;
+    e = ffn::launch_mx_pad_scales(a_given, a_given ? rows : 0, pa, b_scales, cols, pb, width, s);
+    if (a_given) a_scales = pa;
+    b_scales = pb;
+  }
+  if (e != hipSuccess) return done(e);
   Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
   d.out = out;
   return done(ffn::launch_product_mx(
@@ -215,6 +240,8 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   const void* ptrs[] = {x, w13, w2, out};
   if (!w13_scales || !w2_scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 4)) != MOE_OK) return st;
+  if (!scales_aligned(w13_scales, p->hidden) || !scales_aligned(w2_scales, p->inter))
+    return MOE_ERR_ALIGNMENT;
   st = check_workspace(workspace, workspace_bytes, workspace_of(p, MOE_FFN_FORWARD_MXFP4));
   if (st != MOE_OK) return st;
   const int64_t T = p->num_tokens;
@@ -225,7 +252,17 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   uint8_t* xs = xc + rx.codes;
   uint8_t* hc = xc + rx.bytes();
   uint8_t* hs = hc + rh.codes;
-  hipError_t e = ffn::launch_mx_quantize(x, MOE_TYPE_BF16, T, H, xc, xs, s);
+  uint8_t* s13 = hc + rh.bytes();
+  uint8_t* s2 = s13 + padded(2 * (int64_t)I, H);
+  hipError_t e = ffn::launch_mx_quantize(x, MOE_TYPE_BF16, T, H, xc, xs, true, s);
+  if (e == hipSuccess && needs_padding(H)) {
+    e = ffn::launch_mx_pad_scales(w13_scales, 2 * (int64_t)I, s13, nullptr, 0, nullptr, H, s);
+    w13_scales = s13;
+  }
+  if (e == hipSuccess && needs_padding(I)) {
+    e = ffn::launch_mx_pad_scales(w2_scales, H, s2, nullptr, 0, nullptr, I, s);
+    w2_scales = s2;
+  }
   if (e != hipSuccess) return done(e);
   Product up{xc, w13, xs, w13_scales, H / 2, H / 2, T, I, H};
   up.out = hc;

@@ -46,9 +46,10 @@ __device__ __forceinline__ void load8(const void* x, int64_t unit, float* v) {
   }
 }
 
+// pad: 0, or the scale bytes of a row (width/32) where they go into padded rows
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x,
-                                                            int64_t units,
+                                                            int64_t units, int32_t pad,
                                                             uint32_t* __restrict__ codes,
                                                             uint8_t* __restrict__ scales) {
   // units is a multiple of 4: a block's lanes are all in or all out
@@ -78,7 +79,19 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], 1.0f, 2);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], 1.0f, 3);
   codes[u] = c;
-  if ((u & 3) == 0) scales[u >> 2] = bad ? 255 : (uint8_t)s;
+  if ((u & 3) == 0) {
+    const uint8_t byte = bad ? 255 : (uint8_t)s;
+    const int64_t b = u >> 2;
+    if (pad == 0) {
+      scales[b] = byte;
+    } else {
+      const int64_t row = b / pad;
+      const int32_t at = (int32_t)(b - row * pad), stride = (pad + 7) / 8 * 8;
+      scales[row * stride + at] = byte;
+      if (at == pad - 1)
+        for (int32_t i = pad; i < stride; ++i) scales[row * stride + i] = 127;
+    }
+  }
 }
 
 template <int TYPE>
@@ -116,6 +129,20 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint32_t* __
   }
 }
 
+// One thread a padded scale byte, of the first matrix and then of the second.
+__global__ __launch_bounds__(kThreads) void pad_scales_kernel(
+    const uint8_t* __restrict__ s0, int64_t n0, uint8_t* __restrict__ out0,
+    const uint8_t* __restrict__ s1, int64_t n1, uint8_t* __restrict__ out1, int32_t blocks,
+    int32_t stride) {
+  int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (u >= n0 + n1) return;
+  const bool second = u >= n0;
+  if (second) u -= n0;
+  const int64_t row = u / stride;
+  const int32_t at = (int32_t)(u - row * stride);
+  (second ? out1 : out0)[u] = at < blocks ? (second ? s1 : s0)[row * blocks + at] : 127;
+}
+
 // work-groups for `units` lanes: one dimension of a launch holds fewer than 2^32 lanes
 dim3 grid_of(int64_t units) {
   const int64_t groups = (units + kThreads - 1) / kThreads;
@@ -125,19 +152,31 @@ dim3 grid_of(int64_t units) {
 
 }  // namespace
 
+hipError_t launch_mx_pad_scales(const uint8_t* s0, int64_t rows0, uint8_t* out0,
+                                const uint8_t* s1, int64_t rows1, uint8_t* out1, int32_t width,
+                                hipStream_t stream) {
+  const int32_t stride = (int32_t)scale_stride(width);
+  if (rows0 + rows1 == 0) return hipSuccess;
+  hipLaunchKernelGGL(pad_scales_kernel, grid_of((rows0 + rows1) * stride), dim3(kThreads), 0,
+                     stream, s0, rows0 * stride, out0, s1, rows1 * stride, out1, width / 32,
+                     stride);
+  return hipGetLastError();
+}
+
 hipError_t launch_mx_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
-                              uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+                              uint8_t* codes, uint8_t* scales, bool padded, hipStream_t stream) {
   const int64_t units = rows * (width / 8);
   if (units == 0) return hipSuccess;
   const dim3 grid = grid_of(units), block(kThreads);
+  const int32_t pad = padded && width % 256 ? width / 32 : 0;
   if (type == MOE_TYPE_BF16)
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_BF16>, grid, block, 0, stream, x, units,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_BF16>, grid, block, 0, stream, x, units, pad,
                        (uint32_t*)codes, scales);
   else if (type == MOE_TYPE_FP16)
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP16>, grid, block, 0, stream, x, units,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP16>, grid, block, 0, stream, x, units, pad,
                        (uint32_t*)codes, scales);
   else
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP32>, grid, block, 0, stream, x, units,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP32>, grid, block, 0, stream, x, units, pad,
                        (uint32_t*)codes, scales);
   return hipGetLastError();
 }
