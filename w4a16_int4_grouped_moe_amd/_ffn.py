@@ -3,9 +3,12 @@
 from __future__ import annotations
 
 import ctypes
+import functools
+
+import torch
 
 from . import _binding
-from ._binding import _check, _need, _torch
+from ._binding import _check, _need
 
 MOE_TYPE_BF16 = 0
 MOE_TYPE_FP16 = 1
@@ -53,63 +56,67 @@ def _library():
 
 def _launch(device, fn, *args):
     """fn on the device's current stream, with that device current."""
-    torch = _torch()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream))
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 def _gpu(t, name):
-    torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     return t.device
 
 
 def _shaped(t, name, dtype, shape, device):
-    _need(t, name, dtype, len(shape), device)
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    return t
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        return t
+    _need(t, name, dtype, len(shape), device)  # says what is wrong
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
 
 
 def _result(t, name, dtype, shape, device):
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     return _shaped(t, name, dtype, shape, device)
 
 
 def _scratch(workspace, need, device):
     if workspace is None:
-        return _torch().empty(max(need, 1), dtype=_torch().uint8, device=device)
-    _need(workspace, "workspace", _torch().uint8, 1, device)
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    _need(workspace, "workspace", torch.uint8, 1, device)
     return workspace
 
 
-def _pass_bytes(p, kind):
+@functools.lru_cache(maxsize=4096)
+def _problem(num_tokens, hidden, inter, kind):
+    """The sizes as the library takes them, and the workspace bytes (a pure
+    function of the sizes)."""
+    p = FfnProblem(num_tokens, hidden, inter)
     n = ctypes.c_size_t(0)
     _check(_library().moe_ffn_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)))
-    return n.value
+    return ctypes.byref(p), n.value
 
 
 def ffn_workspace_size(num_tokens: int, hidden: int, inter: int, kind: int) -> int:
     """Bytes of workspace of one call (kind: MOE_FFN_*; host only)."""
-    return _pass_bytes(FfnProblem(num_tokens, hidden, inter), kind)
+    return _problem(num_tokens, hidden, inter, kind)[1]
 
 
 def _block(x, w13, w2):
     """The feed-forward block's shapes: (device, T, H, I)."""
-    torch = _torch()
     dev = _gpu(x, "x")
-    _need(x, "x", torch.bfloat16, 2, dev)
-    _need(w2, "w2", torch.bfloat16, 2, dev)
+    if x.dim() != 2 or not isinstance(w2, torch.Tensor) or w2.dim() != 2:
+        _need(x, "x", torch.bfloat16, 2, dev)
+        _need(w2, "w2", torch.bfloat16, 2, dev)
     T, H = x.shape
     I = w2.shape[1]
+    _shaped(x, "x", torch.bfloat16, (T, H), dev)
     _shaped(w13, "w13", torch.bfloat16, (2 * I, H), dev)
     _shaped(w2, "w2", torch.bfloat16, (H, I), dev)
     return dev, T, H, I
@@ -120,15 +127,14 @@ def ffn_forward(x, w13, w2, out=None, gate_up=None, workspace=None):
     [2I, H] (gate rows, then up rows), w2 bf16 [H, I] -> out bf16 [T, H].
     gate_up: optional fp32 [T, 2I], receives the pre-activations that
     ffn_backward reads."""
-    torch = _torch()
     dev, T, H, I = _block(x, w13, w2)
     out = _result(out, "out", torch.bfloat16, (T, H), dev)
     if gate_up is not None:
         _shaped(gate_up, "gate_up", torch.float32, (T, 2 * I), dev)
-    p = FfnProblem(T, H, I)
-    ws = _scratch(workspace, _pass_bytes(p, MOE_FFN_FORWARD), dev)
+    p, need = _problem(T, H, I, MOE_FFN_FORWARD)
+    ws = _scratch(workspace, need, dev)
     _launch(dev, _library().moe_ffn_forward, x.data_ptr(), w13.data_ptr(), w2.data_ptr(),
-            out.data_ptr(), None if gate_up is None else gate_up.data_ptr(), ctypes.byref(p),
+            out.data_ptr(), None if gate_up is None else gate_up.data_ptr(), p,
             ws.data_ptr(), ws.numel())
     return out
 
@@ -137,18 +143,17 @@ def ffn_backward(dout, x, gate_up, w13, w2, dx=None, dw13=None, dw2=None, worksp
     """Gradients of the block (moe_ffn_backward): dout bf16 [T, H] and
     gate_up as ffn_forward wrote it -> (dx, dw13, dw2), bf16 of the shapes of
     x, w13 and w2. Given output tensors are overwritten."""
-    torch = _torch()
     dev, T, H, I = _block(x, w13, w2)
     _shaped(dout, "dout", torch.bfloat16, (T, H), dev)
     _shaped(gate_up, "gate_up", torch.float32, (T, 2 * I), dev)
     dx = _result(dx, "dx", torch.bfloat16, (T, H), dev)
     dw13 = _result(dw13, "dw13", torch.bfloat16, (2 * I, H), dev)
     dw2 = _result(dw2, "dw2", torch.bfloat16, (H, I), dev)
-    p = FfnProblem(T, H, I)
-    ws = _scratch(workspace, _pass_bytes(p, MOE_FFN_BACKWARD), dev)
+    p, need = _problem(T, H, I, MOE_FFN_BACKWARD)
+    ws = _scratch(workspace, need, dev)
     _launch(dev, _library().moe_ffn_backward, dout.data_ptr(), x.data_ptr(), gate_up.data_ptr(),
             w13.data_ptr(), w2.data_ptr(), dx.data_ptr(), dw13.data_ptr(), dw2.data_ptr(),
-            ctypes.byref(p), ws.data_ptr(), ws.numel())
+            p, ws.data_ptr(), ws.numel())
     return dx, dw13, dw2
 
 
@@ -156,33 +161,35 @@ class Mxfp4:
     """A matrix in MXFP4: codes uint8 [rows, width/2] (two e2m1 codes a byte,
     the even input low) and scales uint8 [rows, width/32] (e8m0)."""
 
+    __slots__ = ("_codes", "_scales", "_shape")
+
     def __init__(self, codes, scales):
-        torch = _torch()
         dev = _gpu(codes, "codes")
-        _need(codes, "codes", torch.uint8, 2, dev)
+        if codes.dim() != 2:
+            _need(codes, "codes", torch.uint8, 2, dev)
         rows, half = codes.shape
+        _shaped(codes, "codes", torch.uint8, (rows, half), dev)
         if half % (MX_BLOCK // 2):
             raise ValueError(f"codes hold {half} bytes a row, not whole blocks of 16")
         _shaped(scales, "scales", torch.uint8, (rows, half // (MX_BLOCK // 2)), dev)
-        self.codes = codes
-        self.scales = scales
+        self._codes = codes
+        self._scales = scales
+        self._shape = (rows, 2 * half)
 
-    @property
-    def shape(self):
-        return self.codes.shape[0], 2 * self.codes.shape[1]
+    codes = property(lambda self: self._codes)
+    scales = property(lambda self: self._scales)
+    shape = property(lambda self: self._shape)
+    device = property(lambda self: self._codes.device)
 
-    @property
-    def device(self):
-        return self.codes.device
+
+_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16,
+          torch.float32: MOE_TYPE_FP32}
 
 
 def _type_of(dtype):
-    torch = _torch()
-    types = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16,
-             torch.float32: MOE_TYPE_FP32}
-    if dtype not in types:
+    if dtype not in _TYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    return types[dtype]
+    return _TYPES[dtype]
 
 
 def _is_mx(q, name, device=None):
@@ -196,7 +203,6 @@ def _is_mx(q, name, device=None):
 def mxfp4_quantize(x, codes=None, scales=None) -> Mxfp4:
     """x [rows, width] (bf16, fp16 or fp32; width a multiple of 32) in MXFP4
     (moe_mxfp4_quantize). codes, scales: optional output tensors."""
-    torch = _torch()
     dev = _gpu(x, "x")
     kind = _type_of(x.dtype)
     _need(x, "x", x.dtype, 2, dev)
@@ -212,7 +218,6 @@ def mxfp4_quantize(x, codes=None, scales=None) -> Mxfp4:
 
 def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):
     """The values of q as dtype (default bfloat16; moe_mxfp4_dequantize)."""
-    torch = _torch()
     _is_mx(q, "q")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
@@ -223,6 +228,7 @@ def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def mxfp4_matmul_workspace_size(rows: int, cols: int, width: int, quantize: bool) -> int:
     """Bytes of workspace of mxfp4_matmul (quantize: a is a bf16 tensor)."""
     n = ctypes.c_size_t(0)
@@ -235,7 +241,6 @@ def mxfp4_matmul(a, b: Mxfp4, out=None, dtype=None, workspace=None):
     """a [M, K] times the transpose of b [N, K] (moe_mxfp4_matmul) -> [M, N]
     in dtype (bfloat16, the default, or float32). a: an Mxfp4, or a bf16
     tensor that is quantised as by mxfp4_quantize."""
-    torch = _torch()
     if isinstance(a, Mxfp4):
         dev, (M, K), codes, scales = a.device, a.shape, a.codes, a.scales.data_ptr()
     else:
@@ -261,7 +266,6 @@ def mxfp4_matmul(a, b: Mxfp4, out=None, dtype=None, workspace=None):
 def mxfp4_ffn_forward(x, w13: Mxfp4, w2: Mxfp4, out=None, workspace=None):
     """The gated feed-forward block on MXFP4 weights (moe_mxfp4_ffn_forward):
     x bf16 [T, H], w13 of [2I, H], w2 of [H, I] -> out bf16 [T, H]."""
-    torch = _torch()
     dev = _gpu(x, "x")
     _need(x, "x", torch.bfloat16, 2, dev)
     T, H = x.shape
@@ -271,9 +275,9 @@ def mxfp4_ffn_forward(x, w13: Mxfp4, w2: Mxfp4, out=None, workspace=None):
     if w13.shape != (2 * I, H) or w2.shape != (H, I):
         raise ValueError(f"w13 is {w13.shape} and w2 {w2.shape}, expected (2I, {H}) and ({H}, I)")
     out = _result(out, "out", torch.bfloat16, (T, H), dev)
-    p = FfnProblem(T, H, I)
-    ws = _scratch(workspace, _pass_bytes(p, MOE_FFN_FORWARD_MXFP4), dev)
+    p, need = _problem(T, H, I, MOE_FFN_FORWARD_MXFP4)
+    ws = _scratch(workspace, need, dev)
     _launch(dev, _library().moe_mxfp4_ffn_forward, x.data_ptr(), w13.codes.data_ptr(),
             w13.scales.data_ptr(), w2.codes.data_ptr(), w2.scales.data_ptr(), out.data_ptr(),
-            ctypes.byref(p), ws.data_ptr(), ws.numel())
+            p, ws.data_ptr(), ws.numel())
     return out
