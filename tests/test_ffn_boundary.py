@@ -131,10 +131,11 @@ def test_mxfp4_errors(lib):
 
 
 def test_matmul_errors(lib):
-    need = moe.mxfp4_matmul_workspace_size(4, 8, 64, True)
+    need = moe.mxfp4_matmul_workspace_size(40, 8, 64, True)
+    assert need >= 40 * 64 * 17 // 32
     assert moe.mxfp4_matmul_workspace_size(0, 8, 64, True) == 0
 
-    def call(a=A, sa=None, b=B, sb=C, m=4, n=8, k=64, t=0, o=D, ws=W, nb=need):
+    def call(a=A, sa=None, b=B, sb=C, m=40, n=8, k=64, t=0, o=D, ws=W, nb=need):
         return lib.moe_mxfp4_matmul(a, sa, b, sb, m, n, k, t, o, ws, nb, None)
 
     for bad in (dict(m=-1), dict(n=0), dict(n=12), dict(k=16), dict(m=1 << 31)):

@@ -281,7 +281,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         moe.mxfp4_matmul(x, moe.Mxfp4(w.codes[:7], w.scales[:7]))
     with pytest.raises(ValueError):
-        moe.mxfp4_matmul(x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        moe.mxfp4_matmul(rand(40, 64), w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         moe.Mxfp4(w.codes, w.scales[:, :1].contiguous())
     with pytest.raises(ValueError):

@@ -66,9 +66,25 @@ bool scales_aligned(const uint8_t* s, int32_t width) {
   return needs_padding(width) || ((uintptr_t)s & 7u) == 0;
 }
 
+// The block's two products as the few-row kernels take them
+bool few_tokens(const moe_ffn_problem* p, bool mx) {
+  Product up{}, down{};
+  up.M = down.M = p->num_tokens;
+  up.N = down.K = p->inter;
+  up.K = down.N = p->hidden;
+  return ffn::rows_fit(up, mx, mx ? ffn::kABf16 : ffn::kAAsIs, true) &&
+         ffn::rows_fit(down, mx, mx ? ffn::kAF32 : ffn::kAAsIs, false);
+}
+bool few_rows(int64_t rows, int32_t cols, int32_t width, bool quantize) {
+  Product d{};
+  d.M = rows, d.N = cols, d.K = width;
+  return ffn::rows_fit(d, true, quantize ? ffn::kABf16 : ffn::kAAsIs, false);
+}
+
 size_t workspace_of(const moe_ffn_problem* p, int pass) {
   const int64_t T = p->num_tokens, I = p->inter;
   if (T == 0) return 0;
+  if (pass == MOE_FFN_FORWARD_MXFP4 && few_tokens(p, true)) return region(4 * T * I);
   if (pass == MOE_FFN_FORWARD) return region(2 * T * I);
   if (pass == MOE_FFN_BACKWARD) return region(4 * T * I) + region(2 * T * I);
   return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes() +
@@ -103,11 +119,14 @@ int moe_ffn_forward(const void* x, const void* w13, const void* w2, void* out, f
   Product up{x, w13, nullptr, nullptr, 2 * H, 2 * H, T, p->inter, H};
   up.out = workspace;
   up.aux = gate_up;
-  hipError_t e = ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, s);
-  if (e != hipSuccess) return done(e);
   Product down{workspace, w2, nullptr, nullptr, 2 * I, 2 * I, T, p->hidden, I};
   down.out = out;
-  return done(ffn::launch_product(ffn::kNT, ffn::kStoreBf16, down, s));
+  const bool few = few_tokens(p, false);
+  const hipError_t e = few ? ffn::launch_rows(ffn::kSwiglu, up, s)
+                           : ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, s);
+  if (e != hipSuccess) return done(e);
+  return done(few ? ffn::launch_rows(ffn::kStoreBf16, down, s)
+                  : ffn::launch_product(ffn::kNT, ffn::kStoreBf16, down, s));
 }
 
 int moe_ffn_backward(const void* dout, const void* x, const float* gate_up, const void* w13,
@@ -185,7 +204,7 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   const int st = check_rows(rows, width);
   if (st != MOE_OK) return st;
   if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
-  *bytes = rows == 0 ? 0
+  *bytes = rows == 0 || few_rows(rows, cols, width, quantize) ? 0
                      : (quantize ? MxRegion(rows, width).bytes() : padded(rows, width)) +
                            padded(cols, width);
   return MOE_OK;
@@ -207,6 +226,12 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
     return MOE_ERR_ALIGNMENT;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   hipStream_t s = (hipStream_t)stream;
+  const ffn::Epilogue store = out_type == MOE_TYPE_FP32 ? ffn::kStoreF32 : ffn::kStoreBf16;
+  if (few_rows(rows, cols, width, !a_scales)) {
+    Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
+    d.out = out;
+    return done(ffn::launch_rows_mx(store, a_scales ? ffn::kAAsIs : ffn::kABf16, d, s));
+  }
   uint8_t* ws = (uint8_t*)workspace;
   const uint8_t* a_given = a_scales;
   hipError_t e = hipSuccess;
@@ -227,8 +252,7 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
   if (e != hipSuccess) return done(e);
   Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
   d.out = out;
-  return done(ffn::launch_product_mx(
-      out_type == MOE_TYPE_FP32 ? ffn::kStoreF32 : ffn::kStoreBf16, d, s));
+  return done(ffn::launch_product_mx(store, d, s));
 }
 
 int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_scales,
@@ -247,6 +271,15 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   const int64_t T = p->num_tokens;
   const int32_t H = p->hidden, I = p->inter;
   hipStream_t s = (hipStream_t)stream;
+  if (few_tokens(p, true)) {
+    Product up{x, w13, nullptr, w13_scales, H / 2, H / 2, T, I, H};
+    up.out = workspace;
+    const hipError_t e = ffn::launch_rows_mx(ffn::kSwigluF32, ffn::kABf16, up, s);
+    if (e != hipSuccess) return done(e);
+    Product down{workspace, w2, nullptr, w2_scales, I / 2, I / 2, T, H, I};
+    down.out = out;
+    return done(ffn::launch_rows_mx(ffn::kStoreBf16, ffn::kAF32, down, s));
+  }
   const MxRegion rx(T, H), rh(T, I);
   uint8_t* xc = (uint8_t*)workspace;
   uint8_t* xs = xc + rx.codes;

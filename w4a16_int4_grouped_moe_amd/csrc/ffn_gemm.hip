@@ -24,50 +24,15 @@
 
 #include <utility>
 
+#include "ffn_device.h"
 #include "ffn_internal.h"
-
-// the host pass sees the kernels' stubs alone
-#if !defined(__HIP_DEVICE_COMPILE__)
-#pragma clang diagnostic ignored "-Wunused-function"
-#pragma clang diagnostic ignored "-Wunneeded-internal-declaration"
-#endif
 
 namespace ffn {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-typedef __attribute__((address_space(3))) void* lds_ptr;
-typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
-
-constexpr int kBufferFlags = 0x00020000;  // raw buffer resource, dword 3
-constexpr uint32_t kOut = 0x80000000u;    // an offset past every buffer: reads 0
-constexpr int kRow = 128;                 // bytes of a KC row per stage
+constexpr int kRow = 128;  // bytes of a KC row per stage
 
 enum Kind { KC = 0, RC = 1 };
-
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  // vmcnt[3:0] | expcnt[6:4] | lgkmcnt[11:8] | vmcnt_hi[15:14]
-  static_assert(N >= 0 && N < 64, "vmcnt");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
-}
-__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
 
 // 16 lanes address 4 x 16 16-bit values, four neighbouring lanes a row of 16;
 // lane i receives column i, row j in element j.
@@ -198,19 +163,7 @@ struct Frags {
   }
 };
 
-__device__ __forceinline__ f32x4 mfma(const u32x4& n, const u32x4& m, const f32x4& c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, n),
-                                                 __builtin_bit_cast(bf16x8, m), c, 0, 0, 0);
-}
-template <int SN, int SM>
-__device__ __forceinline__ f32x4 mfma_mx(const u32x4& n, const u32x4& m, const f32x4& c,
-                                         uint32_t sn, uint32_t sm) {
-  const i32x8 a = {(int)n[0], (int)n[1], (int)n[2], (int)n[3]};
-  const i32x8 b = {(int)m[0], (int)m[1], (int)m[2], (int)m[3]};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, SN, (int)sn, SM,
-                                                          (int)sm);
-}
-
+#if defined(__HIP_DEVICE_COMPILE__)
 // The MFMAs of 16 FA rows x 16 FB columns over a stage. MXFP4: sm and sn hold
 // the scale bytes of two sub-tiles a word, two steps each (see put_scales).
 template <int FA, int FB, int X>
@@ -241,6 +194,7 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB
 #pragma unroll
     for (int j = 0; j < FB; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
+#endif
 
 // MXFP4 scales of a tile: thread i carries the eight scale bytes (one stage)
 // of tile row i, A's rows first, then B's two halves. Rows and stages past the
@@ -297,22 +251,13 @@ __device__ __forceinline__ uint32_t mx_quantize8(const float* v, uint32_t* scale
   top = o1 > top ? o1 : top;
   const uint32_t o2 = __shfl_xor(top, 32);
   top = o2 > top ? o2 : top;
-  // e8m0 byte: the exponent field less 2 (subnormal fp32 maxima: 0)
-  const int e = (int)(top >> 23);
-  const bool bad = e == 255;
-  const int s = e < 2 ? 0 : e - 2;
-  *scale = bad ? 255u : (uint32_t)s;
-  uint32_t c = 0;
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    float y[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = bad ? 0.f : ldexpf(v[4 * g + i], 127 - s);
-    uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, y[0], y[1], 1.0f, 0);
-    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, y[2], y[3], 1.0f, 1);
-    c |= (w & 0xffffu) << (16 * g);
-  }
-  return c;
+  *scale = mx_scale(top >> 23);
+  const float unit = mx_unit(*scale);
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], unit, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], unit, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], unit, 3);
+  return *scale == 255 ? 0 : c;
 }
 
 // Stores a wave's accumulators: 16 FA rows from m0; columns n0 .. of acc[0], and

@@ -15,6 +15,7 @@ enum Epilogue {
   kSwigluMx = 3,    // out e2m1 codes of h [M, N/2], aux its scale bytes (scale_stride(N) a row)
   kSwigluGrad = 4,  // the product is dh: aux fp32 [M, 2N] pre-activations (read),
                     // out bf16 [M, 2N] their gradients, out2 bf16 h [M, N]
+  kSwigluF32 = 5,   // out fp32 h [M, N]
 };
 
 // D[m, n] = sum_k A(m, k) B(n, k). An operand is "K contiguous" (element
@@ -45,6 +46,16 @@ struct Product {
 hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, hipStream_t stream);
 // MXFP4 operands, both K contiguous; K a multiple of 32
 hipError_t launch_product_mx(Epilogue epilogue, const Product& p, hipStream_t stream);
+
+// The same products for a few rows (ffn_small.hip), both operands K contiguous
+// and dense. A: as the product takes it, or rows to be quantised to MXFP4.
+// Here a row's scales are K/32 bytes, at any address. rows_fit: whether the
+// kernel takes the problem (at most 16 rows, B below 2 GiB, a quantised A that
+// fits LDS).
+enum AType { kAAsIs = 0, kABf16 = 1, kAF32 = 2 };
+bool rows_fit(const Product& p, bool mx, AType a, bool paired);
+hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream);
+hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream);
 
 // x [rows, width] (type: MOE_TYPE_*) -> e2m1 codes [rows, width/2], scales
 // [rows, width/32], or padded: rows of scale_stride(width)

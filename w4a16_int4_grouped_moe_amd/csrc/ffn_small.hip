@@ -1,0 +1,275 @@
+// ffn_small.hip -- the K-contiguous products for at most 16 rows (gfx950):
+// decoding, where the time is the weights' way from memory.
+//
+// A work-group owns 16 weight rows (SwiGLU: 8 gate rows and their 8 up rows)
+// and all rows of A: one 16 x 16 MFMA tile. Its eight waves take the stages of
+// K (128 bytes of a row) in turn, so that together they read whole kilobytes of
+// each row; a wave keeps a ring of stages in flight in registers, loads
+// straight into the MFMA's layout (lane (r = lane % 16, q = lane / 16): piece
+// 4 step + q of row r) and never waits for another wave. At the end the waves'
+// sums are added in LDS, in wave order.
+//
+// An A that is to be quantised (bf16, or the fp32 h of the block) is quantised
+// by the work-group into LDS: its loads go out first, then the ring's, so the
+// conversion runs under the first weights' latency. Every work-group repeats
+// it (at most 16 rows), which costs less than a launch of its own.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ffn_device.h"
+#include "ffn_internal.h"
+
+namespace ffn {
+namespace {
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kMaxRows = 16;
+constexpr int kMxLds = 56 * 1024;  // quantised A in LDS, codes and scales (64 KB with the sums)
+
+// LDS rows of quantised A: 16 rows at one offset lie in distinct banks
+__host__ __device__ inline int code_stride(int64_t K) { return (int)((K / 2 + 255) / 256 * 256 + 16); }
+__host__ __device__ inline int byte_stride(int64_t K) { return (int)((K / 32 + 7) / 8 * 8 + 4); }
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// 32 values, four (bf16) or eight (fp32) 16-byte pieces -> codes, scale byte
+template <bool F32>
+__device__ __forceinline__ u32x4 quantize_block(const u32x4* v, uint32_t* scale) {
+  u32x4 c;
+  if constexpr (F32) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b = v[i][j] & 0x7fffffffu;
+        top = b > top ? b : top;
+      }
+    *scale = mx_scale(top >> 23);
+    const float unit = mx_unit(*scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 a = __builtin_bit_cast(f32x4, v[2 * i]), b = __builtin_bit_cast(f32x4, v[2 * i + 1]);
+      uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a[0], a[1], unit, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], unit, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[0], b[1], unit, 2);
+      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[2], b[3], unit, 3);
+    }
+  } else {
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        top = __builtin_elementwise_max(top,
+                                        __builtin_bit_cast(u16x2, (uint32_t)(v[i][j] & 0x7fff7fffu)));
+    *scale = mx_scale((uint32_t)(top[0] > top[1] ? top[0] : top[1]) >> 7);
+    const float unit = mx_unit(*scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w = 0;
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][0]), unit, 0);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][1]), unit, 1);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][2]), unit, 2);
+      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][3]), unit, 3);
+    }
+  }
+  if (*scale == 255) c = u32x4{0, 0, 0, 0};
+  return c;
+}
+#endif
+
+// A: as the product's operands (kAsIs), or bf16 / fp32 rows to quantise
+enum AKind { kAsIs = 0, kFromBf16 = 1, kFromF32 = 2 };
+
+template <AKind AK, bool MX, Epilogue EPI>
+__global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluF32;
+  constexpr int kD = AK == kFromF32 ? 3 : 5;  // stages in flight per wave
+  __shared__ __attribute__((aligned(16))) float sums[kWaves][256];
+  extern __shared__ __attribute__((aligned(16))) uint8_t qa[];  // quantised A: codes, then bytes
+
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int M = (int)p.M, N = p.N, kb = (int)(MX ? p.K / 2 : 2 * p.K);  // bytes of a row
+  const int n0 = blockIdx.x * (kPaired ? 8 : 16);
+  const int blocks = (int)(p.K / 32), stages = (kb + 127) / 128;
+
+  const int row = kPaired ? (r < 8 ? n0 + r : N + n0 + r - 8) : n0 + r;
+  const int rows = kPaired ? 2 * N : N;
+  const uint32_t woff = row < rows ? (uint32_t)row * kb + 16 * q : kOut;
+  const uint32_t wsoff = row < rows ? (uint32_t)row * blocks + q : kOut;
+  const uint32_t xoff = r < M ? (uint32_t)r * kb + 16 * q : kOut;
+  const uint32_t xsoff = r < M ? (uint32_t)r * blocks + q : kOut;
+  const __amdgpu_buffer_rsrc_t wres =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.b, 0, rows * kb, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t wsres =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.b_scales, 0, MX ? rows * blocks : 0, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t xres =
+      __builtin_amdgcn_make_buffer_rsrc((void*)p.a, 0, M * kb, kBufferFlags);
+  const __amdgpu_buffer_rsrc_t xsres = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)p.a_scales, 0, MX && AK == kAsIs ? M * blocks : 0, kBufferFlags);
+
+  u32x4 w[kD][2], x[kD][2];
+  uint32_t ws[kD][2], xs[kD][2];
+  auto load = [&](int d, int s) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int at = s * 128 + st * 64;
+      const bool in = at + 16 * q < kb;
+      if constexpr (AK == kAsIs)
+        x[d][st] = __builtin_amdgcn_raw_buffer_load_b128(xres, in ? xoff + at : kOut, 0, 0);
+      w[d][st] = __builtin_amdgcn_raw_buffer_load_b128(wres, in ? woff + at : kOut, 0, 0);
+      if constexpr (MX) {
+        const int b = 8 * s + 4 * st;
+        if constexpr (AK == kAsIs)
+          xs[d][st] = __builtin_amdgcn_raw_buffer_load_b8(xsres, in ? xsoff + b : kOut, 0, 0);
+        ws[d][st] = __builtin_amdgcn_raw_buffer_load_b8(wsres, in ? wsoff + b : kOut, 0, 0);
+      }
+    }
+  };
+  auto fill = [&] {
+#pragma unroll
+    for (int d = 0; d < kD; ++d) load(d, wave + d * kWaves);
+  };
+
+  const int cstride = code_stride(p.K), bstride = byte_stride(p.K);
+  uint8_t* qbytes = qa + M * cstride;
+  const int rq = r < M ? r : M - 1;  // rows past the last: any, their sums are not stored
+  if constexpr (AK == kAsIs) {
+    fill();
+  } else {
+    // blocks of all rows over the threads, up to `kAtOnce` each at a time; the
+    // last round's loads go out ahead of the ring's. Blocks past K (to a whole
+    // stage) get a finite scale.
+    constexpr int kPieces = AK == kFromF32 ? 8 : 4;
+    constexpr int kAtOnce = AK == kFromF32 ? 1 : 2;
+    const int per = (blocks + 7) / 8 * 8, total = M * per;
+    const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)p.a, 0, M * blocks * (16 * kPieces), kBufferFlags);
+    for (int first = threadIdx.x;; first += kAtOnce * kThreads) {
+      u32x4 v[kAtOnce][kPieces];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int u = first + j * kThreads, t = u / per, b = u - t * per;
+        const uint32_t off = u < total && b < blocks
+                                 ? (uint32_t)(t * blocks + b) * (16 * kPieces) : kOut;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          v[j][i] = __builtin_amdgcn_raw_buffer_load_b128(ares, off == kOut ? kOut : off + 16 * i, 0, 0);
+      }
+      const bool last = uniform(first - threadIdx.x) + kAtOnce * kThreads >= total;
+      if (last) fill();
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int u = first + j * kThreads, t = u / per, b = u - t * per;
+        uint32_t scale;
+        const u32x4 c = quantize_block<AK == kFromF32>(v[j], &scale);
+        if (u < total) {
+          *(u32x4*)(qa + t * cstride + 16 * b) = c;
+          qbytes[t * bstride + b] = (uint8_t)scale;
+        }
+      }
+      if (last) break;
+    }
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+  }
+
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = wave; s < stages; s += kD * kWaves) {
+#pragma unroll
+    for (int d = 0; d < kD; ++d) {
+      const int at = s + d * kWaves;
+      if (at >= stages) break;  // uniform: a wave's stages are its own
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        if constexpr (MX) {
+          u32x4 xv;
+          uint32_t xb;
+          if constexpr (AK == kAsIs) {
+            xv = x[d][st], xb = xs[d][st];
+          } else {
+            xv = *(const u32x4*)(qa + rq * cstride + at * 128 + st * 64 + 16 * q);
+            xb = qbytes[rq * bstride + 8 * at + 4 * st + q];
+          }
+          acc = mfma_mx<0, 0>(w[d][st], xv, acc, ws[d][st], xb);
+        } else {
+          acc = mfma(w[d][st], x[d][st], acc);
+        }
+      }
+      load(d, at + kD * kWaves);
+    }
+  }
+
+  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row r
+  *(f32x4*)&sums[wave][r * 16 + 4 * q] = acc;
+  __syncthreads();
+  const int i = threadIdx.x;
+  if constexpr (kPaired) {
+    const int m = i >> 3, j = i & 7;
+    if (i >= 128 || m >= M) return;
+    float g = 0.f, u = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) g += sums[k][m * 16 + j], u += sums[k][m * 16 + 8 + j];
+    const float h = g * sigmoid(g) * u;
+    const int64_t at = (int64_t)m * N + n0 + j;
+    if constexpr (EPI == kSwigluF32) {
+      ((float*)p.out)[at] = h;
+    } else {
+      ((uint16_t*)p.out)[at] = (uint16_t)pack2(h, 0.f);
+      if (p.aux) {
+        float* gu = (float*)p.aux + (int64_t)m * 2 * N + n0 + j;
+        gu[0] = g;
+        gu[N] = u;
+      }
+    }
+  } else {
+    const int m = i >> 4, n = n0 + (i & 15);
+    if (i >= 256 || m >= M || n >= N) return;
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) v += sums[k][i];
+    if constexpr (EPI == kStoreF32)
+      ((float*)p.out)[(int64_t)m * N + n] = v;
+    else
+      ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
+  }
+#endif
+}
+
+template <AKind AK, bool MX, Epilogue EPI>
+hipError_t launch(const Product& p, hipStream_t stream) {
+  const unsigned groups = EPI == kSwiglu || EPI == kSwigluF32 ? (p.N + 7) / 8 : (p.N + 15) / 16;
+  const size_t lds = AK == kAsIs ? 0 : p.M * (code_stride(p.K) + byte_stride(p.K));
+  hipLaunchKernelGGL((rows_kernel<AK, MX, EPI>), dim3(groups), dim3(kThreads), lds, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+bool rows_fit(const Product& p, bool mx, AType a, bool paired) {
+  const int64_t kb = mx ? p.K / 2 : 2 * p.K;
+  return p.M >= 1 && p.M <= kMaxRows && (paired ? 2 : 1) * (int64_t)p.N * kb < 0x7fffffff &&
+         (a == kAAsIs || p.M * ((int64_t)code_stride(p.K) + byte_stride(p.K)) <= kMxLds);
+}
+
+hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream) {
+  if (epilogue == kSwiglu) return launch<kAsIs, false, kSwiglu>(p, stream);
+  if (epilogue == kStoreBf16) return launch<kAsIs, false, kStoreBf16>(p, stream);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream) {
+  if (epilogue == kSwigluF32 && a == kABf16) return launch<kFromBf16, true, kSwigluF32>(p, stream);
+  if (epilogue == kStoreBf16 && a == kAF32) return launch<kFromF32, true, kStoreBf16>(p, stream);
+  if (epilogue == kStoreBf16 && a == kABf16) return launch<kFromBf16, true, kStoreBf16>(p, stream);
+  if (epilogue == kStoreF32 && a == kABf16) return launch<kFromBf16, true, kStoreF32>(p, stream);
+  if (epilogue == kStoreBf16) return launch<kAsIs, true, kStoreBf16>(p, stream);
+  if (epilogue == kStoreF32) return launch<kAsIs, true, kStoreF32>(p, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace ffn

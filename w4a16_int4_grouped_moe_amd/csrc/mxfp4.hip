@@ -4,23 +4,18 @@
 // Both are one pass over memory. A lane owns 8 consecutive values (16 bytes of
 // bf16 or fp16, 32 of fp32; 4 bytes of codes), four neighbouring lanes a block.
 // The largest magnitude is compared as bits (an unsigned maximum orders
-// magnitudes, infinities and NaN on top), so e is its exponent field less 2;
-// v * 2^-e is an exact ldexp, and v_cvt_scalef32_pk_fp4_f32 rounds to nearest
-// even and saturates.
+// magnitudes, infinities and NaN on top), so e is its exponent field less 2,
+// and v_cvt_scalef32_pk_fp4_f32 divides by 2^e, rounds to nearest even and
+// saturates.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "../../include/moe_ffn.h"
+#include "ffn_device.h"
 #include "ffn_internal.h"
 
 namespace ffn {
 namespace {
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef _Float16 h16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 
@@ -67,20 +62,16 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
   top = o1 > top ? o1 : top;
   const uint32_t o2 = __shfl_xor(top, 2);
   top = o2 > top ? o2 : top;
-  const int e = (int)(top >> 23);
-  const bool bad = e == 255;
-  const int s = e < 2 ? 0 : e - 2;
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = bad ? 0.f : ldexpf(v[i], 127 - s);
-  uint32_t c = 0;
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[0], y[1], 1.0f, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], 1.0f, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], 1.0f, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], 1.0f, 3);
+  const uint32_t scale = mx_scale(top >> 23);
+  const float unit = mx_unit(scale);
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], unit, 1);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], unit, 2);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], unit, 3);
+  if (scale == 255) c = 0;
   codes[u] = c;
   if ((u & 3) == 0) {
-    const uint8_t byte = bad ? 255 : (uint8_t)s;
+    const uint8_t byte = (uint8_t)scale;
     const int64_t b = u >> 2;
     if (pad == 0) {
       scales[b] = byte;
