@@ -22,8 +22,7 @@
  * bits: codes uint8 [rows, width/2], scales uint8 [rows, width/32].
  *
  * Conventions are moe_w4a16.h's: dense row-major device tensors, 16-byte
- * aligned (scales: 8-byte aligned for a product whose width is a multiple of
- * 256, else any); the caller owns every buffer and the
+ * aligned (scales need no alignment); the caller owns every buffer and the
  * workspace; nothing is allocated or kept, the host never waits, launches go
  * to `stream` on the current device and may be captured into a HIP graph;
  * calls that share a workspace (two captured graphs, too) must not overlap;

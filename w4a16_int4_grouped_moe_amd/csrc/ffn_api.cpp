@@ -1,5 +1,7 @@
 // ffn_api.cpp -- host side of include/moe_ffn.h: argument checks, workspace
 // layout and launch sequences. Every check runs before the first launch.
+#include <algorithm>
+
 #include "../../include/moe_ffn.h"
 #include "ffn_internal.h"
 #include "internal.h"
@@ -48,23 +50,13 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 
 int done(hipError_t e) { return e == hipSuccess ? MOE_OK : moe::report_hip(e); }
 
-// MXFP4 [rows, width] in a workspace: codes, then padded scales
+// MXFP4 [rows, width] in a workspace: codes, then scales by stage
 struct MxRegion {
   size_t codes, scales;
   MxRegion(int64_t rows, int32_t width)
-      : codes(region(rows * (width / 2))), scales(region(rows * ffn::scale_stride(width))) {}
+      : codes(region(rows * (width / 2))), scales(region(ffn::scale_bytes(rows, width))) {}
   size_t bytes() const { return codes + scales; }
 };
-
-// Widths that are not whole stages: the given scales are copied into padded rows
-bool needs_padding(int32_t width) { return width % 256 != 0; }
-size_t padded(int64_t rows, int32_t width) {
-  return needs_padding(width) ? region(rows * ffn::scale_stride(width)) : 0;
-}
-// Given scales of whole stages are read in place, eight bytes at a time
-bool scales_aligned(const uint8_t* s, int32_t width) {
-  return needs_padding(width) || ((uintptr_t)s & 7u) == 0;
-}
 
 // The block's two products as the few-row kernels take them
 bool few_tokens(const moe_ffn_problem* p, bool mx) {
@@ -81,14 +73,36 @@ bool few_rows(int64_t rows, int32_t cols, int32_t width, bool quantize) {
   return ffn::rows_fit(d, true, quantize ? ffn::kABf16 : ffn::kAAsIs, false);
 }
 
+// The shares' sums of a pass's products, which follow each other: one region
+size_t split_of(const moe_ffn_problem* p, int pass) {
+  const int64_t T = p->num_tokens, H = p->hidden, I = p->inter;
+  const bool mx = pass == MOE_FFN_FORWARD_MXFP4;
+  size_t most = 0;
+  auto add = [&](ffn::Epilogue epi, int64_t M, int64_t N, int64_t K) {
+    most = std::max(most, ffn::product_workspace(epi, M, (int32_t)N, K, mx));
+  };
+  if (pass == MOE_FFN_BACKWARD) {
+    add(ffn::kSwigluGrad, T, I, H);
+    add(ffn::kStoreBf16, T, H, 2 * I);
+    add(ffn::kStoreBf16, 2 * I, H, T);
+    add(ffn::kStoreBf16, H, I, T);
+  } else {
+    add(mx ? ffn::kSwigluMx : ffn::kSwiglu, T, I, H);
+    add(ffn::kStoreBf16, T, H, I);
+  }
+  return region(most);
+}
+
 size_t workspace_of(const moe_ffn_problem* p, int pass) {
-  const int64_t T = p->num_tokens, I = p->inter;
+  const int64_t T = p->num_tokens, H = p->hidden, I = p->inter;
   if (T == 0) return 0;
-  if (pass == MOE_FFN_FORWARD_MXFP4 && few_tokens(p, true)) return region(4 * T * I);
-  if (pass == MOE_FFN_FORWARD) return region(2 * T * I);
-  if (pass == MOE_FFN_BACKWARD) return region(4 * T * I) + region(2 * T * I);
+  if (pass == MOE_FFN_BACKWARD)
+    return region(4 * T * I) + region(2 * T * I) + split_of(p, pass);
+  if (pass == MOE_FFN_FORWARD)
+    return region(2 * T * I) + (few_tokens(p, false) ? 0 : split_of(p, pass));
+  if (few_tokens(p, true)) return region(4 * T * I);
   return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes() +
-         padded(2 * I, p->hidden) + padded(p->hidden, p->inter);
+         region(ffn::scale_bytes(2 * I, H)) + region(ffn::scale_bytes(H, I)) + split_of(p, pass);
 }
 
 }  // namespace
@@ -122,11 +136,12 @@ int moe_ffn_forward(const void* x, const void* w13, const void* w2, void* out, f
   Product down{workspace, w2, nullptr, nullptr, 2 * I, 2 * I, T, p->hidden, I};
   down.out = out;
   const bool few = few_tokens(p, false);
+  char* split = (char*)workspace + region(2 * T * I);
   const hipError_t e = few ? ffn::launch_rows(ffn::kSwiglu, up, s)
-                           : ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, s);
+                           : ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, split, s);
   if (e != hipSuccess) return done(e);
   return done(few ? ffn::launch_rows(ffn::kStoreBf16, down, s)
-                  : ffn::launch_product(ffn::kNT, ffn::kStoreBf16, down, s));
+                  : ffn::launch_product(ffn::kNT, ffn::kStoreBf16, down, split, s));
 }
 
 int moe_ffn_backward(const void* dout, const void* x, const float* gate_up, const void* w13,
@@ -146,27 +161,28 @@ int moe_ffn_backward(const void* dout, const void* x, const float* gate_up, cons
   hipStream_t s = (hipStream_t)stream;
   char* dgu = (char*)workspace;                      // bf16 [T, 2I]
   char* h = T > 0 ? dgu + region(4 * T * I) : dgu;   // bf16 [T, I]
+  char* split = T > 0 ? h + region(2 * T * I) : dgu;
   hipError_t e = hipSuccess;
   if (T > 0) {
     Product dh{dout, w2, nullptr, nullptr, 2 * H, 2 * I, T, p->inter, H};
     dh.out = dgu;
     dh.out2 = h;
     dh.aux = const_cast<float*>(gate_up);
-    e = ffn::launch_product(ffn::kNN, ffn::kSwigluGrad, dh, s);
+    e = ffn::launch_product(ffn::kNN, ffn::kSwigluGrad, dh, split, s);
     if (e == hipSuccess && dx) {
       Product d{dgu, w13, nullptr, nullptr, 4 * I, 2 * H, T, p->hidden, 2 * I};
       d.out = dx;
-      e = ffn::launch_product(ffn::kNN, ffn::kStoreBf16, d, s);
+      e = ffn::launch_product(ffn::kNN, ffn::kStoreBf16, d, split, s);
     }
   }
   if (e == hipSuccess && dw13) {
     Product d13{dgu, x, nullptr, nullptr, 4 * I, 2 * H, 2 * I, p->hidden, T};
     d13.out = dw13;
-    e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d13, s);
+    e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d13, split, s);
     if (e == hipSuccess) {
       Product d2{dout, h, nullptr, nullptr, 2 * H, 2 * I, H, p->inter, T};
       d2.out = dw2;
-      e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d2, s);
+      e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d2, split, s);
     }
   }
   return done(e);
@@ -182,7 +198,7 @@ int moe_mxfp4_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
   if (!scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 2)) != MOE_OK) return st;
   return done(
-      ffn::launch_mx_quantize(x, type, rows, width, codes, scales, false, (hipStream_t)stream));
+      ffn::launch_mx_quantize(x, type, rows, width, codes, scales, (hipStream_t)stream));
 }
 
 int moe_mxfp4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t width,
@@ -204,9 +220,11 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   const int st = check_rows(rows, width);
   if (st != MOE_OK) return st;
   if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
-  *bytes = rows == 0 || few_rows(rows, cols, width, quantize) ? 0
-                     : (quantize ? MxRegion(rows, width).bytes() : padded(rows, width)) +
-                           padded(cols, width);
+  *bytes = 0;
+  if (rows == 0 || few_rows(rows, cols, width, quantize)) return MOE_OK;
+  *bytes = (quantize ? MxRegion(rows, width).bytes() : region(ffn::scale_bytes(rows, width))) +
+           region(ffn::scale_bytes(cols, width)) +
+           region(ffn::product_workspace(ffn::kStoreF32, rows, cols, width, true));
   return MOE_OK;
 }
 
@@ -222,8 +240,6 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
   const void* ptrs[] = {a, b, out};
   if (!b_scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 3)) != MOE_OK) return st;
-  if ((a_scales && !scales_aligned(a_scales, width)) || !scales_aligned(b_scales, width))
-    return MOE_ERR_ALIGNMENT;
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   const ffn::Epilogue store = out_type == MOE_TYPE_FP32 ? ffn::kStoreF32 : ffn::kStoreBf16;
@@ -232,27 +248,23 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
     d.out = out;
     return done(ffn::launch_rows_mx(store, a_scales ? ffn::kAAsIs : ffn::kABf16, d, s));
   }
-  uint8_t* ws = (uint8_t*)workspace;
-  const uint8_t* a_given = a_scales;
-  hipError_t e = hipSuccess;
-  if (!a_scales) {
-    const MxRegion r(rows, width);
-    e = ffn::launch_mx_quantize(a, MOE_TYPE_BF16, rows, width, ws, ws + r.codes, true, s);
-    a = ws;
-    a_scales = ws + r.codes;
-    ws += r.bytes();
-  }
-  if (e == hipSuccess && needs_padding(width)) {
-    uint8_t* pa = ws;
-    uint8_t* pb = a_given ? pa + padded(rows, width) : ws;
-    e = ffn::launch_mx_pad_scales(a_given, a_given ? rows : 0, pa, b_scales, cols, pb, width, s);
-    if (a_given) a_scales = pa;
-    b_scales = pb;
+  uint8_t* sb = (uint8_t*)workspace;
+  uint8_t* sa = sb + region(ffn::scale_bytes(cols, width));
+  uint8_t* codes = sa + region(ffn::scale_bytes(rows, width));
+  uint8_t* split = a_scales ? codes : codes + MxRegion(rows, width).codes;
+  const ffn::ScaleCopy copy_b{b_scales, sb, cols, width};
+  hipError_t e;
+  if (a_scales) {
+    e = ffn::launch_mx_prepare(nullptr, 0, 0, nullptr, nullptr, copy_b, {a_scales, sa, rows, width},
+                               s);
+  } else {
+    e = ffn::launch_mx_prepare(a, rows, width, codes, sa, copy_b, {}, s);
+    a = codes;
   }
   if (e != hipSuccess) return done(e);
-  Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
+  Product d{a, b, sa, sb, width / 2, width / 2, rows, cols, width};
   d.out = out;
-  return done(ffn::launch_product_mx(store, d, s));
+  return done(ffn::launch_product_mx(store, d, split, s));
 }
 
 int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_scales,
@@ -264,8 +276,6 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   const void* ptrs[] = {x, w13, w2, out};
   if (!w13_scales || !w2_scales) return MOE_ERR_NULL;
   if ((st = check_pointers(ptrs, 4)) != MOE_OK) return st;
-  if (!scales_aligned(w13_scales, p->hidden) || !scales_aligned(w2_scales, p->inter))
-    return MOE_ERR_ALIGNMENT;
   st = check_workspace(workspace, workspace_bytes, workspace_of(p, MOE_FFN_FORWARD_MXFP4));
   if (st != MOE_OK) return st;
   const int64_t T = p->num_tokens;
@@ -286,25 +296,19 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   uint8_t* hc = xc + rx.bytes();
   uint8_t* hs = hc + rh.codes;
   uint8_t* s13 = hc + rh.bytes();
-  uint8_t* s2 = s13 + padded(2 * (int64_t)I, H);
-  hipError_t e = ffn::launch_mx_quantize(x, MOE_TYPE_BF16, T, H, xc, xs, true, s);
-  if (e == hipSuccess && needs_padding(H)) {
-    e = ffn::launch_mx_pad_scales(w13_scales, 2 * (int64_t)I, s13, nullptr, 0, nullptr, H, s);
-    w13_scales = s13;
-  }
-  if (e == hipSuccess && needs_padding(I)) {
-    e = ffn::launch_mx_pad_scales(w2_scales, H, s2, nullptr, 0, nullptr, I, s);
-    w2_scales = s2;
-  }
+  uint8_t* s2 = s13 + region(ffn::scale_bytes(2 * (int64_t)I, H));
+  uint8_t* split = s2 + region(ffn::scale_bytes(H, I));
+  hipError_t e = ffn::launch_mx_prepare(x, T, H, xc, xs, {w13_scales, s13, 2 * (int64_t)I, H},
+                                        {w2_scales, s2, H, I}, s);
   if (e != hipSuccess) return done(e);
-  Product up{xc, w13, xs, w13_scales, H / 2, H / 2, T, I, H};
+  Product up{xc, w13, xs, s13, H / 2, H / 2, T, I, H};
   up.out = hc;
   up.aux = hs;
-  e = ffn::launch_product_mx(ffn::kSwigluMx, up, s);
+  e = ffn::launch_product_mx(ffn::kSwigluMx, up, split, s);
   if (e != hipSuccess) return done(e);
-  Product down{hc, w2, hs, w2_scales, I / 2, I / 2, T, H, I};
+  Product down{hc, w2, hs, s2, I / 2, I / 2, T, H, I};
   down.out = out;
-  return done(ffn::launch_product_mx(ffn::kStoreBf16, down, s));
+  return done(ffn::launch_product_mx(ffn::kStoreBf16, down, split, s));
 }
 
 }  // extern "C"

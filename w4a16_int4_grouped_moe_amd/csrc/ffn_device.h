@@ -42,7 +42,11 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + expf(-g)); }
+// 1 / (1 + e^-g) by the hardware's 2^x and reciprocal: within 2^-20 of itself
+// for |g| < 16, further out by |g| 2^-24, far below the roundings that follow
+__device__ __forceinline__ float sigmoid(float g) {
+  return __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+}
 
 // The e8m0 byte of a block from its largest exponent field (fp32's or bf16's):
 // two less, at least 0; 255 for infinities and NaN.

@@ -83,11 +83,12 @@ struct Half {
   int64_t kleft;    // KC: bytes of a row (fits 32 bits); RC: k-rows
   int32_t records;  // KC: bytes that may be read; RC: bytes of a k-row
 
-  // rows [row0, row0 + HR) of an operand of `rows` rows; K: bytes per row (KC) or k-rows (RC)
+  // rows [row0, row0 + HR) of an operand of `rows` rows; K: bytes per row (KC) or k-rows (RC),
+  // of which the first `end` are read
   __device__ __forceinline__ void init(const void* ptr, int64_t row0, int64_t rows, int64_t ld_,
-                                       int64_t K) {
+                                       int64_t K, int64_t end) {
     ld = ld_;
-    kleft = K;
+    kleft = end;
     const int64_t left = rows - row0;
     const int valid = left <= 0 ? 0 : left < HR ? (int)left : HR;
     base = (const uint8_t*)ptr + (valid ? row0 * (KIND == KC ? ld : 2) : 0);
@@ -165,7 +166,7 @@ struct Frags {
 
 #if defined(__HIP_DEVICE_COMPILE__)
 // The MFMAs of 16 FA rows x 16 FB columns over a stage. MXFP4: sm and sn hold
-// the scale bytes of two sub-tiles a word, two steps each (see put_scales).
+// the scale bytes of two sub-tiles a word, two steps each (see read_scales).
 template <int FA, int FB, int X>
 __device__ __forceinline__ void mma_mx(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB],
                                        const u32x4 (&m)[2][FA], uint32_t sn, u32x2 sm) {
@@ -196,46 +197,47 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB
 }
 #endif
 
-// MXFP4 scales of a tile: thread i carries the eight scale bytes (one stage)
-// of tile row i, A's rows first, then B's two halves. Rows and stages past the
-// end read the last one: their codes are 0 and their sums are not stored.
-template <int ROWS_A, int ROWS_B, int GROUP_A, int GROUP_B, int THREADS>
-struct Scales {
-  static constexpr int kBytes = (ROWS_A + ROWS_B) * 8;
-  const uint8_t* row;
-  int last;  // the last stage's offset
-  u32x2 v;
-  static_assert(ROWS_A + ROWS_B == THREADS, "a thread a row");
-
-  __device__ __forceinline__ void init(const Product& p, int64_t m0, int64_t n0, int64_t n1,
-                                       int64_t up) {
-    last = (int)scale_stride(p.K) - 8;
-    const int i = threadIdx.x;
-    if (i < ROWS_A) {
-      row = p.a_scales + (m0 + i < p.M ? m0 + i : p.M - 1) * (int64_t)(last + 8);
-    } else {
-      const int half = (i - ROWS_A) / (ROWS_B / 2), r = (i - ROWS_A) % (ROWS_B / 2);
-      const int64_t n = (half ? n1 : n0) + r;
-      row = p.b_scales + ((n < p.N ? n : p.N - 1) + (half ? up : 0)) * (int64_t)(last + 8);
-    }
+// The MXFP4 scales of a half tile's rows, one stage: 8 bytes a row, copied by
+// one wave (HR / 2 lanes of 16 bytes).
+struct HalfScales {
+  const uint8_t* base;
+  int64_t pitch;  // bytes of a stage
+  int32_t records;
+  int last;
+  // rows from row0 of a matrix whose `rows` rows from `first` are the half's operand
+  __device__ __forceinline__ void init(const uint8_t* scales, int64_t first, int64_t row0,
+                                       int64_t rows, int64_t all, int64_t K) {
+    pitch = 8 * scale_rows(all);
+    last = (int)scale_stages(K) - 1;
+    const int64_t left = rows - row0;
+    records = left <= 0 ? 0 : (int32_t)((left < 128 ? scale_rows(left) : 128) * 8);
+    base = scales + (left > 0 ? first + row0 : 0) * 8;
   }
-  __device__ __forceinline__ void load(int stage) {
-    v = *(const u32x2*)(row + (stage * 8 < last ? stage * 8 : last));
-  }
-  // into LDS in the order the fragments read: a wave's GROUP rows of a half lie
-  // together, and lane (r, q)'s bytes (blocks q and 4 + q: one of each step) of
-  // its sub-tiles are neighbours
-  __device__ __forceinline__ void put(uint8_t* lds) const {
-    const int i = threadIdx.x;
-    const bool b = i >= ROWS_A;
-    const int first = b ? ROWS_A + (i - ROWS_A) / GROUP_B * GROUP_B : i / GROUP_A * GROUP_A;
-    const int n = (b ? GROUP_B : GROUP_A) / 16, sub = (i - first) / 16;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *(uint16_t*)(lds + first * 8 + (((i & 15) * 4 + q) * n + sub) * 2) =
-          (uint16_t)(((v[0] >> (8 * q)) & 0xff) | (((v[1] >> (8 * q)) & 0xff) << 8));
+  template <int HR>
+  __device__ __forceinline__ void copy(uint8_t* slot, int stage, int lane) const {
+    const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + (stage < last ? stage : last) * pitch), 0, records, kBufferFlags);
+    if (lane < HR / 2)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_ptr)slot, 16, 16 * lane, 0, 0, 0);
   }
 };
+
+// A wave's scale operands: lane (r, q) takes bytes q and 4 + q (its blocks of
+// the two steps) of row r of each sub-tile; two sub-tiles a word.
+template <int F>
+__device__ __forceinline__ void read_scales(const uint8_t* slot, int first, int lane,
+                                            uint32_t* word) {
+  const int q = lane >> 4;
+  const uint32_t pick = (uint32_t)(q | (4 + q) << 8);
+  const uint8_t* at = slot + (first + (lane & 15)) * 8;
+#pragma unroll
+  for (int i = 0; i < F; i += 2) {
+    const u32x2 a = *(const u32x2*)(at + i * 16 * 8), b = *(const u32x2*)(at + (i + 1) * 16 * 8);
+    const uint32_t lo = __builtin_amdgcn_perm(a[1], a[0], pick);
+    const uint32_t hi = __builtin_amdgcn_perm(b[1], b[0], pick);
+    word[i / 2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+  }
+}
 
 // Quantises one block of 32 values of which this lane holds 2 x 4 and the
 // lanes 16, 32 and 48 away the rest; returns the two groups' codes (16 bits
@@ -258,6 +260,83 @@ __device__ __forceinline__ uint32_t mx_quantize8(const float* v, uint32_t* scale
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], unit, 2);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], unit, 3);
   return *scale == 255 ? 0 : c;
+}
+
+// The scale byte of h's block from column n of row m; the last block fills its stage.
+__device__ __forceinline__ void put_scale(const Product& p, int64_t m, int64_t n, uint32_t scale) {
+  uint8_t* dst = (uint8_t*)p.aux + (n / 256 * scale_rows(p.M) + m) * 8;
+  const int at = (int)(n / 32) & 7;
+  dst[at] = (uint8_t)scale;
+  if (n + 32 == p.N)
+    for (int i = at + 1; i < 8; ++i) dst[i] = 127;
+}
+
+// Four columns from n of row m: `v`, or a gate and an up group.
+template <Epilogue EPI>
+__device__ __forceinline__ void emit(const Product& p, int64_t m, int64_t n, const f32x4& v,
+                                     const f32x4& up) {
+  const int64_t N = p.N;
+  if constexpr (EPI == kStoreF32 || EPI == kPartial) {
+    *(f32x4*)((float*)p.out + m * N + n) = v;
+  } else if constexpr (EPI == kPartialPaired) {
+    float* gu = (float*)p.out + m * 2 * N + n;
+    *(f32x4*)gu = v;
+    *(f32x4*)(gu + N) = up;
+  } else if constexpr (EPI == kStoreBf16) {
+    *(u32x2*)((uint16_t*)p.out + m * N + n) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+  } else if constexpr (EPI == kSwiglu) {
+    float h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = v[r] * sigmoid(v[r]) * up[r];
+    *(u32x2*)((uint16_t*)p.out + m * N + n) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+    if (p.aux) {
+      float* gu = (float*)p.aux + m * 2 * N + n;
+      *(f32x4*)gu = v;
+      *(f32x4*)(gu + N) = up;
+    }
+  } else {
+    static_assert(EPI == kSwigluGrad, "epilogue");
+    const float* gu = (const float*)p.aux + m * 2 * N + n;
+    const f32x4 g = *(const f32x4*)gu, u = *(const f32x4*)(gu + N);
+    float dg[4], du[4], h[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float sg = sigmoid(g[r]);
+      du[r] = v[r] * g[r] * sg;
+      dg[r] = v[r] * u[r] * sg * (1.0f + g[r] * (1.0f - sg));
+      h[r] = g[r] * sg * u[r];
+    }
+    uint16_t* d = (uint16_t*)p.out + m * 2 * N + n;
+    *(u32x2*)d = u32x2{pack2(dg[0], dg[1]), pack2(dg[2], dg[3])};
+    *(u32x2*)(d + N) = u32x2{pack2(du[0], du[1]), pack2(du[2], du[3])};
+    *(u32x2*)((uint16_t*)p.out2 + m * N + n) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+  }
+}
+
+// Four h columns from n of row m, quantised with the seven lanes that hold the
+// rest of the block (eight neighbours); lanes that store nothing take part.
+__device__ __forceinline__ void emit_mx(const Product& p, int64_t m, int64_t n, const f32x4& g,
+                                        const f32x4& u, bool in) {
+  float h[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    h[r] = g[r] * sigmoid(g[r]) * u[r];
+    const uint32_t b = __builtin_bit_cast(uint32_t, h[r]) & 0x7fffffffu;
+    top = b > top ? b : top;
+  }
+#pragma unroll
+  for (int x = 1; x < 8; x *= 2) {
+    const uint32_t o = __shfl_xor(top, x);
+    top = o > top ? o : top;
+  }
+  const uint32_t scale = mx_scale(top >> 23);
+  const float unit = mx_unit(scale);
+  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, h[0], h[1], unit, 0);
+  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, h[2], h[3], unit, 1);
+  if (!in) return;
+  ((uint16_t*)p.out)[(m * p.N + n) / 4] = scale == 255 ? 0 : (uint16_t)c;
+  if ((n & 31) == 0) put_scale(p, m, n, scale);
 }
 
 // Stores a wave's accumulators: 16 FA rows from m0; columns n0 .. of acc[0], and
@@ -287,62 +366,19 @@ __device__ __forceinline__ void finish(const Product& p, int64_t m0, int64_t n0,
         uint8_t* codes = (uint8_t*)p.out + m * (N / 2) + nb / 2;
         *(uint16_t*)(codes + 2 * q) = (uint16_t)c;
         *(uint16_t*)(codes + 8 + 2 * q) = (uint16_t)(c >> 16);
-        if (q == 0) {
-          uint8_t* scales = (uint8_t*)p.aux + m * scale_stride(N);
-          scales[nb / 32] = (uint8_t)scale;
-          if (nb + 32 == N)
-            for (int64_t b = N / 32; b < scale_stride(N); ++b) scales[b] = 127;
-        }
+        if (q == 0) put_scale(p, m, nb, scale);
       }
       continue;
     }
 #pragma unroll
     for (int j = 0; j < FB; ++j) {
-      const int64_t nq = n0 + j * 16 + (lane >> 4) * 4;
+      const int64_t n = n0 + j * 16 + (lane >> 4) * 4;
       if (m >= p.M) continue;
-      if constexpr (EPI == kSwiglu) {
-        if (nq >= N) continue;
-        float h[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float g = acc[0][i][j][r];
-          h[r] = g * sigmoid(g) * acc[1][i][j][r];
-        }
-        *(u32x2*)((uint16_t*)p.out + m * N + nq) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
-        if (p.aux) {
-          float* gu = (float*)p.aux + m * 2 * N + nq;
-          *(f32x4*)gu = acc[0][i][j];
-          *(f32x4*)(gu + N) = acc[1][i][j];
-        }
-      } else {
-#pragma unroll
-        for (int hb = 0; hb < 2; ++hb) {
-          const int64_t n = nq + hb * half;
-          if (n >= N) continue;
-          const f32x4 v = acc[hb][i][j];
-          if constexpr (EPI == kStoreF32) {
-            *(f32x4*)((float*)p.out + m * N + n) = v;
-          } else if constexpr (EPI == kStoreBf16) {
-            *(u32x2*)((uint16_t*)p.out + m * N + n) =
-                u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-          } else {
-            const float* gu = (const float*)p.aux + m * 2 * N + n;
-            const f32x4 g = *(const f32x4*)gu, u = *(const f32x4*)(gu + N);
-            float dg[4], du[4], h[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float sg = sigmoid(g[r]);
-              du[r] = v[r] * g[r] * sg;
-              dg[r] = v[r] * u[r] * sg * (1.0f + g[r] * (1.0f - sg));
-              h[r] = g[r] * sg * u[r];
-            }
-            uint16_t* d = (uint16_t*)p.out + m * 2 * N + n;
-            *(u32x2*)d = u32x2{pack2(dg[0], dg[1]), pack2(dg[2], dg[3])};
-            *(u32x2*)(d + N) = u32x2{pack2(du[0], du[1]), pack2(du[2], du[3])};
-            *(u32x2*)((uint16_t*)p.out2 + m * N + n) =
-                u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
-          }
-        }
+      if constexpr (EPI == kSwiglu || EPI == kPartialPaired) {
+        if (n < N) emit<EPI>(p, m, n, acc[0][i][j], acc[1][i][j]);
+      } else if constexpr (EPI != kSwigluMx) {
+        if (n < N) emit<EPI>(p, m, n, acc[0][i][j], acc[0][i][j]);
+        if (n + half < N) emit<EPI>(p, m, n + half, acc[1][i][j], acc[1][i][j]);
       }
     }
   }
@@ -364,26 +400,36 @@ __device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
   return TileId{g * 8 + (t - g * group) % h, (t - g * group) / h};
 }
 
-// Tile of 128 x (2 x 64): four waves (2 x 2) of 64 rows x (2 x 32) columns.
-// Two work-groups share a CU and cover each other's waits.
+// Tile of 128 x (2 x 64): four waves (2 x 2) of 64 rows x (2 x 32) columns, for
+// launches that leave CUs idle: a ring of four stages, copied three ahead,
+// and one barrier a stage. blockIdx.y is the work-group's share of K.
 template <Kind KA, Kind KB, bool MX, Epilogue EPI>
-__global__ __launch_bounds__(256, 2) void tile_kernel(const Product p) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass needs the stub alone
+__global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
+#if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NW = 4, HRA = 128, HRB = 64, FA = 4, FB = 2;
-  constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx;  // B half 1: the up columns
-  constexpr int kCols = kPaired ? HRB : 2 * HRB;                // output columns
+  constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
+  constexpr int kCols = kPaired ? HRB : 2 * HRB;  // output columns
   typedef Half<KA, HRA, NW> HA;
   typedef Half<KB, HRB, NW> HB;
+  // an object a stage and operand: the compiler then sees which copies a read has to wait for
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[HA::kBytes], sa1[HA::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb00[HB::kBytes], sb01[HB::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb10[HB::kBytes], sb11[HB::kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t ss[2][MX ? (HRA + 2 * HRB) * 8 : 8];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa2[HA::kBytes], sa3[HA::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[2 * HB::kBytes], sb1[2 * HB::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[2 * HB::kBytes], sb3[2 * HB::kBytes];
+  constexpr int kScales = MX ? 8 * (HRA + 2 * HRB) : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t ss0[kScales], ss1[kScales];
+  __shared__ __attribute__((aligned(16))) uint8_t ss2[kScales], ss3[kScales];
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t tm = (p.M + HRA - 1) / HRA, tn = (p.N + kCols - 1) / kCols;
   const TileId t = tile_of(blockIdx.x, tm, tn);
   const int64_t m0 = t.m * HRA, n0 = t.n * kCols;
+  const int first = blockIdx.y * share;  // stages [first, first + count)
+  const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
+  const int count = stages - first < share ? stages - first : share;
+  if constexpr (EPI == kPartial || EPI == kPartialPaired)
+    p.out = (float*)p.out + (int64_t)blockIdx.y * p.M * p.N * (kPaired ? 2 : 1);
 
   HA a;
   HB b0, b1;
@@ -391,19 +437,23 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(const Product p) {
   Lane<KB, HRB, NW> lb;
   la.init(p.lda, wave, lane);
   lb.init(p.ldb, wave, lane);
-  const int64_t Kext = KA == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
-  const int64_t Kextb = KB == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
-  a.init(p.a, m0, p.M, p.lda, Kext);
-  b0.init(p.b, n0, p.N, p.ldb, Kextb);
+  const int64_t ka = KA == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
+  const int64_t kb = KB == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
+  const int64_t ea = (int64_t)(first + count) * (KA == KC ? kRow : 64);
+  const int64_t eb = (int64_t)(first + count) * (KB == KC ? kRow : 64);
+  a.init(p.a, m0, p.M, p.lda, ka, ka < ea ? ka : ea);
+  b0.init(p.b, n0, p.N, p.ldb, kb, kb < eb ? kb : eb);
   if (kPaired)
-    b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, Kextb);
+    b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, kb, kb < eb ? kb : eb);
   else
-    b1.init(p.b, n0 + HRB, p.N, p.ldb, Kextb);
-  const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
-
-  Scales<HRA, 2 * HRB, 64, 32, 256> sc;
-  if constexpr (MX)
-    sc.init(p, m0, n0, kPaired ? n0 : n0 + HRB, kPaired ? p.N : 0);
+    b1.init(p.b, n0 + HRB, p.N, p.ldb, kb, kb < eb ? kb : eb);
+  HalfScales sca, scb0, scb1;
+  if constexpr (MX) {
+    const int64_t all = kPaired ? 2 * (int64_t)p.N : p.N;
+    sca.init(p.a_scales, 0, m0, p.M, p.M, p.K);
+    scb0.init(p.b_scales, 0, n0, p.N, all, p.K);
+    scb1.init(p.b_scales, kPaired ? p.N : 0, kPaired ? n0 : n0 + HRB, p.N, all, p.K);
+  }
 
   f32x4 acc[2][FA][FB];
 #pragma unroll
@@ -413,52 +463,93 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(const Product p) {
 #pragma unroll
       for (int j = 0; j < FB; ++j) acc[h][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  if constexpr (MX) sc.load(0);
-  a.copy(sa0, 0, wave, la);
-  b0.copy(sb00, 0, wave, lb);
-  b1.copy(sb10, 0, wave, lb);
-
-  auto step = [&](int s, auto parity) {
-    constexpr int cur = decltype(parity)::value;
-    const uint8_t* a_now = cur ? sa1 : sa0;
-    const uint8_t* b0_now = cur ? sb01 : sb00;
-    const uint8_t* b1_now = cur ? sb11 : sb10;
-    if constexpr (MX) sc.put(ss[cur]);
-    wait_vm<0>();
+  constexpr int kCopies = HA::kPer + 2 * HB::kPer;
+  auto copy = [&](int s, auto buffer) {
+    constexpr int buf = decltype(buffer)::value;
+    uint8_t* sa = buf == 0 ? sa0 : buf == 1 ? sa1 : buf == 2 ? sa2 : sa3;
+    uint8_t* sb = buf == 0 ? sb0 : buf == 1 ? sb1 : buf == 2 ? sb2 : sb3;
+    uint8_t* ss = buf == 0 ? ss0 : buf == 1 ? ss1 : buf == 2 ? ss2 : ss3;
+    if constexpr (MX) {
+      if (wave == 0) sca.template copy<HRA>(ss, s, lane);
+      if (wave == 1) scb0.template copy<HRB>(ss + 8 * HRA, s, lane);
+      if (wave == 2) scb1.template copy<HRB>(ss + 8 * (HRA + HRB), s, lane);
+    }
+    a.copy(sa, s, wave, la);
+    b0.copy(sb, s, wave, lb);
+    b1.copy(sb + HB::kBytes, s, wave, lb);
+  };
+  auto step = [&](int s, auto buffer) {
+    constexpr int buf = decltype(buffer)::value;
+    const uint8_t* sa = buf == 0 ? sa0 : buf == 1 ? sa1 : buf == 2 ? sa2 : sa3;
+    const uint8_t* sb = buf == 0 ? sb0 : buf == 1 ? sb1 : buf == 2 ? sb2 : sb3;
+    const uint8_t* ss = buf == 0 ? ss0 : buf == 1 ? ss1 : buf == 2 ? ss2 : ss3;
+    wait_vm<2 * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    a.copy(cur ? sa0 : sa1, s + 1, wave, la);
-    b0.copy(cur ? sb00 : sb01, s + 1, wave, lb);
-    b1.copy(cur ? sb10 : sb11, s + 1, wave, lb);
-    if constexpr (MX) sc.load(s + 1);
+    copy(s + 3, std::integral_constant<int, (buf + 3) % 4>{});
     __builtin_amdgcn_sched_barrier(0);
     Frags<KA, HRA, FA> fa;
     Frags<KB, HRB, FB> fb0, fb1;
-    fa.read(a_now, wm * 64, lane);
-    fb0.read(b0_now, wn * 32, lane);
-    fb1.read(b1_now, wn * 32, lane);
+    fa.read(sa, wm * 64, lane);
+    fb0.read(sb, wn * 32, lane);
+    fb1.read(sb + HB::kBytes, wn * 32, lane);
     u32x2 sm = {};
     uint32_t sn0 = 0, sn1 = 0;
     if constexpr (MX) {
-      const int at = (lane & 15) * 4 + (lane >> 4);
-      sm = *(const u32x2*)(ss[cur] + wm * 64 * 8 + at * 8);
-      sn0 = *(const uint32_t*)(ss[cur] + (HRA + wn * 32) * 8 + at * 4);
-      sn1 = *(const uint32_t*)(ss[cur] + (HRA + HRB + wn * 32) * 8 + at * 4);
+      uint32_t w[2];
+      read_scales<FA>(ss, wm * 64, lane, w);
+      sm = u32x2{w[0], w[1]};
+      read_scales<FB>(ss, HRA + wn * 32, lane, &sn0);
+      read_scales<FB>(ss, HRA + HRB + wn * 32, lane, &sn1);
     }
     mma<MX>(acc[0], fb0.v, fa.v, sn0, sm, std::make_integer_sequence<int, 2 * FA * FB>{});
     mma<MX>(acc[1], fb1.v, fa.v, sn1, sm, std::make_integer_sequence<int, 2 * FA * FB>{});
     __builtin_amdgcn_sched_barrier(0);
   };
+  copy(first, std::integral_constant<int, 0>{});
+  copy(first + 1, std::integral_constant<int, 1>{});
+  copy(first + 2, std::integral_constant<int, 2>{});
   int s = 0;
-  for (; s + 1 < stages; s += 2) {
-    step(s, std::integral_constant<int, 0>{});
-    step(s + 1, std::integral_constant<int, 1>{});
+  for (; s + 3 < count; s += 4) {
+    step(first + s, std::integral_constant<int, 0>{});
+    step(first + s + 1, std::integral_constant<int, 1>{});
+    step(first + s + 2, std::integral_constant<int, 2>{});
+    step(first + s + 3, std::integral_constant<int, 3>{});
   }
-  if (s < stages) step(s, std::integral_constant<int, 0>{});
+  if (s < count) step(first + s, std::integral_constant<int, 0>{});
+  if (s + 1 < count) step(first + s + 1, std::integral_constant<int, 1>{});
+  if (s + 2 < count) step(first + s + 2, std::integral_constant<int, 2>{});
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
-
   finish<EPI, FA, FB>(p, m0 + wm * 64, n0 + wn * 32, HRB, acc, lane);
+#endif
+}
+
+// Adds the shares of K in their order and finishes: one lane four columns of a
+// row; eight lanes a block where h is quantised.
+template <Epilogue EPI>
+__global__ __launch_bounds__(256) void join_kernel(const Product p, const float* __restrict__ sums,
+                                                   int shares) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx;
+  const int64_t quads = p.N / 4;
+  const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+  if (u >= p.M * quads) return;  // N is a multiple of 32 where lanes work together
+  const int64_t m = u / quads, n = (u - m * quads) * 4;
+  const int64_t pitch = (kPaired ? 2 : 1) * (int64_t)p.N;
+  const float* src = sums + m * pitch + n;
+  f32x4 v = *(const f32x4*)src, up = {};
+  if constexpr (kPaired) up = *(const f32x4*)(src + p.N);
+  for (int s = 1; s < shares; ++s) {
+    src += p.M * pitch;
+    v += *(const f32x4*)src;
+    if constexpr (kPaired) up += *(const f32x4*)(src + p.N);
+  }
+  if constexpr (EPI == kSwigluMx) {
+    emit_mx(p, m, n, v, up, true);
+  } else {
+    emit<EPI>(p, m, n, v, up);
+  }
 #endif
 }
 
@@ -494,7 +585,9 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   // AH = 2: the second A halves of the two buffers; AH = 1: the third buffer
   __shared__ __attribute__((aligned(1024))) uint8_t sx0[HA::kBytes], sx1[HB::kBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t sx2[AH == 1 ? HB::kBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t ss[2][MX ? (AH + 2) * HR * 8 : 8];
+  constexpr int kScales = MX ? 8 * (AH + 2) * HR : 16;
+  __shared__ __attribute__((aligned(16))) uint8_t ss0[kScales], ss1[kScales];
+  __shared__ __attribute__((aligned(16))) uint8_t ss2[AH == 1 ? kScales : 16];
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -510,26 +603,30 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   lb.init(KA == KC && KB == KC ? p.lda : p.ldb, wave, lane);  // NT: both rows hold K values
   const int64_t ka = KA == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
   const int64_t kb = KB == KC ? (MX ? p.K / 2 : 2 * p.K) : p.K;
-  a0.init(p.a, m0, p.M, p.lda, ka);
-  if constexpr (AH == 2) a1.init(p.a, m0 + HR, p.M, p.lda, ka);
-  b0.init(p.b, n0, p.N, p.ldb, kb);
+  a0.init(p.a, m0, p.M, p.lda, ka, ka);
+  if constexpr (AH == 2) a1.init(p.a, m0 + HR, p.M, p.lda, ka, ka);
+  b0.init(p.b, n0, p.N, p.ldb, kb, kb);
   if (kPaired)
-    b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, kb);
+    b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, kb, kb);
   else
-    b1.init(p.b, n0 + HR, p.N, p.ldb, kb);
+    b1.init(p.b, n0 + HR, p.N, p.ldb, kb, kb);
   const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
 
-  Scales<AH * HR, 2 * HR, 64, 32, (AH + 2) * HR> sc;
-  const bool scaled = MX && threadIdx.x < (AH + 2) * HR;
+  HalfScales scales[4];  // A's halves, then B's; wave i copies the i-th
   if constexpr (MX) {
-    if (scaled)
-      sc.init(p, m0, n0, kPaired ? n0 : n0 + HR, kPaired ? p.N : 0);
-    if (scaled) {
-      sc.load(0);
-      sc.put(ss[0]);
-      sc.load(1);
-    }
+    const int64_t all = kPaired ? 2 * (int64_t)p.N : p.N;
+    scales[0].init(p.a_scales, 0, m0, p.M, p.M, p.K);
+    if constexpr (AH == 2) scales[1].init(p.a_scales, 0, m0 + HR, p.M, p.M, p.K);
+    scales[AH].init(p.b_scales, 0, n0, p.N, all, p.K);
+    scales[AH + 1].init(p.b_scales, kPaired ? p.N : 0, kPaired ? n0 : n0 + HR, p.N, all, p.K);
   }
+  auto copy_scales = [&](uint8_t* ss, int stage) {
+    if constexpr (MX) {
+#pragma unroll
+      for (int i = 0; i < AH + 2; ++i)
+        if (wave == i) scales[i].template copy<HR>(ss + i * (8 * HR), stage, lane);
+    }
+  };
 
   f32x4 acc[AH][2][FA][FB];
 #pragma unroll
@@ -540,10 +637,12 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
       for (int j = 0; j < FB; ++j) acc[h / 2][h % 2][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   // stages 0 and 1, in the order in which they are waited for
+  copy_scales(ss0, 0);
   a0.copy(sa0, 0, wave, la);
   b0.copy(sb0, 0, wave, lb);
   b1.copy(sc0, 0, wave, lb);
   if constexpr (AH == 2) a1.copy(sx0, 0, wave, la);
+  copy_scales(ss1, 1);
   a0.copy(sa1, 1, wave, la);
   b0.copy(sb1, 1, wave, lb);
   b1.copy(sc1, 1, wave, lb);
@@ -555,9 +654,8 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 
   Frags<KA, HR, FA> fa;
   Frags<KB, HR, FB> fb0, fb1;
-  u32x2 sm = {};
+  u32x2 sm = {}, sm1 = {};
   uint32_t sn0 = 0, sn1 = 0;
-  const int at = (lane & 15) * 4 + (lane >> 4);
 
 #define FFN_MEM_DONE                     \
   wait_lgkm0();                          \
@@ -570,138 +668,247 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   __builtin_amdgcn_sched_barrier(0);     \
   __builtin_amdgcn_s_barrier();          \
   __builtin_amdgcn_sched_barrier(0);
-#define FFN_MMA(ah)                                                                         \
+#define FFN_MMA(ah, sm)                                                                     \
   mma<MX>(acc[ah][0], fb0.v, fa.v, sn0, sm, std::make_integer_sequence<int, 2 * FA * FB>{}); \
   mma<MX>(acc[ah][1], fb1.v, fa.v, sn1, sm, std::make_integer_sequence<int, 2 * FA * FB>{});
 
-  // stage s in buffer `buf`; sbuf: its scales' buffer
-  auto step = [&](int s, auto buffer, int sbuf) {
+  // stage s in buffer `buf`; its scales are read in its first phase, so that their place is
+  // free for stage s + 2 in the second
+  auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     constexpr int two = (buf + 2) % 3;  // AH = 1: the buffer of stage s + 2
     uint8_t* a_now = buf == 0 ? sa0 : buf == 1 ? sa1 : sx0;
     uint8_t* b0_now = buf == 0 ? sb0 : buf == 1 ? sb1 : sx1;
     uint8_t* b1_now = buf == 0 ? sc0 : buf == 1 ? sc1 : sx2;
+    uint8_t* ss_now = buf == 0 ? ss0 : buf == 1 ? ss1 : ss2;
     fa.read(a_now, wm * 64, lane);
     fb0.read(b0_now, wn * 32, lane);
     fb1.read(b1_now, wn * 32, lane);
     if constexpr (MX) {
-      sm = *(const u32x2*)(ss[sbuf] + wm * 64 * 8 + at * 8);
-      sn0 = *(const uint32_t*)(ss[sbuf] + (AH * HR + wn * 32) * 8 + at * 4);
-      sn1 = *(const uint32_t*)(ss[sbuf] + (AH * HR + HR + wn * 32) * 8 + at * 4);
+      uint32_t w[2];
+      read_scales<FA>(ss_now, wm * 64, lane, w);
+      sm = u32x2{w[0], w[1]};
+      if constexpr (AH == 2) {
+        read_scales<FA>(ss_now, HR + wm * 64, lane, w);
+        sm1 = u32x2{w[0], w[1]};
+      }
+      read_scales<FB>(ss_now, AH * HR + wn * 32, lane, &sn0);
+      read_scales<FB>(ss_now, (AH + 1) * HR + wn * 32, lane, &sn1);
     }
     if constexpr (AH == 2) {
+      __builtin_amdgcn_sched_barrier(0);  // the reads first: copies wait for their queue
       a1.copy(buf ? sx0 : sx1, s + 1, wave, la);
       wait_vm<4 * kCopies>();
       FFN_MEM_DONE
-      FFN_MMA(0)
+      FFN_MMA(0, sm)
       FFN_MMA_DONE
       fa.read(buf ? sx1 : sx0, wm * 64, lane);
-      if constexpr (MX) {
-        sm = *(const u32x2*)(ss[sbuf] + (HR + wm * 64) * 8 + at * 8);
-        sc.put(ss[sbuf ^ 1]);
-        sc.load(s + 2);
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      copy_scales(ss_now, s + 2);
       a0.copy(a_now, s + 2, wave, la);
       b0.copy(b0_now, s + 2, wave, lb);
       b1.copy(b1_now, s + 2, wave, lb);
       wait_vm<4 * kCopies>();
       FFN_MEM_DONE
-      FFN_MMA(1)
+      FFN_MMA(1, sm1)
       FFN_MMA_DONE
     } else {
-      if constexpr (MX) {
-        if (scaled) {
-          sc.put(ss[sbuf ^ 1]);
-          sc.load(s + 2);
-        }
-      }
+      __builtin_amdgcn_sched_barrier(0);
+      copy_scales(two == 0 ? ss0 : two == 1 ? ss1 : ss2, s + 2);
       a0.copy(two == 0 ? sa0 : two == 1 ? sa1 : sx0, s + 2, wave, la);
       b0.copy(two == 0 ? sb0 : two == 1 ? sb1 : sx1, s + 2, wave, lb);
       b1.copy(two == 0 ? sc0 : two == 1 ? sc1 : sx2, s + 2, wave, lb);
       wait_vm<3 * kCopies>();
       FFN_MEM_DONE
-      FFN_MMA(0)
+      FFN_MMA(0, sm)
       FFN_MMA_DONE
     }
   };
   int s = 0;
   if constexpr (AH == 2) {
     for (; s + 1 < stages; s += 2) {
-      step(s, std::integral_constant<int, 0>{}, 0);
-      step(s + 1, std::integral_constant<int, 1>{}, 1);
+      step(s, std::integral_constant<int, 0>{});
+      step(s + 1, std::integral_constant<int, 1>{});
     }
-    if (s < stages) step(s, std::integral_constant<int, 0>{}, 0);
+    if (s < stages) step(s, std::integral_constant<int, 0>{});
   } else {
     for (; s + 2 < stages; s += 3) {
-      step(s, std::integral_constant<int, 0>{}, s & 1);
-      step(s + 1, std::integral_constant<int, 1>{}, (s + 1) & 1);
-      step(s + 2, std::integral_constant<int, 2>{}, s & 1);
+      step(s, std::integral_constant<int, 0>{});
+      step(s + 1, std::integral_constant<int, 1>{});
+      step(s + 2, std::integral_constant<int, 2>{});
     }
-    if (s < stages) step(s, std::integral_constant<int, 0>{}, s & 1);
-    if (s + 1 < stages) step(s + 1, std::integral_constant<int, 1>{}, (s + 1) & 1);
+    if (s < stages) step(s, std::integral_constant<int, 0>{});
+    if (s + 1 < stages) step(s + 1, std::integral_constant<int, 1>{});
   }
 #undef FFN_MEM_DONE
 #undef FFN_MMA_DONE
 #undef FFN_MMA
   if (wave < NW / 2) __builtin_amdgcn_s_barrier();
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
+
+  // The tile leaves through LDS, an A half (128 x 256 fp32, 16 rows an object)
+  // at a time, so that memory sees whole rows: a lane then holds four columns
+  // and a wave a row of the tile (paired: two rows, each lane its gate and up
+  // columns). 16-byte piece c of a row lies at c ^ (row % 16).
+  const int r = lane & 15, q = lane >> 4;
+  uint8_t* const w0 = wm ? sb1 : sa0;
+  uint8_t* const w1 = wm ? sc1 : sb0;
+  uint8_t* const w2 = wm ? sx0 : sc0;
+  uint8_t* const w3 = wm ? sx1 : sa1;
+  const uint8_t* mine = wave < 4 ? (wave < 2 ? (wave == 0 ? sa0 : sb0) : (wave == 2 ? sc0 : sa1))
+                                 : (wave < 6 ? (wave == 4 ? sb1 : sc1) : (wave == 6 ? sx0 : sx1));
 #pragma unroll
-  for (int h = 0; h < AH; ++h)
-    finish<EPI, FA, FB>(p, m0 + h * HR + wm * 64, n0 + wn * 32, HR, acc[h], lane);
+  for (int h = 0; h < AH; ++h) {
+    __builtin_amdgcn_s_barrier();  // every wave is done with what the LDS held
+#pragma unroll
+    for (int i = 0; i < FA; ++i) {
+      uint8_t* row = (i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : w3) + r * 1024;
+#pragma unroll
+      for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+        for (int j = 0; j < FB; ++j)
+          *(f32x4*)(row + (((hb * 32 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][hb][i][j];
+    }
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    const int64_t mw = m0 + h * HR + wave * 16;
+    if constexpr (kPaired) {
+      const int64_t n = n0 + 4 * (lane & 31);
+#pragma unroll
+      for (int t = 0; t < 8; t += 4) {
+        f32x4 g[4], u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int x = 2 * (t + k) + (lane >> 5);
+          g[k] = *(const f32x4*)(mine + x * 1024 + (((lane & 31) ^ x) * 16));
+          u[k] = *(const f32x4*)(mine + x * 1024 + ((((lane & 31) + 32) ^ x) * 16));
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t m = mw + 2 * (t + k) + (lane >> 5);
+          const bool in = m < p.M && n < p.N;
+          if constexpr (EPI == kSwigluMx) {
+            emit_mx(p, m, n, g[k], u[k], in);
+          } else {
+            if (in) emit<EPI>(p, m, n, g[k], u[k]);
+          }
+        }
+      }
+    } else {
+      const int64_t n = n0 + 4 * lane;
+#pragma unroll
+      for (int t = 0; t < 16; t += 8) {
+        f32x4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          v[k] = *(const f32x4*)(mine + (t + k) * 1024 + ((lane ^ (t + k)) * 16));
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (mw + t + k < p.M && n < p.N) emit<EPI>(p, mw + t + k, n, v[k], v[k]);
+      }
+    }
+    wait_lgkm0();
+  }
 #endif
 }
 
-template <Kind KA, Kind KB, bool MX, Epilogue EPI>
-hipError_t launch(const Product& p, hipStream_t stream) {
-  constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
+// How a product is cut: the tile (0: 128 x 128, 1: 128 x 256, 2: 256 x 256;
+// half the columns where gate and up pair), and for tile 0 the shares of K.
+struct Cut {
+  int tile = 0, shares = 1, share = 1;
+  int64_t groups = 0;
+};
+Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, bool mx) {
+  const bool paired = epi == kSwiglu || epi == kSwigluMx;
   auto tiles = [&](int64_t rows, int64_t cols) {
-    return ((p.M + rows - 1) / rows) * ((p.N + cols - 1) / cols);
+    if (paired) cols /= 2;
+    return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
   };
-  const int64_t small = tiles(128, paired ? 64 : 128);
-  if (small == 0) return hipSuccess;
-  if (small > 0x7fffff) return hipErrorInvalidConfiguration;
-  const int64_t b2 = tiles(256, paired ? 128 : 256), b1 = tiles(128, paired ? 128 : 256);
-  // The tile by the time of a stage of K over all rounds of its work-groups on
-  // 256 CUs, in quarters of the 256 x 256 tile's 1.45 us: a 128 x 256 tile's
-  // stage takes 1.19 us (at 4096 tokens, 7168/2048: d h 133 us against 181 in
-  // 128 tiles of 256 x 256; the gate and up product 201 against 163), a round
-  // of two 128 x 128 tiles a CU 1.0 to 1.4 us (167 us and 232 us there), of
-  // one 0.75 us. Of equals the larger tile.
-  auto rounds = [](int64_t n, int64_t at_once) { return (double)((n + at_once - 1) / at_once); };
-  const double t2 = 4.0 * rounds(b2, 256), t1 = 3.3 * rounds(b1, 256);
-  const double t0 = small <= 256 ? 2.1 : 3.4 * rounds(small, 512);
-  if (t2 <= t1 && t2 <= t0)
-    hipLaunchKernelGGL((big_tile_kernel<2, KA, KB, MX, EPI>), dim3((unsigned)b2), dim3(512), 0,
-                       stream, p);
-  else if (t1 <= t0)
-    hipLaunchKernelGGL((big_tile_kernel<1, KA, KB, MX, EPI>), dim3((unsigned)b1), dim3(512), 0,
-                       stream, p);
-  else
-    hipLaunchKernelGGL((tile_kernel<KA, KB, MX, EPI>), dim3((unsigned)small), dim3(256), 0,
-                       stream, p);
+  auto rounds = [](int64_t n) { return (double)((n + 255) / 256); };
+  const int64_t n0 = tiles(128, 128), n1 = tiles(128, 256), n2 = tiles(256, 256);
+  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
+  // Microseconds on 256 CUs: rounds of work-groups times the stages of K and
+  // what a work-group costs besides; shares of K add their sums' way through
+  // memory (about 4 TB/s) and a launch. Measured: see the table of stage times.
+  const double fixed = 5.0;
+  auto time = [&](double n, double per_stage, double st) { return n * (st * per_stage + fixed); };
+  Cut c;
+  c.groups = n0;
+  double best = 1e30;
+  for (int shares = 1; shares <= 32 && (shares == 1 || shares <= stages / 2); ++shares) {
+    const int64_t share = (stages + shares - 1) / shares;
+    if (share * (shares - 1) >= stages && shares > 1) continue;  // an empty last share
+    const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
+    const double t = time(rounds(n0 * shares), 0.6, (double)share) +
+                     (shares > 1 ? 4.0 + 2 * sums / 4e6 : 0.0);
+    if (t < best) best = t, c.tile = 0, c.shares = shares, c.share = (int)(share ? share : 1);
+    if (n0 * shares >= 512) break;
+  }
+  const double t1 = time(rounds(n1), 1.19, (double)stages), t2 = time(rounds(n2), 1.45, (double)stages);
+  if (t1 <= best) best = t1, c = Cut{1, 1, (int)stages, n1};
+  if (t2 <= best) best = t2, c = Cut{2, 1, (int)stages, n2};
+  return c;
+}
+
+template <Epilogue EPI>
+hipError_t join(const Product& p, const void* sums, int shares, hipStream_t stream) {
+  const int64_t groups = (p.M * (p.N / 4) + 255) / 256, y = (groups + (1 << 20) - 1) >> 20;
+  hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups + y - 1) / y), (unsigned)y),
+                     dim3(256), 0, stream, p, (const float*)sums, shares);
+  return hipGetLastError();
+}
+
+template <Kind KA, Kind KB, bool MX, Epilogue EPI>
+hipError_t launch(const Product& p, void* split, hipStream_t stream) {
+  constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  const Cut c = cut_of(EPI, p.M, p.N, p.K, MX);
+  if (c.groups > 0x7fffff) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)c.groups, c.shares);
+  if (c.tile == 2) {
+    hipLaunchKernelGGL((big_tile_kernel<2, KA, KB, MX, EPI>), grid, dim3(512), 0, stream, p);
+  } else if (c.tile == 1) {
+    hipLaunchKernelGGL((big_tile_kernel<1, KA, KB, MX, EPI>), grid, dim3(512), 0, stream, p);
+  } else if (c.shares == 1) {
+    hipLaunchKernelGGL((tile_kernel<KA, KB, MX, EPI>), grid, dim3(256), 0, stream, p, c.share);
+  } else {
+    Product part = p;
+    part.out = split;
+    hipLaunchKernelGGL((tile_kernel<KA, KB, MX, paired ? kPartialPaired : kPartial>), grid,
+                       dim3(256), 0, stream, part, c.share);
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess ? e : join<EPI>(p, split, c.shares, stream);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p,
+size_t product_workspace(Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx) {
+  const Cut c = cut_of(epilogue, M, N, K, mx);
+  const bool paired = epilogue == kSwiglu || epilogue == kSwigluMx;
+  return c.shares > 1 ? (size_t)c.shares * M * N * (paired ? 8 : 4) : 0;
+}
+
+hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,
                           hipStream_t stream) {
-  if (layout == kNT && epilogue == kSwiglu) return launch<KC, KC, false, kSwiglu>(p, stream);
+  if (layout == kNT && epilogue == kSwiglu) return launch<KC, KC, false, kSwiglu>(p, split, stream);
   if (layout == kNT && epilogue == kStoreBf16)
-    return launch<KC, KC, false, kStoreBf16>(p, stream);
+    return launch<KC, KC, false, kStoreBf16>(p, split, stream);
   if (layout == kNN && epilogue == kSwigluGrad)
-    return launch<KC, RC, false, kSwigluGrad>(p, stream);
+    return launch<KC, RC, false, kSwigluGrad>(p, split, stream);
   if (layout == kNN && epilogue == kStoreBf16)
-    return launch<KC, RC, false, kStoreBf16>(p, stream);
+    return launch<KC, RC, false, kStoreBf16>(p, split, stream);
   if (layout == kTN && epilogue == kStoreBf16)
-    return launch<RC, RC, false, kStoreBf16>(p, stream);
+    return launch<RC, RC, false, kStoreBf16>(p, split, stream);
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_product_mx(Epilogue epilogue, const Product& p, hipStream_t stream) {
-  if (epilogue == kStoreBf16) return launch<KC, KC, true, kStoreBf16>(p, stream);
-  if (epilogue == kStoreF32) return launch<KC, KC, true, kStoreF32>(p, stream);
-  if (epilogue == kSwigluMx) return launch<KC, KC, true, kSwigluMx>(p, stream);
+hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
+                             hipStream_t stream) {
+  if (epilogue == kStoreBf16) return launch<KC, KC, true, kStoreBf16>(p, split, stream);
+  if (epilogue == kStoreF32) return launch<KC, KC, true, kStoreF32>(p, split, stream);
+  if (epilogue == kSwigluMx) return launch<KC, KC, true, kSwigluMx>(p, split, stream);
   return hipErrorInvalidValue;
 }
 

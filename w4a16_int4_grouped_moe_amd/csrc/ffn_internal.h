@@ -12,10 +12,12 @@ enum Epilogue {
   kStoreBf16 = 0,   // out bf16 [M, N]
   kStoreF32 = 1,    // out fp32 [M, N]
   kSwiglu = 2,      // out bf16 h [M, N]; aux fp32 [M, 2N] pre-activations or NULL
-  kSwigluMx = 3,    // out e2m1 codes of h [M, N/2], aux its scale bytes (scale_stride(N) a row)
+  kSwigluMx = 3,    // out e2m1 codes of h [M, N/2], aux its scale bytes by stage
   kSwigluGrad = 4,  // the product is dh: aux fp32 [M, 2N] pre-activations (read),
                     // out bf16 [M, 2N] their gradients, out2 bf16 h [M, N]
   kSwigluF32 = 5,   // out fp32 h [M, N]
+  kPartial = 6,     // a share of K: fp32 sums [share][M, N] in out
+  kPartialPaired = 7,  // fp32 gate and up sums [share][M, 2N]
 };
 
 // D[m, n] = sum_k A(m, k) B(n, k). An operand is "K contiguous" (element
@@ -23,15 +25,20 @@ enum Epilogue {
 // template parameter of the kernel (see Layout).
 enum Layout { kNT = 0, kNN = 1, kTN = 2 };  // A/B: KC/KC, KC/RC, RC/RC
 
-// The products read scale bytes eight at a time (one stage of K): each row's
-// scales are padded to whole stages, and rows start at multiples of 8 bytes.
-// The padding holds 127 (the scale 1; the codes there are 0).
-__host__ __device__ inline int64_t scale_stride(int64_t K) { return (K / 32 + 7) / 8 * 8; }
+// The tiled products read scales a stage of K (8 blocks) at a time, all rows of
+// a tile together: [stage][row][8 bytes], rows padded to an even number, the
+// last stage's missing blocks with any finite scale (their codes are 0).
+__host__ __device__ inline int64_t scale_stages(int64_t K) { return (K + 255) / 256; }
+__host__ __device__ inline int64_t scale_rows(int64_t rows) { return (rows + 1) / 2 * 2; }
+__host__ __device__ inline int64_t scale_bytes(int64_t rows, int64_t K) {
+  return 8 * scale_rows(rows) * scale_stages(K);
+}
 
 struct Product {
   const void* a;
   const void* b;
-  const uint8_t* a_scales = nullptr;  // MXFP4: e8m0 bytes, rows of scale_stride(K)
+  const uint8_t* a_scales = nullptr;  // MXFP4: e8m0 bytes by stage, scale_rows(M) and
+                                      // scale_rows(rows of b) a stage
   const uint8_t* b_scales = nullptr;
   int64_t lda, ldb;  // bytes from one row (KC) or one k (RC) to the next
   int64_t M;
@@ -42,10 +49,15 @@ struct Product {
   void* aux = nullptr;
 };
 
-// bf16 operands
-hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, hipStream_t stream);
+// bf16 operands. split: workspace of product_workspace bytes (16-byte aligned).
+hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,
+                          hipStream_t stream);
 // MXFP4 operands, both K contiguous; K a multiple of 32
-hipError_t launch_product_mx(Epilogue epilogue, const Product& p, hipStream_t stream);
+hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
+                             hipStream_t stream);
+// Where few tiles would run a long K, its shares go to several work-groups and
+// their sums here; 0 where they do not.
+size_t product_workspace(Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
 
 // The same products for a few rows (ffn_small.hip), both operands K contiguous
 // and dense. A: as the product takes it, or rows to be quantised to MXFP4.
@@ -57,15 +69,21 @@ bool rows_fit(const Product& p, bool mx, AType a, bool paired);
 hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream);
 hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream);
 
-// x [rows, width] (type: MOE_TYPE_*) -> e2m1 codes [rows, width/2], scales
-// [rows, width/32], or padded: rows of scale_stride(width)
+// x [rows, width] (type: MOE_TYPE_*) -> e2m1 codes [rows, width/2], scales [rows, width/32]
 hipError_t launch_mx_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
-                              uint8_t* codes, uint8_t* scales, bool padded, hipStream_t stream);
-// Two matrices' scales [rows, width/32] copied into padded rows (either may be
-// NULL with 0 rows)
-hipError_t launch_mx_pad_scales(const uint8_t* s0, int64_t rows0, uint8_t* out0,
-                                const uint8_t* s1, int64_t rows1, uint8_t* out1, int32_t width,
-                                hipStream_t stream);
+                              uint8_t* codes, uint8_t* scales, hipStream_t stream);
+// What the tiled products need beforehand, in one launch: x bf16 (or NULL)
+// quantised with its scales by stage, and up to two matrices' scales
+// [rows, width/32] copied into that order (src NULL: none).
+struct ScaleCopy {
+  const uint8_t* src = nullptr;
+  uint8_t* dst = nullptr;
+  int64_t rows = 0;
+  int32_t width = 0;
+};
+hipError_t launch_mx_prepare(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                             uint8_t* scales, const ScaleCopy& s0, const ScaleCopy& s1,
+                             hipStream_t stream);
 hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
                                 int32_t width, int32_t type, void* out, hipStream_t stream);
 

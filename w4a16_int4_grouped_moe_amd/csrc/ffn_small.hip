@@ -16,7 +16,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
+#include <algorithm>
 
 #include "ffn_device.h"
 #include "ffn_internal.h"
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kMaxRows = 16;
-constexpr int kMxLds = 56 * 1024;  // quantised A in LDS, codes and scales (64 KB with the sums)
+constexpr int kMxLds = 64 * 1024;  // quantised A in LDS, codes and scales
 
 // LDS rows of quantised A: 16 rows at one offset lie in distinct banks
 __host__ __device__ inline int code_stride(int64_t K) { return (int)((K / 2 + 255) / 256 * 256 + 16); }
@@ -88,8 +88,9 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluF32;
   constexpr int kD = AK == kFromF32 ? 3 : 5;  // stages in flight per wave
-  __shared__ __attribute__((aligned(16))) float sums[kWaves][256];
-  extern __shared__ __attribute__((aligned(16))) uint8_t qa[];  // quantised A: codes, then bytes
+  // quantised A (codes, then bytes), and in its place at the end the waves' sums
+  extern __shared__ __attribute__((aligned(16))) uint8_t qa[];
+  float* const sums = (float*)qa;
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -205,7 +206,8 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
   }
 
   // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row r
-  *(f32x4*)&sums[wave][r * 16 + 4 * q] = acc;
+  if constexpr (AK != kAsIs) __syncthreads();  // A is read to the end
+  *(f32x4*)&sums[wave * 256 + r * 16 + 4 * q] = acc;
   __syncthreads();
   const int i = threadIdx.x;
   if constexpr (kPaired) {
@@ -213,7 +215,7 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
     if (i >= 128 || m >= M) return;
     float g = 0.f, u = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) g += sums[k][m * 16 + j], u += sums[k][m * 16 + 8 + j];
+    for (int k = 0; k < kWaves; ++k) g += sums[k * 256 + m * 16 + j], u += sums[k * 256 + m * 16 + 8 + j];
     const float h = g * sigmoid(g) * u;
     const int64_t at = (int64_t)m * N + n0 + j;
     if constexpr (EPI == kSwigluF32) {
@@ -231,7 +233,7 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
     if (i >= 256 || m >= M || n >= N) return;
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += sums[k][i];
+    for (int k = 0; k < kWaves; ++k) v += sums[k * 256 + i];
     if constexpr (EPI == kStoreF32)
       ((float*)p.out)[(int64_t)m * N + n] = v;
     else
@@ -243,7 +245,8 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
 template <AKind AK, bool MX, Epilogue EPI>
 hipError_t launch(const Product& p, hipStream_t stream) {
   const unsigned groups = EPI == kSwiglu || EPI == kSwigluF32 ? (p.N + 7) / 8 : (p.N + 15) / 16;
-  const size_t lds = AK == kAsIs ? 0 : p.M * (code_stride(p.K) + byte_stride(p.K));
+  const size_t a = AK == kAsIs ? 0 : p.M * (code_stride(p.K) + byte_stride(p.K));
+  const size_t lds = std::max<size_t>(a, kWaves * 256 * sizeof(float));
   hipLaunchKernelGGL((rows_kernel<AK, MX, EPI>), dim3(groups), dim3(kThreads), lds, stream, p);
   return hipGetLastError();
 }

@@ -41,15 +41,9 @@ __device__ __forceinline__ void load8(const void* x, int64_t unit, float* v) {
   }
 }
 
-// pad: 0, or the scale bytes of a row (width/32) where they go into padded rows
+// Eight values of a block -> their codes; *byte: the block's scale
 template <int TYPE>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x,
-                                                            int64_t units, int32_t pad,
-                                                            uint32_t* __restrict__ codes,
-                                                            uint8_t* __restrict__ scales) {
-  // units is a multiple of 4: a block's lanes are all in or all out
-  const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  if (u >= units) return;
+__device__ __forceinline__ uint32_t quantize8(const void* x, int64_t u, uint32_t* byte) {
   float v[8];
   load8<TYPE>(x, u, v);
   uint32_t top = 0;
@@ -62,27 +56,87 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
   top = o1 > top ? o1 : top;
   const uint32_t o2 = __shfl_xor(top, 2);
   top = o2 > top ? o2 : top;
-  const uint32_t scale = mx_scale(top >> 23);
-  const float unit = mx_unit(scale);
+  *byte = mx_scale(top >> 23);
+  const float unit = mx_unit(*byte);
   uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], unit, 1);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], unit, 2);
   c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], unit, 3);
-  if (scale == 255) c = 0;
-  codes[u] = c;
-  if ((u & 3) == 0) {
-    const uint8_t byte = (uint8_t)scale;
-    const int64_t b = u >> 2;
-    if (pad == 0) {
-      scales[b] = byte;
-    } else {
-      const int64_t row = b / pad;
-      const int32_t at = (int32_t)(b - row * pad), stride = (pad + 7) / 8 * 8;
-      scales[row * stride + at] = byte;
-      if (at == pad - 1)
-        for (int32_t i = pad; i < stride; ++i) scales[row * stride + i] = 127;
+  return *byte == 255 ? 0 : c;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restrict__ x,
+                                                            int64_t units,
+                                                            uint32_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales) {
+  // units is a multiple of 4: a block's lanes are all in or all out
+  const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (u >= units) return;
+  uint32_t byte;
+  codes[u] = quantize8<TYPE>(x, u, &byte);
+  if ((u & 3) == 0) scales[u >> 2] = (uint8_t)byte;
+}
+
+// The first work-groups copy scales into the order by stage, one wave 64 rows
+// of four stages (the rows' bytes come in runs of 32 and leave 512 at a time);
+// they wait on memory, so they start ahead of those that quantise x.
+struct Prepare {
+  const void* x;
+  int64_t units, rows;
+  int32_t blocks;  // of a row of x
+  uint32_t* codes;
+  uint8_t* scales;
+  int64_t groups0, groups;  // work-groups of s0, of s0 and s1
+  ScaleCopy s0, s1;
+};
+__global__ __launch_bounds__(kThreads) void prepare_kernel(const Prepare p) {
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (group >= p.groups) {
+    const int64_t u = (group - p.groups) * kThreads + threadIdx.x;
+    if (u >= p.units) return;
+    uint32_t byte;
+    p.codes[u] = quantize8<MOE_TYPE_BF16>(p.x, u, &byte);
+    if ((u & 3) != 0) return;
+    const int64_t b = u >> 2, row = b / p.blocks;
+    const int32_t at = (int32_t)(b - row * p.blocks);
+    uint8_t* dst = p.scales + ((at >> 3) * scale_rows(p.rows) + row) * 8;
+    dst[at & 7] = (uint8_t)byte;
+    if (at == p.blocks - 1)
+      for (int i = (at & 7) + 1; i < 8; ++i) dst[i] = 127;
+    return;
+  }
+  const bool second = group >= p.groups0;
+  const ScaleCopy& s = second ? p.s1 : p.s0;
+  const int64_t wave = (group - (second ? p.groups0 : 0)) * (kThreads / 64) + (threadIdx.x >> 6);
+  const int64_t stages = scale_stages(s.width), quads = (stages + 3) / 4;
+  const int64_t row = wave / quads * 64 + (threadIdx.x & 63), s0 = wave % quads * 4;
+  if (row >= s.rows) return;
+  const int32_t blocks = s.width / 32;
+  const uint8_t* src = s.src + row * blocks;
+  const int64_t pitch = scale_rows(s.rows) * 8;
+  uint8_t* dst = s.dst + row * 8 + s0 * pitch;
+  const int count = (int)(stages - s0 < 4 ? stages - s0 : 4);
+  u32x2 v[4];
+  if (blocks % 8 == 0 && ((uintptr_t)s.src & 7) == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) v[i] = *(const u32x2*)(src + (s0 + i) * 8);
+  } else {  // rows start at any byte, and the last stage may be short
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t b = (s0 + i) * 8 + j;
+        const uint32_t byte = b < blocks ? src[b] : 127u;
+        v[i][j / 4] = (v[i][j / 4] & ~(0xffu << (8 * (j & 3)))) | (byte << (8 * (j & 3)));
+      }
     }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < count) *(u32x2*)(dst + i * pitch) = v[i];
 }
 
 template <int TYPE>
@@ -120,54 +174,51 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint32_t* __
   }
 }
 
-// One thread a padded scale byte, of the first matrix and then of the second.
-__global__ __launch_bounds__(kThreads) void pad_scales_kernel(
-    const uint8_t* __restrict__ s0, int64_t n0, uint8_t* __restrict__ out0,
-    const uint8_t* __restrict__ s1, int64_t n1, uint8_t* __restrict__ out1, int32_t blocks,
-    int32_t stride) {
-  int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
-  if (u >= n0 + n1) return;
-  const bool second = u >= n0;
-  if (second) u -= n0;
-  const int64_t row = u / stride;
-  const int32_t at = (int32_t)(u - row * stride);
-  (second ? out1 : out0)[u] = at < blocks ? (second ? s1 : s0)[row * blocks + at] : 127;
-}
-
-// work-groups for `units` lanes: one dimension of a launch holds fewer than 2^32 lanes
-dim3 grid_of(int64_t units) {
-  const int64_t groups = (units + kThreads - 1) / kThreads;
+// a launch of `groups` work-groups: one dimension holds fewer than 2^32 lanes
+dim3 grid_of(int64_t groups) {
   const int64_t y = (groups + (1 << 20) - 1) >> 20;
   return dim3((unsigned)((groups + y - 1) / y), (unsigned)y);
 }
 
 }  // namespace
 
-hipError_t launch_mx_pad_scales(const uint8_t* s0, int64_t rows0, uint8_t* out0,
-                                const uint8_t* s1, int64_t rows1, uint8_t* out1, int32_t width,
-                                hipStream_t stream) {
-  const int32_t stride = (int32_t)scale_stride(width);
-  if (rows0 + rows1 == 0) return hipSuccess;
-  hipLaunchKernelGGL(pad_scales_kernel, grid_of((rows0 + rows1) * stride), dim3(kThreads), 0,
-                     stream, s0, rows0 * stride, out0, s1, rows1 * stride, out1, width / 32,
-                     stride);
+hipError_t launch_mx_prepare(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                             uint8_t* scales, const ScaleCopy& s0, const ScaleCopy& s1,
+                             hipStream_t stream) {
+  auto copy_groups = [](const ScaleCopy& s) {
+    const int64_t waves = (s.rows + 63) / 64 * ((scale_stages(s.width) + 3) / 4);
+    return s.src ? (waves + kThreads / 64 - 1) / (kThreads / 64) : (int64_t)0;
+  };
+  Prepare p{};
+  p.x = x;
+  p.units = x ? rows * (width / 8) : 0;
+  p.rows = rows;
+  p.blocks = width / 32;
+  p.codes = (uint32_t*)codes;
+  p.scales = scales;
+  p.groups0 = copy_groups(s0);
+  p.groups = p.groups0 + copy_groups(s1);
+  p.s0 = s0;
+  p.s1 = s1;
+  const int64_t total = p.groups + (p.units + kThreads - 1) / kThreads;
+  if (total == 0) return hipSuccess;
+  hipLaunchKernelGGL(prepare_kernel, grid_of(total), dim3(kThreads), 0, stream, p);
   return hipGetLastError();
 }
 
 hipError_t launch_mx_quantize(const void* x, int32_t type, int64_t rows, int32_t width,
-                              uint8_t* codes, uint8_t* scales, bool padded, hipStream_t stream) {
+                              uint8_t* codes, uint8_t* scales, hipStream_t stream) {
   const int64_t units = rows * (width / 8);
   if (units == 0) return hipSuccess;
-  const dim3 grid = grid_of(units), block(kThreads);
-  const int32_t pad = padded && width % 256 ? width / 32 : 0;
+  const dim3 grid = grid_of((units + kThreads - 1) / kThreads), block(kThreads);
   if (type == MOE_TYPE_BF16)
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_BF16>, grid, block, 0, stream, x, units, pad,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_BF16>, grid, block, 0, stream, x, units,
                        (uint32_t*)codes, scales);
   else if (type == MOE_TYPE_FP16)
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP16>, grid, block, 0, stream, x, units, pad,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP16>, grid, block, 0, stream, x, units,
                        (uint32_t*)codes, scales);
   else
-    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP32>, grid, block, 0, stream, x, units, pad,
+    hipLaunchKernelGGL(quantize_kernel<MOE_TYPE_FP32>, grid, block, 0, stream, x, units,
                        (uint32_t*)codes, scales);
   return hipGetLastError();
 }
@@ -176,7 +227,7 @@ hipError_t launch_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int
                                 int32_t width, int32_t type, void* out, hipStream_t stream) {
   const int64_t units = rows * (width / 8);
   if (units == 0) return hipSuccess;
-  const dim3 grid = grid_of(units), block(kThreads);
+  const dim3 grid = grid_of((units + kThreads - 1) / kThreads), block(kThreads);
   if (type == MOE_TYPE_BF16)
     hipLaunchKernelGGL(dequantize_kernel<MOE_TYPE_BF16>, grid, block, 0, stream,
                        (const uint32_t*)codes, scales, units, out);
