@@ -78,17 +78,17 @@ size_t split_of(const moe_ffn_problem* p, int pass) {
   const int64_t T = p->num_tokens, H = p->hidden, I = p->inter;
   const bool mx = pass == MOE_FFN_FORWARD_MXFP4;
   size_t most = 0;
-  auto add = [&](ffn::Epilogue epi, int64_t M, int64_t N, int64_t K) {
-    most = std::max(most, ffn::product_workspace(epi, M, (int32_t)N, K, mx));
+  auto add = [&](ffn::Layout layout, ffn::Epilogue epi, int64_t M, int64_t N, int64_t K) {
+    most = std::max(most, ffn::product_workspace(layout, epi, M, (int32_t)N, K, mx));
   };
   if (pass == MOE_FFN_BACKWARD) {
-    add(ffn::kSwigluGrad, T, I, H);
-    add(ffn::kStoreBf16, T, H, 2 * I);
-    add(ffn::kStoreBf16, 2 * I, H, T);
-    add(ffn::kStoreBf16, H, I, T);
+    add(ffn::kNN, ffn::kSwigluGrad, T, I, H);
+    add(ffn::kNN, ffn::kStoreBf16, T, H, 2 * I);
+    add(ffn::kTN, ffn::kStoreBf16, 2 * I, H, T);
+    add(ffn::kTN, ffn::kStoreBf16, H, I, T);
   } else {
-    add(mx ? ffn::kSwigluMx : ffn::kSwiglu, T, I, H);
-    add(ffn::kStoreBf16, T, H, I);
+    add(ffn::kNT, mx ? ffn::kSwigluMx : ffn::kSwiglu, T, I, H);
+    add(ffn::kNT, ffn::kStoreBf16, T, H, I);
   }
   return region(most);
 }
@@ -224,7 +224,7 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   if (rows == 0 || few_rows(rows, cols, width, quantize)) return MOE_OK;
   *bytes = (quantize ? MxRegion(rows, width).bytes() : region(ffn::scale_bytes(rows, width))) +
            region(ffn::scale_bytes(cols, width)) +
-           region(ffn::product_workspace(ffn::kStoreF32, rows, cols, width, true));
+           region(ffn::product_workspace(ffn::kNT, ffn::kStoreF32, rows, cols, width, true));
   return MOE_OK;
 }
 

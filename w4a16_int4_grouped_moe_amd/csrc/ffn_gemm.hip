@@ -239,29 +239,6 @@ __device__ __forceinline__ void read_scales(const uint8_t* slot, int first, int 
   }
 }
 
-// Quantises one block of 32 values of which this lane holds 2 x 4 and the
-// lanes 16, 32 and 48 away the rest; returns the two groups' codes (16 bits
-// each) and the block's scale byte.
-__device__ __forceinline__ uint32_t mx_quantize8(const float* v, uint32_t* scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v[i]) & 0x7fffffffu;
-    top = b > top ? b : top;
-  }
-  const uint32_t o1 = __shfl_xor(top, 16);
-  top = o1 > top ? o1 : top;
-  const uint32_t o2 = __shfl_xor(top, 32);
-  top = o2 > top ? o2 : top;
-  *scale = mx_scale(top >> 23);
-  const float unit = mx_unit(*scale);
-  uint32_t c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, v[0], v[1], unit, 0);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2], v[3], unit, 1);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4], v[5], unit, 2);
-  c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6], v[7], unit, 3);
-  return *scale == 255 ? 0 : c;
-}
-
 // The scale byte of h's block from column n of row m; the last block fills its stage.
 __device__ __forceinline__ void put_scale(const Product& p, int64_t m, int64_t n, uint32_t scale) {
   uint8_t* dst = (uint8_t*)p.aux + (n / 256 * scale_rows(p.M) + m) * 8;
@@ -294,23 +271,31 @@ __device__ __forceinline__ void emit(const Product& p, int64_t m, int64_t n, con
       *(f32x4*)gu = v;
       *(f32x4*)(gu + N) = up;
     }
-  } else {
-    static_assert(EPI == kSwigluGrad, "epilogue");
-    const float* gu = (const float*)p.aux + m * 2 * N + n;
-    const f32x4 g = *(const f32x4*)gu, u = *(const f32x4*)(gu + N);
-    float dg[4], du[4], h[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float sg = sigmoid(g[r]);
-      du[r] = v[r] * g[r] * sg;
-      dg[r] = v[r] * u[r] * sg * (1.0f + g[r] * (1.0f - sg));
-      h[r] = g[r] * sg * u[r];
-    }
-    uint16_t* d = (uint16_t*)p.out + m * 2 * N + n;
-    *(u32x2*)d = u32x2{pack2(dg[0], dg[1]), pack2(dg[2], dg[3])};
-    *(u32x2*)(d + N) = u32x2{pack2(du[0], du[1]), pack2(du[2], du[3])};
-    *(u32x2*)((uint16_t*)p.out2 + m * N + n) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
   }
+}
+
+// Four columns of dh -> the gradients of g and u, and h.
+__device__ __forceinline__ void emit_grad(const Product& p, int64_t m, int64_t n, const f32x4& v,
+                                          const f32x4& g, const f32x4& u) {
+  const int64_t N = p.N;
+  float dg[4], du[4], h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float sg = sigmoid(g[r]);
+    du[r] = v[r] * g[r] * sg;
+    dg[r] = v[r] * u[r] * sg * (1.0f + g[r] * (1.0f - sg));
+    h[r] = g[r] * sg * u[r];
+  }
+  uint16_t* d = (uint16_t*)p.out + m * 2 * N + n;
+  *(u32x2*)d = u32x2{pack2(dg[0], dg[1]), pack2(dg[2], dg[3])};
+  *(u32x2*)(d + N) = u32x2{pack2(du[0], du[1]), pack2(du[2], du[3])};
+  *(u32x2*)((uint16_t*)p.out2 + m * N + n) = u32x2{pack2(h[0], h[1]), pack2(h[2], h[3])};
+}
+__device__ __forceinline__ void load_gate_up(const Product& p, int64_t m, int64_t n, f32x4& g,
+                                             f32x4& u) {
+  const float* gu = (const float*)p.aux + m * 2 * (int64_t)p.N + n;
+  g = *(const f32x4*)gu;
+  u = *(const f32x4*)(gu + p.N);
 }
 
 // Four h columns from n of row m, quantised with the seven lanes that hold the
@@ -339,46 +324,48 @@ __device__ __forceinline__ void emit_mx(const Product& p, int64_t m, int64_t n, 
   if ((n & 31) == 0) put_scale(p, m, n, scale);
 }
 
-// Stores a wave's accumulators: 16 FA rows from m0; columns n0 .. of acc[0], and
-// of acc[1] `half` further (or, paired, the up columns of the same h columns).
-// A lane holds columns nq .. nq + 3 of row m.
-template <Epilogue EPI, int FA, int FB>
-__device__ __forceinline__ void finish(const Product& p, int64_t m0, int64_t n0, int half,
-                                       const f32x4 (&acc)[2][FA][FB], int lane) {
-  const int64_t N = p.N;
+// A tile leaves through LDS as fp32 rows, so that memory sees whole rows: the
+// waves write their accumulators (16-byte piece c of row r at c ^ (r % 16)),
+// then each takes 16 KB of whole rows, a lane four columns of one (paired: of
+// its gate and its up columns). COLS: columns of a row in LDS; m0: the row of
+// the tile's matrix at `lds`.
+template <Epilogue EPI, int COLS>
+__device__ __forceinline__ void store_rows(const Product& p, const uint8_t* lds, int64_t m0,
+                                           int64_t n0, int lane) {
+  constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
+  constexpr int kLanes = COLS / (kPaired ? 8 : 4);  // a row's lanes
+  constexpr int kRowsAtOnce = 64 / kLanes, kRows = 16384 / (4 * COLS);
+  constexpr int kBatch = kPaired ? 4 : 8;
+  const int c = lane % kLanes;
+  const int64_t n = n0 + 4 * c;
 #pragma unroll
-  for (int i = 0; i < FA; ++i) {
-    const int64_t m = m0 + i * 16 + (lane & 15);
-    if constexpr (EPI == kSwigluMx) {
-      float h[8];
+  for (int t = 0; t < kRows / kRowsAtOnce; t += kBatch) {
+    f32x4 v[kBatch], up[kBatch], g[kBatch];
+    if constexpr (EPI == kSwigluGrad) {  // a batch's pre-activations on their way together
 #pragma unroll
-      for (int j = 0; j < FB; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float g = acc[0][i][j][r];
-          h[4 * j + r] = g * sigmoid(g) * acc[1][i][j][r];
-        }
-      uint32_t scale;
-      const uint32_t c = mx_quantize8(h, &scale);
-      const int64_t nb = n0;  // the block's first column; N is a multiple of 32
-      if (m < p.M && nb < N) {
-        const int q = lane >> 4;
-        uint8_t* codes = (uint8_t*)p.out + m * (N / 2) + nb / 2;
-        *(uint16_t*)(codes + 2 * q) = (uint16_t)c;
-        *(uint16_t*)(codes + 8 + 2 * q) = (uint16_t)(c >> 16);
-        if (q == 0) put_scale(p, m, nb, scale);
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t m = m0 + kRowsAtOnce * (t + k) + lane / kLanes;
+        g[k] = up[k] = f32x4{};
+        if (m < p.M && n < p.N) load_gate_up(p, m, n, g[k], up[k]);
       }
-      continue;
     }
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int64_t n = n0 + j * 16 + (lane >> 4) * 4;
-      if (m >= p.M) continue;
-      if constexpr (EPI == kSwiglu || EPI == kPartialPaired) {
-        if (n < N) emit<EPI>(p, m, n, acc[0][i][j], acc[1][i][j]);
-      } else if constexpr (EPI != kSwigluMx) {
-        if (n < N) emit<EPI>(p, m, n, acc[0][i][j], acc[0][i][j]);
-        if (n + half < N) emit<EPI>(p, m, n + half, acc[1][i][j], acc[1][i][j]);
+    for (int k = 0; k < kBatch; ++k) {
+      const int x = kRowsAtOnce * (t + k) + lane / kLanes;
+      v[k] = *(const f32x4*)(lds + x * (4 * COLS) + ((c ^ (x & 15)) * 16));
+      if constexpr (kPaired)
+        up[k] = *(const f32x4*)(lds + x * (4 * COLS) + (((c + kLanes) ^ (x & 15)) * 16));
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t m = m0 + kRowsAtOnce * (t + k) + lane / kLanes;
+      const bool in = m < p.M && n < p.N;
+      if constexpr (EPI == kSwigluMx) {
+        emit_mx(p, m, n, v[k], up[k], in);
+      } else if constexpr (EPI == kSwigluGrad) {
+        if (in) emit_grad(p, m, n, v[k], g[k], up[k]);
+      } else {
+        if (in) emit<EPI>(p, m, n, v[k], up[k]);
       }
     }
   }
@@ -521,7 +508,21 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
   if (s + 1 < count) step(first + s + 1, std::integral_constant<int, 1>{});
   if (s + 2 < count) step(first + s + 2, std::integral_constant<int, 2>{});
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
-  finish<EPI, FA, FB>(p, m0 + wm * 64, n0 + wn * 32, HRB, acc, lane);
+  __builtin_amdgcn_s_barrier();
+  const int r = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int i = 0; i < FA; ++i) {  // 32 rows of 128 columns an object
+    uint8_t* row = (i < 2 ? (wm ? sa2 : sa0) : (wm ? sa3 : sa1)) + ((i & 1) * 16 + r) * 512;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < FB; ++j)
+        *(f32x4*)(row + (((h * 16 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][i][j];
+  }
+  wait_lgkm0();
+  __builtin_amdgcn_s_barrier();
+  store_rows<EPI, 128>(p, wave < 2 ? (wave == 0 ? sa0 : sa1) : (wave == 2 ? sa2 : sa3),
+                       m0 + wave * 32, n0, lane);
 #endif
 }
 
@@ -547,6 +548,10 @@ __global__ __launch_bounds__(256) void join_kernel(const Product p, const float*
   }
   if constexpr (EPI == kSwigluMx) {
     emit_mx(p, m, n, v, up, true);
+  } else if constexpr (EPI == kSwigluGrad) {
+    f32x4 g;
+    load_gate_up(p, m, n, g, up);
+    emit_grad(p, m, n, v, g, up);
   } else {
     emit<EPI>(p, m, n, v, up);
   }
@@ -746,10 +751,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   if (wave < NW / 2) __builtin_amdgcn_s_barrier();
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
 
-  // The tile leaves through LDS, an A half (128 x 256 fp32, 16 rows an object)
-  // at a time, so that memory sees whole rows: a lane then holds four columns
-  // and a wave a row of the tile (paired: two rows, each lane its gate and up
-  // columns). 16-byte piece c of a row lies at c ^ (row % 16).
+  // an A half at a time: 128 rows of 256 columns, 16 an object
   const int r = lane & 15, q = lane >> 4;
   uint8_t* const w0 = wm ? sb1 : sa0;
   uint8_t* const w1 = wm ? sc1 : sb0;
@@ -771,42 +773,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     }
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
-    const int64_t mw = m0 + h * HR + wave * 16;
-    if constexpr (kPaired) {
-      const int64_t n = n0 + 4 * (lane & 31);
-#pragma unroll
-      for (int t = 0; t < 8; t += 4) {
-        f32x4 g[4], u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int x = 2 * (t + k) + (lane >> 5);
-          g[k] = *(const f32x4*)(mine + x * 1024 + (((lane & 31) ^ x) * 16));
-          u[k] = *(const f32x4*)(mine + x * 1024 + ((((lane & 31) + 32) ^ x) * 16));
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t m = mw + 2 * (t + k) + (lane >> 5);
-          const bool in = m < p.M && n < p.N;
-          if constexpr (EPI == kSwigluMx) {
-            emit_mx(p, m, n, g[k], u[k], in);
-          } else {
-            if (in) emit<EPI>(p, m, n, g[k], u[k]);
-          }
-        }
-      }
-    } else {
-      const int64_t n = n0 + 4 * lane;
-#pragma unroll
-      for (int t = 0; t < 16; t += 8) {
-        f32x4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          v[k] = *(const f32x4*)(mine + (t + k) * 1024 + ((lane ^ (t + k)) * 16));
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (mw + t + k < p.M && n < p.N) emit<EPI>(p, mw + t + k, n, v[k], v[k]);
-      }
-    }
+    store_rows<EPI, 256>(p, mine, m0 + h * HR + wave * 16, n0, lane);
     wait_lgkm0();
   }
 #endif
@@ -818,36 +785,44 @@ struct Cut {
   int tile = 0, shares = 1, share = 1;
   int64_t groups = 0;
 };
-Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, bool mx) {
+// Microseconds a stage of K takes one round of work-groups on 256 CUs, and what
+// a work-group costs besides. Measured on products of 20 to 4096 rows at
+// widths 256 to 7168 (bf16 with K contiguous operands; with a row contiguous
+// one; MXFP4).
+struct Rate {
+  double stage[3], fixed[3];
+};
+constexpr Rate kRates[3] = {{{0.62, 0.88, 1.42}, {4.5, 4.5, 7.0}},
+                            {{0.92, 0.85, 1.42}, {4.0, 5.0, 7.0}},
+                            {{0.85, 1.20, 1.80}, {4.5, 4.5, 8.0}}};
+// The cheapest cut. Shares of K cost a launch and the sums' way to memory and
+// back (about 4 TB/s); of equals the larger tile.
+Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx) {
   const bool paired = epi == kSwiglu || epi == kSwigluMx;
+  const Rate& rate = kRates[mx ? 2 : layout == kNT ? 0 : 1];
+  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
   auto tiles = [&](int64_t rows, int64_t cols) {
     if (paired) cols /= 2;
     return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
   };
-  auto rounds = [](int64_t n) { return (double)((n + 255) / 256); };
-  const int64_t n0 = tiles(128, 128), n1 = tiles(128, 256), n2 = tiles(256, 256);
-  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  // Microseconds on 256 CUs: rounds of work-groups times the stages of K and
-  // what a work-group costs besides; shares of K add their sums' way through
-  // memory (about 4 TB/s) and a launch. Measured: see the table of stage times.
-  const double fixed = 5.0;
-  auto time = [&](double n, double per_stage, double st) { return n * (st * per_stage + fixed); };
-  Cut c;
-  c.groups = n0;
-  double best = 1e30;
-  for (int shares = 1; shares <= 32 && (shares == 1 || shares <= stages / 2); ++shares) {
-    const int64_t share = (stages + shares - 1) / shares;
-    if (share * (shares - 1) >= stages && shares > 1) continue;  // an empty last share
-    const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
-    const double t = time(rounds(n0 * shares), 0.6, (double)share) +
-                     (shares > 1 ? 4.0 + 2 * sums / 4e6 : 0.0);
-    if (t < best) best = t, c.tile = 0, c.shares = shares, c.share = (int)(share ? share : 1);
-    if (n0 * shares >= 512) break;
+  auto time = [&](int tile, int64_t groups, int64_t st) {
+    return (double)((groups + 255) / 256) * (st * rate.stage[tile] + rate.fixed[tile]);
+  };
+  const int64_t n[3] = {tiles(128, 128), tiles(128, 256), tiles(256, 256)};
+  Cut best{2, 1, (int)stages, n[2]};
+  double least = time(2, n[2], stages);
+  if (time(1, n[1], stages) < least) {
+    least = time(1, n[1], stages);
+    best = Cut{1, 1, (int)stages, n[1]};
   }
-  const double t1 = time(rounds(n1), 1.19, (double)stages), t2 = time(rounds(n2), 1.45, (double)stages);
-  if (t1 <= best) best = t1, c = Cut{1, 1, (int)stages, n1};
-  if (t2 <= best) best = t2, c = Cut{2, 1, (int)stages, n2};
-  return c;
+  for (int shares = 1; shares <= 32 && n[0] * shares <= 1024; ++shares) {
+    const int64_t share = (stages + shares - 1) / shares;
+    if (shares > 1 && (2 * shares > stages || share * (shares - 1) >= stages)) continue;
+    const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
+    const double t = time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : 0.0);
+    if (t < least) least = t, best = Cut{0, shares, (int)share, n[0]};
+  }
+  return best;
 }
 
 template <Epilogue EPI>
@@ -858,11 +833,12 @@ hipError_t join(const Product& p, const void* sums, int shares, hipStream_t stre
   return hipGetLastError();
 }
 
-template <Kind KA, Kind KB, bool MX, Epilogue EPI>
+template <Layout L, bool MX, Epilogue EPI>
 hipError_t launch(const Product& p, void* split, hipStream_t stream) {
+  constexpr Kind KA = L == kTN ? RC : KC, KB = L == kNT ? KC : RC;
   constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  const Cut c = cut_of(EPI, p.M, p.N, p.K, MX);
+  const Cut c = cut_of(EPI, p.M, p.N, p.K, L, MX);
   if (c.groups > 0x7fffff) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)c.groups, c.shares);
   if (c.tile == 2) {
@@ -884,31 +860,32 @@ hipError_t launch(const Product& p, void* split, hipStream_t stream) {
 
 }  // namespace
 
-size_t product_workspace(Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx) {
-  const Cut c = cut_of(epilogue, M, N, K, mx);
+size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
+                         bool mx) {
+  const Cut c = cut_of(epilogue, M, N, K, layout, mx);
   const bool paired = epilogue == kSwiglu || epilogue == kSwigluMx;
   return c.shares > 1 ? (size_t)c.shares * M * N * (paired ? 8 : 4) : 0;
 }
 
 hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,
                           hipStream_t stream) {
-  if (layout == kNT && epilogue == kSwiglu) return launch<KC, KC, false, kSwiglu>(p, split, stream);
+  if (layout == kNT && epilogue == kSwiglu) return launch<kNT, false, kSwiglu>(p, split, stream);
   if (layout == kNT && epilogue == kStoreBf16)
-    return launch<KC, KC, false, kStoreBf16>(p, split, stream);
+    return launch<kNT, false, kStoreBf16>(p, split, stream);
   if (layout == kNN && epilogue == kSwigluGrad)
-    return launch<KC, RC, false, kSwigluGrad>(p, split, stream);
+    return launch<kNN, false, kSwigluGrad>(p, split, stream);
   if (layout == kNN && epilogue == kStoreBf16)
-    return launch<KC, RC, false, kStoreBf16>(p, split, stream);
+    return launch<kNN, false, kStoreBf16>(p, split, stream);
   if (layout == kTN && epilogue == kStoreBf16)
-    return launch<RC, RC, false, kStoreBf16>(p, split, stream);
+    return launch<kTN, false, kStoreBf16>(p, split, stream);
   return hipErrorInvalidValue;
 }
 
 hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
                              hipStream_t stream) {
-  if (epilogue == kStoreBf16) return launch<KC, KC, true, kStoreBf16>(p, split, stream);
-  if (epilogue == kStoreF32) return launch<KC, KC, true, kStoreF32>(p, split, stream);
-  if (epilogue == kSwigluMx) return launch<KC, KC, true, kSwigluMx>(p, split, stream);
+  if (epilogue == kStoreBf16) return launch<kNT, true, kStoreBf16>(p, split, stream);
+  if (epilogue == kStoreF32) return launch<kNT, true, kStoreF32>(p, split, stream);
+  if (epilogue == kSwigluMx) return launch<kNT, true, kSwigluMx>(p, split, stream);
   return hipErrorInvalidValue;
 }
 

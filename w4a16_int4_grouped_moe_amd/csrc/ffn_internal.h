@@ -57,7 +57,8 @@ hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
                              hipStream_t stream);
 // Where few tiles would run a long K, its shares go to several work-groups and
 // their sums here; 0 where they do not.
-size_t product_workspace(Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
+size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
+                         bool mx);
 
 // The same products for a few rows (ffn_small.hip), both operands K contiguous
 // and dense. A: as the product takes it, or rows to be quantised to MXFP4.
