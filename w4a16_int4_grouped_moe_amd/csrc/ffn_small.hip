@@ -33,50 +33,47 @@ __host__ __device__ inline int code_stride(int64_t K) { return (int)((K / 2 + 25
 __host__ __device__ inline int byte_stride(int64_t K) { return (int)((K / 32 + 7) / 8 * 8 + 4); }
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// 32 values, four (bf16) or eight (fp32) 16-byte pieces -> codes, scale byte
+template <int CTRL>
+__device__ __forceinline__ uint32_t other_max(uint32_t v) {
+  const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+  return o > v ? o : v;
+}
+// One 16-byte piece of a block, the neighbouring four (bf16) or eight (fp32)
+// lanes holding the whole: its codes (32 or 16 bits) and the block's scale.
 template <bool F32>
-__device__ __forceinline__ u32x4 quantize_block(const u32x4* v, uint32_t* scale) {
-  u32x4 c;
+__device__ __forceinline__ uint32_t quantize_piece(const u32x4& v, uint32_t* scale) {
+  uint32_t top;
   if constexpr (F32) {
-    uint32_t top = 0;
+    top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b = v[i][j] & 0x7fffffffu;
-        top = b > top ? b : top;
-      }
-    *scale = mx_scale(top >> 23);
-    const float unit = mx_unit(*scale);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f32x4 a = __builtin_bit_cast(f32x4, v[2 * i]), b = __builtin_bit_cast(f32x4, v[2 * i + 1]);
-      uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a[0], a[1], unit, 0);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, a[2], a[3], unit, 1);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[0], b[1], unit, 2);
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, b[2], b[3], unit, 3);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t b = v[j] & 0x7fffffffu;
+      top = b > top ? b : top;
     }
   } else {
-    u16x2 top = {0, 0};
+    u16x2 m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        top = __builtin_elementwise_max(top,
-                                        __builtin_bit_cast(u16x2, (uint32_t)(v[i][j] & 0x7fff7fffu)));
-    *scale = mx_scale((uint32_t)(top[0] > top[1] ? top[0] : top[1]) >> 7);
-    const float unit = mx_unit(*scale);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t w = 0;
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][0]), unit, 0);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][1]), unit, 1);
-      w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][2]), unit, 2);
-      c[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, (uint32_t)v[i][3]), unit, 3);
-    }
+    for (int j = 0; j < 4; ++j)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)(v[j] & 0x7fff7fffu)));
+    top = m[0] > m[1] ? m[0] : m[1];
   }
-  if (*scale == 255) c = u32x4{0, 0, 0, 0};
-  return c;
+  top = other_max<0xB1>(top);                     // lane ^ 1
+  top = other_max<0x4E>(top);                     // lane ^ 2
+  if constexpr (F32) top = other_max<0x141>(top);  // the other four of eight
+  *scale = mx_scale(top >> (F32 ? 23 : 7));
+  const float unit = mx_unit(*scale);
+  uint32_t c = 0;
+  if constexpr (F32) {
+    const f32x4 f = __builtin_bit_cast(f32x4, v);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[0], f[1], unit, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, f[2], f[3], unit, 1);
+  } else {
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)v[0]), unit, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)v[1]), unit, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)v[2]), unit, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)v[3]), unit, 3);
+  }
+  return *scale == 255 ? 0 : c;
 }
 #endif
 
@@ -142,36 +139,49 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
   if constexpr (AK == kAsIs) {
     fill();
   } else {
-    // blocks of all rows over the threads, up to `kAtOnce` each at a time; the
-    // last round's loads go out ahead of the ring's. Blocks past K (to a whole
-    // stage) get a finite scale.
-    constexpr int kPieces = AK == kFromF32 ? 8 : 4;
-    constexpr int kAtOnce = AK == kFromF32 ? 1 : 2;
-    const int per = (blocks + 7) / 8 * 8, total = M * per;
+    // The rows' 16-byte pieces over the threads: 2^sh threads a row (all of them
+    // where it has more pieces), kAtOnce loads each under way, the last ones
+    // ahead of the ring's. Pieces past K, to a whole stage, are zeros with a
+    // finite scale.
+    constexpr int kSize = AK == kFromF32 ? 4 : 2;       // bytes of a value
+    constexpr int kLanes = 2 * kSize;                   // lanes of a block
+    constexpr int kAtOnce = 4;
+    const int have = blocks * kLanes, pieces = (blocks + 7) / 8 * 8 * kLanes;
+    const int sh = pieces >= kThreads ? 9 : 32 - __builtin_clz(pieces - 1);
+    const int across = 1 << sh, down = kThreads >> sh;  // threads a row, rows at once
+    const int t0 = threadIdx.x >> sh, c0 = threadIdx.x & (across - 1);
+    const int turns = (pieces + across - 1) >> sh;      // a row's
+    const int total = (M + down - 1) / down * turns;
     const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)p.a, 0, M * blocks * (16 * kPieces), kBufferFlags);
-    for (int first = threadIdx.x;; first += kAtOnce * kThreads) {
-      u32x4 v[kAtOnce][kPieces];
+        (void*)p.a, 0, M * have * 16, kBufferFlags);
+    int t = t0, c = c0, turn = 0;
+    auto next = [&](int& t, int& c, int& turn) {
+      c += across;
+      if (++turn == turns) turn = 0, c = c0, t += down;
+    };
+    for (int first = 0;; first += kAtOnce) {
+      u32x4 v[kAtOnce];
+      int tl = t, cl = c, turnl = turn;
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int u = first + j * kThreads, t = u / per, b = u - t * per;
-        const uint32_t off = u < total && b < blocks
-                                 ? (uint32_t)(t * blocks + b) * (16 * kPieces) : kOut;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          v[j][i] = __builtin_amdgcn_raw_buffer_load_b128(ares, off == kOut ? kOut : off + 16 * i, 0, 0);
+        const bool in = first + j < total && tl < M && cl < have;
+        v[j] = __builtin_amdgcn_raw_buffer_load_b128(ares, in ? (tl * have + cl) * 16 : kOut, 0, 0);
+        next(tl, cl, turnl);
       }
-      const bool last = uniform(first - threadIdx.x) + kAtOnce * kThreads >= total;
+      const bool last = first + kAtOnce >= total;
       if (last) fill();
 #pragma unroll
       for (int j = 0; j < kAtOnce; ++j) {
-        const int u = first + j * kThreads, t = u / per, b = u - t * per;
         uint32_t scale;
-        const u32x4 c = quantize_block<AK == kFromF32>(v[j], &scale);
-        if (u < total) {
-          *(u32x4*)(qa + t * cstride + 16 * b) = c;
-          qbytes[t * bstride + b] = (uint8_t)scale;
+        const uint32_t code = quantize_piece<AK == kFromF32>(v[j], &scale);
+        if (first + j < total && t < M && c < pieces) {
+          if constexpr (AK == kFromF32)
+            *(uint16_t*)(qa + t * cstride + 2 * c) = (uint16_t)code;
+          else
+            *(uint32_t*)(qa + t * cstride + 4 * c) = code;
+          if (c % kLanes == 0) qbytes[t * bstride + c / kLanes] = (uint8_t)scale;
         }
+        next(t, c, turn);
       }
       if (last) break;
     }
