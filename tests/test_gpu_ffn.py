@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 BF, U, FN = 2.0 ** -8, 2.0 ** -24, 2.0 ** -20
 SHAPES = [(1, 8, 8), (1, 64, 32), (2, 72, 40), (5, 136, 264), (17, 64, 2048), (64, 256, 128),
           (127, 128, 128), (129, 520, 72), (200, 1000, 680), (256, 640, 384), (300, 64, 64),
-          (33, 7168, 256)]
+          (33, 7168, 256), (31, 696, 256), (48, 1000, 680), (64, 2048, 512)]
 
 
 def inputs(T, H, I, seed=0, scale=1.0):

@@ -105,7 +105,7 @@ def test_every_code_and_scale_reads_back():
 
 
 PRODUCTS = [(1, 8, 32), (1, 4096, 7168), (2, 264, 992), (7, 72, 256), (16, 512, 1024), (33, 136, 64),
-            (64, 128, 2048), (128, 128, 256), (129, 1000, 480), (300, 264, 7168), (777, 72, 992)]
+            (64, 128, 2048), (128, 128, 256), (129, 1000, 480), (300, 264, 7168), (777, 72, 992), (17, 1000, 992), (48, 264, 704), (64, 4096, 1024)]
 
 
 def product_close(got, a, b, n, rounded):
@@ -158,7 +158,8 @@ def test_scales_of_all_sizes(M):
     assert torch.equal(marked[keep], out[keep])
 
 
-FFN = [(1, 32, 32), (1, 7168, 256), (3, 96, 64), (8, 512, 256), (40, 992, 160), (130, 256, 736), (257, 64, 96)]
+FFN = [(1, 32, 32), (1, 7168, 256), (3, 96, 64), (8, 512, 256), (40, 992, 160), (130, 256, 736), (257, 64, 96),
+       (20, 704, 256), (57, 1024, 2048), (64, 512, 160), (16, 7168, 2048)]
 
 
 @pytest.mark.parametrize("T,H,I", FFN)

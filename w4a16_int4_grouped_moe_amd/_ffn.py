@@ -213,7 +213,9 @@ def mxfp4_quantize(x, codes=None, scales=None) -> Mxfp4:
     scales = _result(scales, "scales", torch.uint8, (rows, width // MX_BLOCK), dev)
     _launch(dev, _library().moe_mxfp4_quantize, x.data_ptr(), kind, rows, width,
             codes.data_ptr(), scales.data_ptr())
-    return Mxfp4(codes, scales)
+    q = object.__new__(Mxfp4)  # checked above
+    q._codes, q._scales, q._shape = codes, scales, (rows, width)
+    return q
 
 
 def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):

@@ -58,20 +58,52 @@ struct MxRegion {
   size_t bytes() const { return codes + scales; }
 };
 
-// The block's two products as the few-row kernels take them
-bool few_tokens(const moe_ffn_problem* p, bool mx) {
+// How a forward pass runs its products: tiled, or as the few-row kernels take
+// them; in MXFP4 these quantise A themselves, or find x quantised by a launch
+// ahead (more than 16 rows).
+enum Path { kTiled, kFew, kFewPrepared };
+
+Path path_of(const moe_ffn_problem* p, bool mx) {
   Product up{}, down{};
   up.M = down.M = p->num_tokens;
   up.N = down.K = p->inter;
   up.K = down.N = p->hidden;
-  return ffn::rows_fit(up, mx, mx ? ffn::kABf16 : ffn::kAAsIs, true) &&
-         ffn::rows_fit(down, mx, mx ? ffn::kAF32 : ffn::kAAsIs, false);
+  if (!ffn::rows_fit(down, mx, mx ? ffn::kAF32 : ffn::kAAsIs, false)) return kTiled;
+  Path few = kFew;
+  if (!ffn::rows_fit(up, mx, mx ? ffn::kABf16 : ffn::kAAsIs, true)) {
+    if (!mx || !ffn::rows_fit(up, mx, ffn::kAAsIs, true)) return kTiled;
+    few = kFewPrepared;
+  }
+  if (p->num_tokens <= 16 && few == kFew) return few;
+  const ffn::Epilogue swiglu = mx ? ffn::kSwigluMx : ffn::kSwiglu;
+  const double tiled =
+      ffn::product_time(ffn::kNT, swiglu, up.M, up.N, up.K, mx) +
+      ffn::product_time(ffn::kNT, ffn::kStoreBf16, down.M, down.N, down.K, mx);
+  const double rows = ffn::rows_time(up, mx, ffn::kAAsIs, true) +
+                      ffn::rows_time(down, mx, mx ? ffn::kAF32 : ffn::kAAsIs, false);
+  return rows < tiled ? few : kTiled;
 }
-bool few_rows(int64_t rows, int32_t cols, int32_t width, bool quantize) {
+
+Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize) {
   Product d{};
   d.M = rows, d.N = cols, d.K = width;
-  return ffn::rows_fit(d, true, quantize ? ffn::kABf16 : ffn::kAAsIs, false);
+  if (ffn::rows_fit(d, true, quantize ? ffn::kABf16 : ffn::kAAsIs, false) && rows <= 16)
+    return kFew;
+  if (!ffn::rows_fit(d, true, ffn::kAAsIs, false)) return kTiled;
+  const double tiled = ffn::product_time(ffn::kNT, ffn::kStoreF32, rows, cols, width, true);
+  // the given scales of a tiled product go through a launch too
+  return ffn::rows_time(d, true, ffn::kAAsIs, false) < tiled + (quantize ? 0.0 : 3.0)
+             ? quantize ? kFewPrepared : kFew
+             : kTiled;
 }
+
+// x in MXFP4 as the few-row kernels read it: codes, then K/32 bytes a row
+struct RowRegion {
+  size_t codes, scales;
+  RowRegion(int64_t rows, int32_t width)
+      : codes(region(rows * (width / 2))), scales(region(rows * (width / 32))) {}
+  size_t bytes() const { return codes + scales; }
+};
 
 // The shares' sums of a pass's products, which follow each other: one region
 size_t split_of(const moe_ffn_problem* p, int pass) {
@@ -99,8 +131,10 @@ size_t workspace_of(const moe_ffn_problem* p, int pass) {
   if (pass == MOE_FFN_BACKWARD)
     return region(4 * T * I) + region(2 * T * I) + split_of(p, pass);
   if (pass == MOE_FFN_FORWARD)
-    return region(2 * T * I) + (few_tokens(p, false) ? 0 : split_of(p, pass));
-  if (few_tokens(p, true)) return region(4 * T * I);
+    return region(2 * T * I) + (path_of(p, false) == kTiled ? split_of(p, pass) : 0);
+  const Path path = path_of(p, true);
+  if (path != kTiled)
+    return region(4 * T * I) + (path == kFewPrepared ? RowRegion(T, p->hidden).bytes() : 0);
   return MxRegion(T, p->hidden).bytes() + MxRegion(T, p->inter).bytes() +
          region(ffn::scale_bytes(2 * I, H)) + region(ffn::scale_bytes(H, I)) + split_of(p, pass);
 }
@@ -135,7 +169,7 @@ int moe_ffn_forward(const void* x, const void* w13, const void* w2, void* out, f
   up.aux = gate_up;
   Product down{workspace, w2, nullptr, nullptr, 2 * I, 2 * I, T, p->hidden, I};
   down.out = out;
-  const bool few = few_tokens(p, false);
+  const bool few = path_of(p, false) != kTiled;
   char* split = (char*)workspace + region(2 * T * I);
   const hipError_t e = few ? ffn::launch_rows(ffn::kSwiglu, up, s)
                            : ffn::launch_product(ffn::kNT, ffn::kSwiglu, up, split, s);
@@ -221,7 +255,9 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   if (st != MOE_OK) return st;
   if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
   *bytes = 0;
-  if (rows == 0 || few_rows(rows, cols, width, quantize)) return MOE_OK;
+  const Path path = rows == 0 ? kFew : path_of(rows, cols, width, quantize);
+  if (path == kFewPrepared) *bytes = RowRegion(rows, width).bytes();
+  if (path != kTiled) return MOE_OK;
   *bytes = (quantize ? MxRegion(rows, width).bytes() : region(ffn::scale_bytes(rows, width))) +
            region(ffn::scale_bytes(cols, width)) +
            region(ffn::product_workspace(ffn::kNT, ffn::kStoreF32, rows, cols, width, true));
@@ -243,7 +279,17 @@ int moe_mxfp4_matmul(const void* a, const uint8_t* a_scales, const uint8_t* b,
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   const ffn::Epilogue store = out_type == MOE_TYPE_FP32 ? ffn::kStoreF32 : ffn::kStoreBf16;
-  if (few_rows(rows, cols, width, !a_scales)) {
+  const Path path = path_of(rows, cols, width, !a_scales);
+  if (path != kTiled) {
+    if (path == kFewPrepared) {
+      uint8_t* codes = (uint8_t*)workspace;
+      uint8_t* scales = codes + RowRegion(rows, width).codes;
+      const hipError_t e =
+          ffn::launch_mx_quantize(a, MOE_TYPE_BF16, rows, width, codes, scales, s);
+      if (e != hipSuccess) return done(e);
+      a = codes;
+      a_scales = scales;
+    }
     Product d{a, b, a_scales, b_scales, width / 2, width / 2, rows, cols, width};
     d.out = out;
     return done(ffn::launch_rows_mx(store, a_scales ? ffn::kAAsIs : ffn::kABf16, d, s));
@@ -281,10 +327,20 @@ int moe_mxfp4_ffn_forward(const void* x, const uint8_t* w13, const uint8_t* w13_
   const int64_t T = p->num_tokens;
   const int32_t H = p->hidden, I = p->inter;
   hipStream_t s = (hipStream_t)stream;
-  if (few_tokens(p, true)) {
+  const Path path = path_of(p, true);
+  if (path != kTiled) {
     Product up{x, w13, nullptr, w13_scales, H / 2, H / 2, T, I, H};
     up.out = workspace;
-    const hipError_t e = ffn::launch_rows_mx(ffn::kSwigluF32, ffn::kABf16, up, s);
+    hipError_t e = hipSuccess;
+    if (path == kFewPrepared) {
+      uint8_t* codes = (uint8_t*)workspace + region(4 * T * I);
+      uint8_t* scales = codes + RowRegion(T, H).codes;
+      e = ffn::launch_mx_quantize(x, MOE_TYPE_BF16, T, H, codes, scales, s);
+      up.a = codes;
+      up.a_scales = scales;
+    }
+    if (e == hipSuccess)
+      e = ffn::launch_rows_mx(ffn::kSwigluF32, path == kFew ? ffn::kABf16 : ffn::kAAsIs, up, s);
     if (e != hipSuccess) return done(e);
     Product down{workspace, w2, nullptr, w2_scales, I / 2, I / 2, T, H, I};
     down.out = out;

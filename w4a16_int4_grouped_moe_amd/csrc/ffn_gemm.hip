@@ -784,6 +784,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 struct Cut {
   int tile = 0, shares = 1, share = 1;
   int64_t groups = 0;
+  double time = 0;  // estimate
 };
 // Microseconds a stage of K takes one round of work-groups on 256 CUs, and what
 // a work-group costs besides. Measured on products of 20 to 4096 rows at
@@ -822,6 +823,7 @@ Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx
     const double t = time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : 0.0);
     if (t < least) least = t, best = Cut{0, shares, (int)share, n[0]};
   }
+  best.time = least;
   return best;
 }
 
@@ -865,6 +867,10 @@ size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N,
   const Cut c = cut_of(epilogue, M, N, K, layout, mx);
   const bool paired = epilogue == kSwiglu || epilogue == kSwigluMx;
   return c.shares > 1 ? (size_t)c.shares * M * N * (paired ? 8 : 4) : 0;
+}
+
+double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx) {
+  return cut_of(epilogue, M, N, K, layout, mx).time;
 }
 
 hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,

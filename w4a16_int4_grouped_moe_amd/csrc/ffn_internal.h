@@ -63,10 +63,13 @@ size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N,
 // The same products for a few rows (ffn_small.hip), both operands K contiguous
 // and dense. A: as the product takes it, or rows to be quantised to MXFP4.
 // Here a row's scales are K/32 bytes, at any address. rows_fit: whether the
-// kernel takes the problem (at most 16 rows, B below 2 GiB, a quantised A that
-// fits LDS).
+// kernel takes the problem (at most 64 rows, 16 of bf16 to quantise; B below
+// 2 GiB; a quantised A that fits LDS). The times are estimates in microseconds
+// by which a call chooses.
 enum AType { kAAsIs = 0, kABf16 = 1, kAF32 = 2 };
 bool rows_fit(const Product& p, bool mx, AType a, bool paired);
+double rows_time(const Product& p, bool mx, AType a, bool paired);
+double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
 hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream);
 hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream);
 

@@ -1,8 +1,8 @@
-// ffn_small.hip -- the K-contiguous products for at most 16 rows (gfx950):
+// ffn_small.hip -- the K-contiguous products for at most 64 rows (gfx950):
 // decoding, where the time is the weights' way from memory.
 //
 // A work-group owns 16 weight rows (SwiGLU: 8 gate rows and their 8 up rows)
-// and all rows of A: one 16 x 16 MFMA tile. Its eight waves take the stages of
+// and all rows of A: one, two or four 16 x 16 MFMA tiles. Its eight waves take the stages of
 // K (128 bytes of a row) in turn, so that together they read whole kilobytes of
 // each row; a wave keeps a ring of stages in flight in registers, loads
 // straight into the MFMA's layout (lane (r = lane % 16, q = lane / 16): piece
@@ -12,7 +12,7 @@
 // An A that is to be quantised (bf16, or the fp32 h of the block) is quantised
 // by the work-group into LDS: its loads go out first, then the ring's, so the
 // conversion runs under the first weights' latency. Every work-group repeats
-// it (at most 16 rows), which costs less than a launch of its own.
+// it, which for a few rows costs less than a launch of its own.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,7 +25,7 @@ namespace ffn {
 namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kMaxRows = 16;
+constexpr int kMaxRows = 64;
 constexpr int kMxLds = 64 * 1024;  // quantised A in LDS, codes and scales
 
 // LDS rows of quantised A: 16 rows at one offset lie in distinct banks
@@ -80,11 +80,13 @@ __device__ __forceinline__ uint32_t quantize_piece(const u32x4& v, uint32_t* sca
 // A: as the product's operands (kAsIs), or bf16 / fp32 rows to quantise
 enum AKind { kAsIs = 0, kFromBf16 = 1, kFromF32 = 2 };
 
-template <AKind AK, bool MX, Epilogue EPI>
-__global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
+// MT: 16-row tiles of A
+template <AKind AK, bool MX, Epilogue EPI, int MT>
+__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(const Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluF32;
-  constexpr int kD = AK == kFromF32 ? 3 : 5;  // stages in flight per wave
+  // stages in flight per wave, by what their registers leave
+  constexpr int kD = AK == kFromF32 ? 3 : MT == 1 ? 5 : MT == 2 ? 4 : 3;
   // quantised A (codes, then bytes), and in its place at the end the waves' sums
   extern __shared__ __attribute__((aligned(16))) uint8_t qa[];
   float* const sums = (float*)qa;
@@ -99,8 +101,12 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
   const int rows = kPaired ? 2 * N : N;
   const uint32_t woff = row < rows ? (uint32_t)row * kb + 16 * q : kOut;
   const uint32_t wsoff = row < rows ? (uint32_t)row * blocks + q : kOut;
-  const uint32_t xoff = r < M ? (uint32_t)r * kb + 16 * q : kOut;
-  const uint32_t xsoff = r < M ? (uint32_t)r * blocks + q : kOut;
+  uint32_t xoff[MT], xsoff[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    xoff[i] = 16 * i + r < M ? (uint32_t)(16 * i + r) * kb + 16 * q : kOut;
+    xsoff[i] = 16 * i + r < M ? (uint32_t)(16 * i + r) * blocks + q : kOut;
+  }
   const __amdgpu_buffer_rsrc_t wres =
       __builtin_amdgcn_make_buffer_rsrc((void*)p.b, 0, rows * kb, kBufferFlags);
   const __amdgpu_buffer_rsrc_t wsres =
@@ -110,20 +116,24 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
   const __amdgpu_buffer_rsrc_t xsres = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.a_scales, 0, MX && AK == kAsIs ? M * blocks : 0, kBufferFlags);
 
-  u32x4 w[kD][2], x[kD][2];
-  uint32_t ws[kD][2], xs[kD][2];
+  u32x4 w[kD][2], x[kD][2][MT];
+  uint32_t ws[kD][2], xs[kD][2][MT];
   auto load = [&](int d, int s) {
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       const int at = s * 128 + st * 64;
       const bool in = at + 16 * q < kb;
       if constexpr (AK == kAsIs)
-        x[d][st] = __builtin_amdgcn_raw_buffer_load_b128(xres, in ? xoff + at : kOut, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          x[d][st][i] = __builtin_amdgcn_raw_buffer_load_b128(xres, in ? xoff[i] + at : kOut, 0, 0);
       w[d][st] = __builtin_amdgcn_raw_buffer_load_b128(wres, in ? woff + at : kOut, 0, 0);
       if constexpr (MX) {
         const int b = 8 * s + 4 * st;
         if constexpr (AK == kAsIs)
-          xs[d][st] = __builtin_amdgcn_raw_buffer_load_b8(xsres, in ? xsoff + b : kOut, 0, 0);
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+            xs[d][st][i] = __builtin_amdgcn_raw_buffer_load_b8(xsres, in ? xsoff[i] + b : kOut, 0, 0);
         ws[d][st] = __builtin_amdgcn_raw_buffer_load_b8(wsres, in ? wsoff + b : kOut, 0, 0);
       }
     }
@@ -135,7 +145,6 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
 
   const int cstride = code_stride(p.K), bstride = byte_stride(p.K);
   uint8_t* qbytes = qa + M * cstride;
-  const int rq = r < M ? r : M - 1;  // rows past the last: any, their sums are not stored
   if constexpr (AK == kAsIs) {
     fill();
   } else {
@@ -189,84 +198,127 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(const Product p) {
     __builtin_amdgcn_s_barrier();
   }
 
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s = wave; s < stages; s += kD * kWaves) {
 #pragma unroll
     for (int d = 0; d < kD; ++d) {
       const int at = s + d * kWaves;
       if (at >= stages) break;  // uniform: a wave's stages are its own
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
-        if constexpr (MX) {
-          u32x4 xv;
-          uint32_t xb;
-          if constexpr (AK == kAsIs) {
-            xv = x[d][st], xb = xs[d][st];
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          if constexpr (MX) {
+            u32x4 xv;
+            uint32_t xb;
+            if constexpr (AK == kAsIs) {
+              xv = x[d][st][i], xb = xs[d][st][i];
+            } else {
+              // rows past the last: any, their sums are not stored
+              const int row = 16 * i + r < M ? 16 * i + r : M - 1;
+              xv = *(const u32x4*)(qa + row * cstride + at * 128 + st * 64 + 16 * q);
+              xb = qbytes[row * bstride + 8 * at + 4 * st + q];
+            }
+            acc[i] = mfma_mx<0, 0>(w[d][st], xv, acc[i], ws[d][st], xb);
           } else {
-            xv = *(const u32x4*)(qa + rq * cstride + at * 128 + st * 64 + 16 * q);
-            xb = qbytes[rq * bstride + 8 * at + 4 * st + q];
+            acc[i] = mfma(w[d][st], x[d][st][i], acc[i]);
           }
-          acc = mfma_mx<0, 0>(w[d][st], xv, acc, ws[d][st], xb);
-        } else {
-          acc = mfma(w[d][st], x[d][st], acc);
         }
-      }
       load(d, at + kD * kWaves);
     }
   }
 
-  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row r
+  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row 16 i + r
   if constexpr (AK != kAsIs) __syncthreads();  // A is read to the end
-  *(f32x4*)&sums[wave * 256 + r * 16 + 4 * q] = acc;
-  __syncthreads();
-  const int i = threadIdx.x;
-  if constexpr (kPaired) {
-    const int m = i >> 3, j = i & 7;
-    if (i >= 128 || m >= M) return;
-    float g = 0.f, u = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) g += sums[k * 256 + m * 16 + j], u += sums[k * 256 + m * 16 + 8 + j];
-    const float h = g * sigmoid(g) * u;
-    const int64_t at = (int64_t)m * N + n0 + j;
-    if constexpr (EPI == kSwigluF32) {
-      ((float*)p.out)[at] = h;
-    } else {
-      ((uint16_t*)p.out)[at] = (uint16_t)pack2(h, 0.f);
-      if (p.aux) {
-        float* gu = (float*)p.aux + (int64_t)m * 2 * N + n0 + j;
-        gu[0] = g;
-        gu[N] = u;
+  for (int i = 0; i < MT; ++i)
+    *(f32x4*)&sums[(wave * MT + i) * 256 + r * 16 + 4 * q] = acc[i];
+  __syncthreads();
+  if constexpr (kPaired) {
+    for (int i = threadIdx.x; i < 128 * MT; i += kThreads) {
+      const int m = i >> 3, j = i & 7;
+      if (m >= M) break;
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        g += sums[k * MT * 256 + m * 16 + j];
+        u += sums[k * MT * 256 + m * 16 + 8 + j];
+      }
+      const float h = g * sigmoid(g) * u;
+      const int64_t at = (int64_t)m * N + n0 + j;
+      if constexpr (EPI == kSwigluF32) {
+        ((float*)p.out)[at] = h;
+      } else {
+        ((uint16_t*)p.out)[at] = (uint16_t)pack2(h, 0.f);
+        if (p.aux) {
+          float* gu = (float*)p.aux + (int64_t)m * 2 * N + n0 + j;
+          gu[0] = g;
+          gu[N] = u;
+        }
       }
     }
   } else {
-    const int m = i >> 4, n = n0 + (i & 15);
-    if (i >= 256 || m >= M || n >= N) return;
-    float v = 0.f;
+    for (int i = threadIdx.x; i < 256 * MT; i += kThreads) {
+      const int m = i >> 4, n = n0 + (i & 15);
+      if (m >= M) break;
+      if (n >= N) continue;
+      float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += sums[k * 256 + i];
-    if constexpr (EPI == kStoreF32)
-      ((float*)p.out)[(int64_t)m * N + n] = v;
-    else
-      ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
+      for (int k = 0; k < kWaves; ++k) v += sums[k * MT * 256 + i];
+      if constexpr (EPI == kStoreF32)
+        ((float*)p.out)[(int64_t)m * N + n] = v;
+      else
+        ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
+    }
   }
 #endif
 }
 
-template <AKind AK, bool MX, Epilogue EPI>
-hipError_t launch(const Product& p, hipStream_t stream) {
+template <AKind AK, bool MX, Epilogue EPI, int MT>
+hipError_t launch_tiles(const Product& p, hipStream_t stream) {
   const unsigned groups = EPI == kSwiglu || EPI == kSwigluF32 ? (p.N + 7) / 8 : (p.N + 15) / 16;
   const size_t a = AK == kAsIs ? 0 : p.M * (code_stride(p.K) + byte_stride(p.K));
-  const size_t lds = std::max<size_t>(a, kWaves * 256 * sizeof(float));
-  hipLaunchKernelGGL((rows_kernel<AK, MX, EPI>), dim3(groups), dim3(kThreads), lds, stream, p);
+  const size_t lds = std::max<size_t>(a, kWaves * MT * 256 * sizeof(float));
+  hipLaunchKernelGGL((rows_kernel<AK, MX, EPI, MT>), dim3(groups), dim3(kThreads), lds, stream,
+                     p);
   return hipGetLastError();
+}
+template <AKind AK, bool MX, Epilogue EPI>
+hipError_t launch(const Product& p, hipStream_t stream) {
+  if (p.M <= 16) return launch_tiles<AK, MX, EPI, 1>(p, stream);
+  if (AK == kFromBf16) return hipErrorInvalidValue;  // rows_fit takes 16 rows of those at most
+  if constexpr (AK != kFromBf16) {
+    if (p.M <= 32) return launch_tiles<AK, MX, EPI, 2>(p, stream);
+    if (p.M <= 64) return launch_tiles<AK, MX, EPI, 4>(p, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 bool rows_fit(const Product& p, bool mx, AType a, bool paired) {
   const int64_t kb = mx ? p.K / 2 : 2 * p.K;
-  return p.M >= 1 && p.M <= kMaxRows && (paired ? 2 : 1) * (int64_t)p.N * kb < 0x7fffffff &&
+  return p.M >= 1 && p.M <= (a == kABf16 ? 16 : kMaxRows) &&
+         (paired ? 2 : 1) * (int64_t)p.N * kb < 0x7fffffff &&
          (a == kAAsIs || p.M * ((int64_t)code_stride(p.K) + byte_stride(p.K)) <= kMxLds);
+}
+
+// Microseconds: a launch and a work-group's start and end, then what a CU spends
+// on its work-groups' loads (a 16 x 64-byte load holds its address path 64
+// cycles; MXFP4 with its scale bytes measured 240 a stage and tile), or the
+// weights' way from memory; and the conversion of an fp32 A, about 280 cycles
+// for each 16 bytes of a thread.
+double rows_time(const Product& p, bool mx, AType a, bool paired) {
+  const int64_t rows = (paired ? 2 : 1) * (int64_t)p.N, groups = (rows + 15) / 16;
+  const int tiles = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+  const int64_t stages = (p.K + (mx ? 255 : 63)) / (mx ? 256 : 64);
+  double cycles = (double)stages * (1 + tiles) * (mx ? 240 : 128);
+  if (a == kAF32) cycles += (double)p.M * p.K / (4 * kThreads) * 280;
+  const double busy = (double)((groups + 255) / 256) * cycles / 2400;
+  const double memory = (double)rows * p.K * (mx ? 0.53 : 2.0) / 4.5e6;
+  return 4.0 + (busy > memory ? busy : memory);
 }
 
 hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream) {
@@ -277,6 +329,7 @@ hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream) 
 
 hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream) {
   if (epilogue == kSwigluF32 && a == kABf16) return launch<kFromBf16, true, kSwigluF32>(p, stream);
+  if (epilogue == kSwigluF32 && a == kAAsIs) return launch<kAsIs, true, kSwigluF32>(p, stream);
   if (epilogue == kStoreBf16 && a == kAF32) return launch<kFromF32, true, kStoreBf16>(p, stream);
   if (epilogue == kStoreBf16 && a == kABf16) return launch<kFromBf16, true, kStoreBf16>(p, stream);
   if (epilogue == kStoreF32 && a == kABf16) return launch<kFromBf16, true, kStoreF32>(p, stream);
