@@ -242,6 +242,20 @@ def test_many_rows_past_2_gib():
     close(dx[-300:], ref, t)
 
 
+@pytest.mark.parametrize("T,H,I", [(260, 16640, 64), (4100, 136, 2112), (8200, 520, 1032)])
+def test_a_nearly_empty_last_round_of_tiles(T, H, I):
+    """Products of a little more than a whole number of rounds of tiles run as two launches."""
+    x, w13, w2, d = inputs(T, H, I, seed=11)
+    gu = torch.empty(T, 2 * I, device="cuda")
+    out = moe.ffn_forward(x, w13, w2, gate_up=gu)
+    ref_gu, gu_tol, y, tol = reference_forward(x, w13, w2)
+    close(out, y, tol)
+    assert ((gu.double() - ref_gu).abs() <= gu_tol).all()
+    got = moe.ffn_backward(d, x, gu, w13, w2)
+    for value, (ref, t) in zip(got, reference_backward(d, x, gu, w13, w2)):
+        close(value, ref, t)
+
+
 def test_refusals():
     x, w13, w2, d = inputs(4, 64, 32)
     gu = torch.empty(4, 64, device="cuda")

@@ -130,6 +130,14 @@ def test_product(M, N, K, codes, dtype):
     assert (whole[:pad] == 7).all() and (whole[pad + M * N:] == 7).all()
 
 
+def test_a_nearly_empty_last_round_of_tiles():
+    """A product of 272 and 289 tiles of 256 x 256: two launches, the second from row 3840 or 3855 on."""
+    for M, N, K in ((4100, 4096, 544), (4300, 4232, 256)):
+        x, w = rand(M, K, seed=1), rand(N, K, seed=2)
+        got = moe.mxfp4_matmul(x, moe.mxfp4_quantize(w), dtype=torch.float32)
+        product_close(got, q_values(x), q_values(w), K, False)
+
+
 def test_product_of_row_slices_and_odd_scale_rows():
     """Rows taken out of larger matrices: scales then start at any byte."""
     x, w = rand(70, 96, seed=1), rand(40, 96, seed=2)

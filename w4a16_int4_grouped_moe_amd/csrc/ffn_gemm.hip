@@ -409,14 +409,15 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int64_t tm = (p.M + HRA - 1) / HRA, tn = (p.N + kCols - 1) / kCols;
+  const int64_t rows = p.m_end - p.m_first;
+  const int64_t tm = (rows + HRA - 1) / HRA, tn = (p.N + kCols - 1) / kCols;
   const TileId t = tile_of(blockIdx.x, tm, tn);
-  const int64_t m0 = t.m * HRA, n0 = t.n * kCols;
+  const int64_t m0 = p.m_first + t.m * HRA, n0 = t.n * kCols;
   const int first = blockIdx.y * share;  // stages [first, first + count)
   const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
   const int count = stages - first < share ? stages - first : share;
   if constexpr (EPI == kPartial || EPI == kPartialPaired)
-    p.out = (float*)p.out + (int64_t)blockIdx.y * p.M * p.N * (kPaired ? 2 : 1);
+    p.out = (float*)p.out + ((int64_t)blockIdx.y * rows - p.m_first) * p.N * (kPaired ? 2 : 1);
 
   HA a;
   HB b0, b1;
@@ -535,14 +536,15 @@ __global__ __launch_bounds__(256) void join_kernel(const Product p, const float*
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx;
   const int64_t quads = p.N / 4;
   const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-  if (u >= p.M * quads) return;  // N is a multiple of 32 where lanes work together
-  const int64_t m = u / quads, n = (u - m * quads) * 4;
+  const int64_t rows = p.m_end - p.m_first;
+  if (u >= rows * quads) return;  // N is a multiple of 32 where lanes work together
+  const int64_t row = u / quads, m = p.m_first + row, n = (u - row * quads) * 4;
   const int64_t pitch = (kPaired ? 2 : 1) * (int64_t)p.N;
-  const float* src = sums + m * pitch + n;
+  const float* src = sums + row * pitch + n;
   f32x4 v = *(const f32x4*)src, up = {};
   if constexpr (kPaired) up = *(const f32x4*)(src + p.N);
   for (int s = 1; s < shares; ++s) {
-    src += p.M * pitch;
+    src += rows * pitch;
     v += *(const f32x4*)src;
     if constexpr (kPaired) up += *(const f32x4*)(src + p.N);
   }
@@ -562,8 +564,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Product p, const float*
 // half x 32 columns of both B halves. A phase is one A half against both B
 // halves, 32 MFMAs (512 cycles) a wave. The two waves of a SIMD run half a
 // phase apart: one reads fragments and issues copies while the other's MFMAs
-// run, with a barrier after each of the two parts; s_setprio keeps the MFMAs
-// in front. A half tile is copied into its own place as soon as the phase that
+// run, with a barrier after each of the two parts. A half tile is copied into its own place as soon as the phase that
 // read it is over.
 //
 //   AH  buffers  phase  reads      copies                 waits for (at its end)
@@ -596,9 +597,10 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const int64_t tm = (p.M + AH * HR - 1) / (AH * HR), tn = (p.N + kCols - 1) / kCols;
+  const int64_t tm = (p.m_end - p.m_first + AH * HR - 1) / (AH * HR);
+  const int64_t tn = (p.N + kCols - 1) / kCols;
   const TileId t = tile_of(blockIdx.x, tm, tn);
-  const int64_t m0 = t.m * (AH * HR), n0 = t.n * kCols;
+  const int64_t m0 = p.m_first + t.m * (AH * HR), n0 = t.n * kCols;
 
   HA a0, a1;
   HB b0, b1;
@@ -666,10 +668,8 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   wait_lgkm0();                          \
   __builtin_amdgcn_sched_barrier(0);     \
   __builtin_amdgcn_s_barrier();          \
-  __builtin_amdgcn_sched_barrier(0);     \
-  __builtin_amdgcn_s_setprio(1);
+  __builtin_amdgcn_sched_barrier(0);
 #define FFN_MMA_DONE                     \
-  __builtin_amdgcn_s_setprio(0);         \
   __builtin_amdgcn_sched_barrier(0);     \
   __builtin_amdgcn_s_barrier();          \
   __builtin_amdgcn_sched_barrier(0);
@@ -829,18 +829,45 @@ Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx
 
 template <Epilogue EPI>
 hipError_t join(const Product& p, const void* sums, int shares, hipStream_t stream) {
-  const int64_t groups = (p.M * (p.N / 4) + 255) / 256, y = (groups + (1 << 20) - 1) >> 20;
+  const int64_t groups = ((p.m_end - p.m_first) * (p.N / 4) + 255) / 256, y = (groups + (1 << 20) - 1) >> 20;
   hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups + y - 1) / y), (unsigned)y),
                      dim3(256), 0, stream, p, (const float*)sums, shares);
   return hipGetLastError();
 }
 
+// A product whose last round of tiles is nearly empty is computed in two
+// launches: its first rows in whole rounds of 256 x 256 tiles, the rest cut on
+// its own (4100 tokens at 7168/2048: one round and 4 rows instead of two).
+struct Plan {
+  int64_t first = 0;  // rows of the first launch, or 0
+  Cut whole, rest;    // whole: of the first rows, where there are two
+  double time = 0;
+};
+Plan plan_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx) {
+  Plan best;
+  best.whole = cut_of(epi, M, N, K, layout, mx);
+  best.time = best.whole.time;
+  const bool paired = epi == kSwiglu || epi == kSwigluMx;
+  const int64_t cols = paired ? 128 : 256, tn = (N + cols - 1) / cols;
+  const int64_t rounds = ((M + 255) / 256 * tn + 255) / 256;
+  if (rounds < 2) return best;
+  const int64_t rows = (rounds - 1) * 256 / tn * 256;  // of whole rounds
+  if (rows <= 0 || rows >= M) return best;
+  const Cut rest = cut_of(epi, M - rows, N, K, layout, mx);
+  Cut first{2, 1, 0, rows / 256 * tn};
+  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
+  const Rate& rate = kRates[mx ? 2 : layout == kNT ? 0 : 1];
+  first.time = (double)((first.groups + 255) / 256) * (stages * rate.stage[2] + rate.fixed[2]);
+  if (first.time + rest.time + 3.0 < 0.95 * best.time)
+    best.first = rows, best.whole = first, best.rest = rest,
+    best.time = first.time + rest.time + 3.0;
+  return best;
+}
+
 template <Layout L, bool MX, Epilogue EPI>
-hipError_t launch(const Product& p, void* split, hipStream_t stream) {
+hipError_t launch_cut(const Product& p, const Cut& c, void* split, hipStream_t stream) {
   constexpr Kind KA = L == kTN ? RC : KC, KB = L == kNT ? KC : RC;
   constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
-  if (p.M == 0 || p.N == 0) return hipSuccess;
-  const Cut c = cut_of(EPI, p.M, p.N, p.K, L, MX);
   if (c.groups > 0x7fffff) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)c.groups, c.shares);
   if (c.tile == 2) {
@@ -860,17 +887,31 @@ hipError_t launch(const Product& p, void* split, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <Layout L, bool MX, Epilogue EPI>
+hipError_t launch(Product p, void* split, hipStream_t stream) {
+  if (p.M == 0 || p.N == 0) return hipSuccess;
+  const Plan plan = plan_of(EPI, p.M, p.N, p.K, L, MX);
+  p.m_end = plan.first ? plan.first : p.M;
+  const hipError_t e = launch_cut<L, MX, EPI>(p, plan.whole, split, stream);
+  if (e != hipSuccess || !plan.first) return e;
+  p.m_first = plan.first;
+  p.m_end = p.M;
+  return launch_cut<L, MX, EPI>(p, plan.rest, split, stream);
+}
+
 }  // namespace
 
 size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
                          bool mx) {
-  const Cut c = cut_of(epilogue, M, N, K, layout, mx);
+  if (M == 0) return 0;
+  const Plan plan = plan_of(epilogue, M, N, K, layout, mx);
   const bool paired = epilogue == kSwiglu || epilogue == kSwigluMx;
-  return c.shares > 1 ? (size_t)c.shares * M * N * (paired ? 8 : 4) : 0;
+  const Cut& c = plan.first ? plan.rest : plan.whole;
+  return c.shares > 1 ? (size_t)c.shares * (M - plan.first) * N * (paired ? 8 : 4) : 0;
 }
 
 double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx) {
-  return cut_of(epilogue, M, N, K, layout, mx).time;
+  return plan_of(epilogue, M, N, K, layout, mx).time;
 }
 
 hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,

@@ -47,6 +47,7 @@ struct Product {
   void* out = nullptr;
   void* out2 = nullptr;
   void* aux = nullptr;
+  int64_t m_first = 0, m_end = 0;  // set by a launch: the rows it computes
 };
 
 // bf16 operands. split: workspace of product_workspace bytes (16-byte aligned).
