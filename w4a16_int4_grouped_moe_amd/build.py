@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libmoe_w4a16.so")
 PROBE_LIB = os.path.join(HERE, "libmoe_probe.so")
 PROBE_SOURCES = ["read_probe.hip"]
 SOURCES = ["align.hip", "route.hip", "gemm_small.hip", "gemm_prefill.hip", "prepack.hip", "combine.hip",
-           "api.cpp", "ffn_gemm.hip", "ffn_small.hip", "mxfp4.hip", "ffn_api.cpp"]
+           "api.cpp", "ffn_gemm.hip", "ffn_small.hip", "mxfp4.hip", "ffn_plan.cpp",
+           "ffn_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # packed fp32 VALU forms are disabled for all device code

@@ -779,89 +779,12 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 #endif
 }
 
-// How a product is cut: the tile (0: 128 x 128, 1: 128 x 256, 2: 256 x 256;
-// half the columns where gate and up pair), and for tile 0 the shares of K.
-struct Cut {
-  int tile = 0, shares = 1, share = 1;
-  int64_t groups = 0;
-  double time = 0;  // estimate
-};
-// Microseconds a stage of K takes one round of work-groups on 256 CUs, and what
-// a work-group costs besides. Measured on products of 20 to 4096 rows at
-// widths 256 to 7168 (bf16 with K contiguous operands; with a row contiguous
-// one; MXFP4).
-struct Rate {
-  double stage[3], fixed[3];
-};
-constexpr Rate kRates[3] = {{{0.62, 0.88, 1.42}, {4.5, 4.5, 7.0}},
-                            {{0.92, 0.85, 1.42}, {4.0, 5.0, 7.0}},
-                            {{0.85, 1.20, 1.80}, {4.5, 4.5, 8.0}}};
-// The cheapest cut. Shares of K cost a launch and the sums' way to memory and
-// back (about 4 TB/s); of equals the larger tile.
-Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx) {
-  const bool paired = epi == kSwiglu || epi == kSwigluMx;
-  const Rate& rate = kRates[mx ? 2 : layout == kNT ? 0 : 1];
-  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  auto tiles = [&](int64_t rows, int64_t cols) {
-    if (paired) cols /= 2;
-    return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
-  };
-  auto time = [&](int tile, int64_t groups, int64_t st) {
-    return (double)((groups + 255) / 256) * (st * rate.stage[tile] + rate.fixed[tile]);
-  };
-  const int64_t n[3] = {tiles(128, 128), tiles(128, 256), tiles(256, 256)};
-  Cut best{2, 1, (int)stages, n[2]};
-  double least = time(2, n[2], stages);
-  if (time(1, n[1], stages) < least) {
-    least = time(1, n[1], stages);
-    best = Cut{1, 1, (int)stages, n[1]};
-  }
-  for (int shares = 1; shares <= 32 && n[0] * shares <= 1024; ++shares) {
-    const int64_t share = (stages + shares - 1) / shares;
-    if (shares > 1 && (2 * shares > stages || share * (shares - 1) >= stages)) continue;
-    const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
-    const double t = time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : 0.0);
-    if (t < least) least = t, best = Cut{0, shares, (int)share, n[0]};
-  }
-  best.time = least;
-  return best;
-}
-
 template <Epilogue EPI>
 hipError_t join(const Product& p, const void* sums, int shares, hipStream_t stream) {
   const int64_t groups = ((p.m_end - p.m_first) * (p.N / 4) + 255) / 256, y = (groups + (1 << 20) - 1) >> 20;
   hipLaunchKernelGGL((join_kernel<EPI>), dim3((unsigned)((groups + y - 1) / y), (unsigned)y),
                      dim3(256), 0, stream, p, (const float*)sums, shares);
   return hipGetLastError();
-}
-
-// A product whose last round of tiles is nearly empty is computed in two
-// launches: its first rows in whole rounds of 256 x 256 tiles, the rest cut on
-// its own (4100 tokens at 7168/2048: one round and 4 rows instead of two).
-struct Plan {
-  int64_t first = 0;  // rows of the first launch, or 0
-  Cut whole, rest;    // whole: of the first rows, where there are two
-  double time = 0;
-};
-Plan plan_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx) {
-  Plan best;
-  best.whole = cut_of(epi, M, N, K, layout, mx);
-  best.time = best.whole.time;
-  const bool paired = epi == kSwiglu || epi == kSwigluMx;
-  const int64_t cols = paired ? 128 : 256, tn = (N + cols - 1) / cols;
-  const int64_t rounds = ((M + 255) / 256 * tn + 255) / 256;
-  if (rounds < 2) return best;
-  const int64_t rows = (rounds - 1) * 256 / tn * 256;  // of whole rounds
-  if (rows <= 0 || rows >= M) return best;
-  const Cut rest = cut_of(epi, M - rows, N, K, layout, mx);
-  Cut first{2, 1, 0, rows / 256 * tn};
-  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  const Rate& rate = kRates[mx ? 2 : layout == kNT ? 0 : 1];
-  first.time = (double)((first.groups + 255) / 256) * (stages * rate.stage[2] + rate.fixed[2]);
-  if (first.time + rest.time + 3.0 < 0.95 * best.time)
-    best.first = rows, best.whole = first, best.rest = rest,
-    best.time = first.time + rest.time + 3.0;
-  return best;
 }
 
 template <Layout L, bool MX, Epilogue EPI>
@@ -900,19 +823,6 @@ hipError_t launch(Product p, void* split, hipStream_t stream) {
 }
 
 }  // namespace
-
-size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
-                         bool mx) {
-  if (M == 0) return 0;
-  const Plan plan = plan_of(epilogue, M, N, K, layout, mx);
-  const bool paired = epilogue == kSwiglu || epilogue == kSwigluMx;
-  const Cut& c = plan.first ? plan.rest : plan.whole;
-  return c.shares > 1 ? (size_t)c.shares * (M - plan.first) * N * (paired ? 8 : 4) : 0;
-}
-
-double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx) {
-  return plan_of(epilogue, M, N, K, layout, mx).time;
-}
 
 hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, void* split,
                           hipStream_t stream) {

@@ -56,10 +56,24 @@ hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, vo
 // MXFP4 operands, both K contiguous; K a multiple of 32
 hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
                              hipStream_t stream);
-// Where few tiles would run a long K, its shares go to several work-groups and
-// their sums here; 0 where they do not.
+// How a tiled product is cut (ffn_plan.cpp): the tile (0: 128 x 128, 1: 128 x
+// 256, 2: 256 x 256; half the columns where gate and up pair), its work-groups,
+// and for tile 0 the shares of K, `share` stages each.
+struct Cut {
+  int tile = 0, shares = 1, share = 1;
+  int64_t groups = 0;
+  double time = 0;  // estimate, microseconds
+};
+struct Plan {
+  int64_t first = 0;  // rows of a first launch where there are two, or 0
+  Cut whole, rest;    // whole: of the first rows, where there are two
+  double time = 0;
+};
+Plan plan_of(Epilogue epilogue, int64_t M, int64_t N, int64_t K, Layout layout, bool mx);
+// Bytes of the shares' sums (`split`), and the plan's time
 size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
                          bool mx);
+double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
 
 // The same products for a few rows (ffn_small.hip), both operands K contiguous
 // and dense. A: as the product takes it, or rows to be quantised to MXFP4.
@@ -70,7 +84,14 @@ size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N,
 enum AType { kAAsIs = 0, kABf16 = 1, kAF32 = 2 };
 bool rows_fit(const Product& p, bool mx, AType a, bool paired);
 double rows_time(const Product& p, bool mx, AType a, bool paired);
-double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
+constexpr int kRowsThreads = 512;  // of a work-group
+// LDS rows of an A quantised there: 16 rows at one offset lie in distinct banks
+__host__ __device__ inline int rows_code_stride(int64_t K) {
+  return (int)((K / 2 + 255) / 256 * 256 + 16);
+}
+__host__ __device__ inline int rows_byte_stride(int64_t K) {
+  return (int)((K / 32 + 7) / 8 * 8 + 4);
+}
 hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream);
 hipError_t launch_rows_mx(Epilogue epilogue, AType a, const Product& p, hipStream_t stream);
 

@@ -24,13 +24,8 @@
 namespace ffn {
 namespace {
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kMaxRows = 64;
-constexpr int kMxLds = 64 * 1024;  // quantised A in LDS, codes and scales
-
-// LDS rows of quantised A: 16 rows at one offset lie in distinct banks
-__host__ __device__ inline int code_stride(int64_t K) { return (int)((K / 2 + 255) / 256 * 256 + 16); }
-__host__ __device__ inline int byte_stride(int64_t K) { return (int)((K / 32 + 7) / 8 * 8 + 4); }
+constexpr int kWaves = 8, kThreads = kRowsThreads;
+static_assert(kThreads == 64 * kWaves, "a work-group of the estimates");
 
 #if defined(__HIP_DEVICE_COMPILE__)
 template <int CTRL>
@@ -143,7 +138,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(const P
     for (int d = 0; d < kD; ++d) load(d, wave + d * kWaves);
   };
 
-  const int cstride = code_stride(p.K), bstride = byte_stride(p.K);
+  const int cstride = rows_code_stride(p.K), bstride = rows_byte_stride(p.K);
   uint8_t* qbytes = qa + M * cstride;
   if constexpr (AK == kAsIs) {
     fill();
@@ -279,7 +274,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(const P
 template <AKind AK, bool MX, Epilogue EPI, int MT>
 hipError_t launch_tiles(const Product& p, hipStream_t stream) {
   const unsigned groups = EPI == kSwiglu || EPI == kSwigluF32 ? (p.N + 7) / 8 : (p.N + 15) / 16;
-  const size_t a = AK == kAsIs ? 0 : p.M * (code_stride(p.K) + byte_stride(p.K));
+  const size_t a = AK == kAsIs ? 0 : p.M * (rows_code_stride(p.K) + rows_byte_stride(p.K));
   const size_t lds = std::max<size_t>(a, kWaves * MT * 256 * sizeof(float));
   hipLaunchKernelGGL((rows_kernel<AK, MX, EPI, MT>), dim3(groups), dim3(kThreads), lds, stream,
                      p);
@@ -297,29 +292,6 @@ hipError_t launch(const Product& p, hipStream_t stream) {
 }
 
 }  // namespace
-
-bool rows_fit(const Product& p, bool mx, AType a, bool paired) {
-  const int64_t kb = mx ? p.K / 2 : 2 * p.K;
-  return p.M >= 1 && p.M <= (a == kABf16 ? 16 : kMaxRows) &&
-         (paired ? 2 : 1) * (int64_t)p.N * kb < 0x7fffffff &&
-         (a == kAAsIs || p.M * ((int64_t)code_stride(p.K) + byte_stride(p.K)) <= kMxLds);
-}
-
-// Microseconds: a launch and a work-group's start and end, then what a CU spends
-// on its work-groups' loads (a 16 x 64-byte load holds its address path 64
-// cycles; MXFP4 with its scale bytes measured 240 a stage and tile), or the
-// weights' way from memory; and the conversion of an fp32 A, about 280 cycles
-// for each 16 bytes of a thread.
-double rows_time(const Product& p, bool mx, AType a, bool paired) {
-  const int64_t rows = (paired ? 2 : 1) * (int64_t)p.N, groups = (rows + 15) / 16;
-  const int tiles = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
-  const int64_t stages = (p.K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  double cycles = (double)stages * (1 + tiles) * (mx ? 240 : 128);
-  if (a == kAF32) cycles += (double)p.M * p.K / (4 * kThreads) * 280;
-  const double busy = (double)((groups + 255) / 256) * cycles / 2400;
-  const double memory = (double)rows * p.K * (mx ? 0.53 : 2.0) / 4.5e6;
-  return 4.0 + (busy > memory ? busy : memory);
-}
 
 hipError_t launch_rows(Epilogue epilogue, const Product& p, hipStream_t stream) {
   if (epilogue == kSwiglu) return launch<kAsIs, false, kSwiglu>(p, stream);
