@@ -166,6 +166,16 @@ def test_mxfp4_ffn_errors(lib):
     assert call(x=None, pp=problem(T=0)) == moe.MOE_OK
 
 
+def test_binding_refuses_sizes_past_a_c_int(lib):
+    big = (1 << 32) + 64  # would be 64
+    for args in ((4, big, 32), (4, 64, big)):
+        with pytest.raises(ValueError):
+            moe.ffn_workspace_size(*args, moe.MOE_FFN_FORWARD)
+    for args in ((4, big, 64), (4, 64, big)):
+        with pytest.raises(ValueError):
+            moe.mxfp4_matmul_workspace_size(*args, True)
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):

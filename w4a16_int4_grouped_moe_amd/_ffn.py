@@ -18,6 +18,7 @@ MOE_FFN_BACKWARD = 1
 MOE_FFN_FORWARD_MXFP4 = 2
 
 MX_BLOCK = 32
+MAX_INT32 = 0x7fffffff
 
 
 class FfnProblem(ctypes.Structure):
@@ -97,6 +98,8 @@ def _scratch(workspace, need, device):
 def _problem(num_tokens, hidden, inter, kind):
     """The sizes as the library takes them, and the workspace bytes (a pure
     function of the sizes)."""
+    if max(hidden, inter) > MAX_INT32:  # as a C int they would be others
+        raise ValueError(f"hidden {hidden} or inter {inter} is out of range")
     p = FfnProblem(num_tokens, hidden, inter)
     n = ctypes.c_size_t(0)
     _check(_library().moe_ffn_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)))
@@ -169,8 +172,8 @@ class Mxfp4:
             _need(codes, "codes", torch.uint8, 2, dev)
         rows, half = codes.shape
         _shaped(codes, "codes", torch.uint8, (rows, half), dev)
-        if half % (MX_BLOCK // 2):
-            raise ValueError(f"codes hold {half} bytes a row, not whole blocks of 16")
+        if half % (MX_BLOCK // 2) or 2 * half > MAX_INT32:
+            raise ValueError(f"codes hold {half} bytes a row, not whole blocks of 16 in range")
         _shaped(scales, "scales", torch.uint8, (rows, half // (MX_BLOCK // 2)), dev)
         self._codes = codes
         self._scales = scales
@@ -207,8 +210,8 @@ def mxfp4_quantize(x, codes=None, scales=None) -> Mxfp4:
     kind = _type_of(x.dtype)
     _need(x, "x", x.dtype, 2, dev)
     rows, width = x.shape
-    if width % MX_BLOCK:
-        raise ValueError(f"x has width {width}, not a multiple of {MX_BLOCK}")
+    if width % MX_BLOCK or width > MAX_INT32:
+        raise ValueError(f"x has width {width}, not a multiple of {MX_BLOCK} in range")
     codes = _result(codes, "codes", torch.uint8, (rows, width // 2), dev)
     scales = _result(scales, "scales", torch.uint8, (rows, width // MX_BLOCK), dev)
     _launch(dev, _library().moe_mxfp4_quantize, x.data_ptr(), kind, rows, width,
@@ -233,6 +236,8 @@ def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):
 @functools.lru_cache(maxsize=4096)
 def mxfp4_matmul_workspace_size(rows: int, cols: int, width: int, quantize: bool) -> int:
     """Bytes of workspace of mxfp4_matmul (quantize: a is a bf16 tensor)."""
+    if max(cols, width) > MAX_INT32:
+        raise ValueError(f"cols {cols} or width {width} is out of range")
     n = ctypes.c_size_t(0)
     _check(_library().moe_mxfp4_matmul_workspace_size(rows, cols, width, int(quantize),
                                                       ctypes.byref(n)))
