@@ -51,11 +51,21 @@ void outputs(ffn::Epilogue e, const ffn::Product& p) {
     default: expect(false, "epilogue");
   }
 }
+void cut(const ffn::Cut& c, bool pair, int64_t M, int64_t N, int64_t K, bool mx) {
+  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
+  const int64_t rows = c.tile == 2 ? 256 : 128, cols = (c.tile == 0 ? 128 : 256) / (pair ? 2 : 1);
+  expect(c.tile >= 0 && c.tile <= 2, "tile");
+  expect(c.groups == ((M + rows - 1) / rows) * ((N + cols - 1) / cols), "work-groups");
+  expect(c.shares >= 1 && (c.tile == 0 || c.shares == 1), "shares");
+  if (c.tile == 0) {
+    expect((int64_t)c.share * c.shares >= stages, "the shares cover K");
+    expect(c.shares == 1 || (int64_t)c.share * (c.shares - 1) < stages, "no empty share");
+  }
+}
 }  // namespace
 
 namespace ffn {
-hipError_t launch_product(Layout l, Epilogue e, const Product& p, void* split, hipStream_t) {
-  ++launches;
+static void operands(Layout l, Epilogue e, const Product& p) {
   const size_t rows_b = (size_t)p.N * (paired(e) ? 2 : 1);
   if (l == kTN) {
     if (p.K) need(p.a, (p.K - 1) * p.lda + 2 * p.M, "a");
@@ -67,6 +77,10 @@ hipError_t launch_product(Layout l, Epilogue e, const Product& p, void* split, h
   else if (p.K)
     need(p.b, (p.K - 1) * p.ldb + 2 * p.N, "b");
   outputs(e, p);
+}
+hipError_t launch_product(Layout l, Epilogue e, const Product& p, void* split, hipStream_t) {
+  ++launches;
+  operands(l, e, p);
   need(split, product_workspace(l, e, p.M, p.N, p.K, false), "sums");
   return hipSuccess;
 }
@@ -79,6 +93,22 @@ hipError_t launch_product_mx(Epilogue e, const Product& p, void* split, hipStrea
   need(p.b_scales, scale_bytes(rows_b, p.K), "b scales");
   outputs(e, p);
   need(split, product_workspace(kNT, e, p.M, p.N, p.K, true), "sums");
+  return hipSuccess;
+}
+hipError_t launch_gradients(const GradientsPlan& plan, const Product (&d)[3], void* split,
+                            hipStream_t) {
+  ++launches;
+  expect(plan.together, "together");
+  need(split, plan.bytes, "sums");
+  size_t at = 0;
+  for (int i = 0; i < 3; ++i) {
+    operands(i ? kTN : kNN, kStoreBf16, d[i]);
+    cut(plan.cut[i], false, d[i].M, d[i].N, d[i].K, false);
+    if (plan.cut[i].shares == 1) continue;
+    expect(plan.sums[i] == at && at % 16 == 0, "place of the sums");
+    at += 4 * (size_t)d[i].M * d[i].N * plan.cut[i].shares;
+  }
+  expect(at == plan.bytes, "bytes of the sums");
   return hipSuccess;
 }
 hipError_t launch_rows(Epilogue e, const Product& p, hipStream_t) {
@@ -200,17 +230,6 @@ void product(int64_t M, int32_t N, int32_t K) {
     }
 }
 
-void cut(const ffn::Cut& c, bool pair, int64_t M, int64_t N, int64_t K, bool mx) {
-  const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  const int64_t rows = c.tile == 2 ? 256 : 128, cols = (c.tile == 0 ? 128 : 256) / (pair ? 2 : 1);
-  expect(c.tile >= 0 && c.tile <= 2, "tile");
-  expect(c.groups == ((M + rows - 1) / rows) * ((N + cols - 1) / cols), "work-groups");
-  expect(c.shares >= 1 && (c.tile == 0 || c.shares == 1), "shares");
-  if (c.tile == 0) {
-    expect((int64_t)c.share * c.shares >= stages, "the shares cover K");
-    expect(c.shares == 1 || (int64_t)c.share * (c.shares - 1) < stages, "no empty share");
-  }
-}
 void plan(int64_t M, int64_t N, int64_t K) {
   ++cases;
   for (int mx = 0; mx < 2; ++mx)

@@ -112,6 +112,27 @@ def test_backward(T, H, I):
         assert intact()
 
 
+@pytest.mark.parametrize("T,H,I", [(20, 696, 256), (201, 1000, 680), (1500, 1024, 256),
+                                   (4000, 200, 64), (1000, 1000, 680), (300, 4096, 512)])
+def test_backward_products_in_one_launch(T, H, I):
+    """Sizes at which dx, dw13 and dw2 share a launch, with and without shares of their sums, in a
+    workspace of just the size asked for."""
+    x, w13, w2, d = inputs(T, H, I, seed=12)
+    gu = x.float() @ w13.float().T
+    want = reference_backward(d, x, gu, w13, w2)
+    need = moe.ffn_workspace_size(T, H, I, 1)
+    ws, ws_ok = guarded((need,), torch.uint8)
+    outs = [guarded(s, torch.bfloat16) for s in ((T, H), (2 * I, H), (H, I))]
+    got = moe.ffn_backward(d, x, gu, w13, w2, *(o for o, _ in outs), workspace=ws)
+    for value, (ref, tol), (_, intact) in zip(got, want, outs):
+        close(value, ref, tol)
+        assert intact()
+    assert ws_ok()
+    first = [v.clone() for v in got]
+    again = moe.ffn_backward(d, x, gu, w13, w2)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 def test_gradients_against_differences():
     """sum(out * dout) changes along a direction as the gradients say (central differences of the
     fp64 block; the gradients' own error is their bound summed over the direction)."""

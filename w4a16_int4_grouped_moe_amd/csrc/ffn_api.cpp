@@ -118,6 +118,7 @@ size_t split_of(const moe_ffn_problem* p, int pass) {
     add(ffn::kNN, ffn::kStoreBf16, T, H, 2 * I);
     add(ffn::kTN, ffn::kStoreBf16, 2 * I, H, T);
     add(ffn::kTN, ffn::kStoreBf16, H, I, T);
+    most = std::max(most, ffn::gradients_plan(T, H, I).bytes);
   } else {
     add(ffn::kNT, mx ? ffn::kSwigluMx : ffn::kSwiglu, T, I, H);
     add(ffn::kNT, ffn::kStoreBf16, T, H, I);
@@ -203,22 +204,21 @@ int moe_ffn_backward(const void* dout, const void* x, const float* gate_up, cons
     dh.out2 = h;
     dh.aux = const_cast<float*>(gate_up);
     e = ffn::launch_product(ffn::kNN, ffn::kSwigluGrad, dh, split, s);
-    if (e == hipSuccess && dx) {
-      Product d{dgu, w13, nullptr, nullptr, 4 * I, 2 * H, T, p->hidden, 2 * I};
-      d.out = dx;
-      e = ffn::launch_product(ffn::kNN, ffn::kStoreBf16, d, split, s);
-    }
   }
-  if (e == hipSuccess && dw13) {
-    Product d13{dgu, x, nullptr, nullptr, 4 * I, 2 * H, 2 * I, p->hidden, T};
-    d13.out = dw13;
-    e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d13, split, s);
-    if (e == hipSuccess) {
-      Product d2{dout, h, nullptr, nullptr, 2 * H, 2 * I, H, p->inter, T};
-      d2.out = dw2;
-      e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d2, split, s);
-    }
+  Product d[3] = {{dgu, w13, nullptr, nullptr, 4 * I, 2 * H, T, p->hidden, 2 * I},
+                  {dgu, x, nullptr, nullptr, 4 * I, 2 * H, 2 * I, p->hidden, T},
+                  {dout, h, nullptr, nullptr, 2 * H, 2 * I, H, p->inter, T}};
+  d[0].out = dx;
+  d[1].out = dw13;
+  d[2].out = dw2;
+  if (e == hipSuccess && dx && dw13) {
+    const ffn::GradientsPlan plan = ffn::gradients_plan(T, H, I);
+    if (plan.together) return done(ffn::launch_gradients(plan, d, split, s));
   }
+  if (e == hipSuccess && dx && T > 0)
+    e = ffn::launch_product(ffn::kNN, ffn::kStoreBf16, d[0], split, s);
+  for (int i = 1; i < 3 && e == hipSuccess && dw13; ++i)
+    e = ffn::launch_product(ffn::kTN, ffn::kStoreBf16, d[i], split, s);
   return done(e);
 }
 

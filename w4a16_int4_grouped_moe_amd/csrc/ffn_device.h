@@ -23,6 +23,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void* lds_ptr;
+typedef __attribute__((address_space(3))) uint8_t* lds_bytes;
+typedef __attribute__((address_space(3))) u32x2* lds_u32x2;
+typedef __attribute__((address_space(3))) u32x4* lds_u32x4;
+typedef __attribute__((address_space(3))) f32x4* lds_f32x4;
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 constexpr int kBufferFlags = 0x00020000;  // raw buffer resource, dword 3

@@ -36,7 +36,7 @@ enum Kind { KC = 0, RC = 1 };
 
 // 16 lanes address 4 x 16 16-bit values, four neighbouring lanes a row of 16;
 // lane i receives column i, row j in element j.
-__device__ __forceinline__ s16x4 read_transposed(const uint8_t* p) {
+__device__ __forceinline__ s16x4 read_transposed(lds_bytes p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p);
 }
 
@@ -98,9 +98,9 @@ struct Half {
       records = 2 * valid;
   }
 
-  __device__ __forceinline__ void copy(uint8_t* slot, int stage, int wave,
+  __device__ __forceinline__ void copy(lds_bytes slot, int stage, int wave,
                                        const Lane<KIND, HR, NW>& at) const {
-    uint8_t* dst = slot + wave * (kPer * 1024);
+    const lds_bytes dst = slot + wave * (kPer * 1024);
     if constexpr (KIND == KC) {
       const __amdgpu_buffer_rsrc_t res =
           __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records, kBufferFlags);
@@ -137,21 +137,21 @@ struct Frags {
     const int q = lane >> 4;
     return (lane & 15) * kRow + ((q ^ ((lane >> 1) & 7)) * 16);
   }
-  __device__ __forceinline__ void read(const uint8_t* slot, int first, int lane) {
+  __device__ __forceinline__ void read(lds_bytes slot, int first, int lane) {
     if constexpr (KIND == KC) {
       const int b = lane_base(lane) + first * kRow;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int i = 0; i < F; ++i)
-          v[s][i] = *(const u32x4*)(slot + (b ^ (s * 64)) + i * 16 * kRow);
+          v[s][i] = *(lds_u32x4)(slot + (b ^ (s * 64)) + i * 16 * kRow);
     } else {
       const int q = lane >> 4, j = (lane >> 2) & 3;
       const int x = spread<HR>(8 * q + j);
-      const uint8_t* b = slot + (8 * q + j) * (2 * HR) + (lane & 3) * 8;
+      const lds_bytes b = slot + (8 * q + j) * (2 * HR) + (lane & 3) * 8;
 #pragma unroll
       for (int i = 0; i < F; ++i) {
-        const uint8_t* c = b + (((first >> 4) + i) ^ x) * 32;
+        const lds_bytes c = b + (((first >> 4) + i) ^ x) * 32;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           const s16x4 lo = read_transposed(c + s * 32 * (2 * HR));
@@ -214,7 +214,7 @@ struct HalfScales {
     base = scales + (left > 0 ? first + row0 : 0) * 8;
   }
   template <int HR>
-  __device__ __forceinline__ void copy(uint8_t* slot, int stage, int lane) const {
+  __device__ __forceinline__ void copy(lds_bytes slot, int stage, int lane) const {
     const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(base + (stage < last ? stage : last) * pitch), 0, records, kBufferFlags);
     if (lane < HR / 2)
@@ -225,14 +225,14 @@ struct HalfScales {
 // A wave's scale operands: lane (r, q) takes bytes q and 4 + q (its blocks of
 // the two steps) of row r of each sub-tile; two sub-tiles a word.
 template <int F>
-__device__ __forceinline__ void read_scales(const uint8_t* slot, int first, int lane,
+__device__ __forceinline__ void read_scales(lds_bytes slot, int first, int lane,
                                             uint32_t* word) {
   const int q = lane >> 4;
   const uint32_t pick = (uint32_t)(q | (4 + q) << 8);
-  const uint8_t* at = slot + (first + (lane & 15)) * 8;
+  const lds_bytes at = slot + (first + (lane & 15)) * 8;
 #pragma unroll
   for (int i = 0; i < F; i += 2) {
-    const u32x2 a = *(const u32x2*)(at + i * 16 * 8), b = *(const u32x2*)(at + (i + 1) * 16 * 8);
+    const u32x2 a = *(lds_u32x2)(at + i * 16 * 8), b = *(lds_u32x2)(at + (i + 1) * 16 * 8);
     const uint32_t lo = __builtin_amdgcn_perm(a[1], a[0], pick);
     const uint32_t hi = __builtin_amdgcn_perm(b[1], b[0], pick);
     word[i / 2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
@@ -259,8 +259,11 @@ __device__ __forceinline__ void emit(const Product& p, int64_t m, int64_t n, con
     float* gu = (float*)p.out + m * 2 * N + n;
     *(f32x4*)gu = v;
     *(f32x4*)(gu + N) = up;
-  } else if constexpr (EPI == kStoreBf16) {
-    *(u32x2*)((uint16_t*)p.out + m * N + n) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+  } else if constexpr (EPI == kStoreBf16 || EPI == kStoreOrSums) {
+    if (EPI == kStoreOrSums && p.aux)
+      *(f32x4*)((float*)p.aux + m * N + n) = v;
+    else
+      *(u32x2*)((uint16_t*)p.out + m * N + n) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
   } else if constexpr (EPI == kSwiglu) {
     float h[4];
 #pragma unroll
@@ -330,7 +333,7 @@ __device__ __forceinline__ void emit_mx(const Product& p, int64_t m, int64_t n, 
 // its gate and its up columns). COLS: columns of a row in LDS; m0: the row of
 // the tile's matrix at `lds`.
 template <Epilogue EPI, int COLS>
-__device__ __forceinline__ void store_rows(const Product& p, const uint8_t* lds, int64_t m0,
+__device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int64_t m0,
                                            int64_t n0, int lane) {
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
   constexpr int kLanes = COLS / (kPaired ? 8 : 4);  // a row's lanes
@@ -352,9 +355,9 @@ __device__ __forceinline__ void store_rows(const Product& p, const uint8_t* lds,
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int x = kRowsAtOnce * (t + k) + lane / kLanes;
-      v[k] = *(const f32x4*)(lds + x * (4 * COLS) + ((c ^ (x & 15)) * 16));
+      v[k] = *(lds_f32x4)(lds + x * (4 * COLS) + ((c ^ (x & 15)) * 16));
       if constexpr (kPaired)
-        up[k] = *(const f32x4*)(lds + x * (4 * COLS) + (((c + kLanes) ^ (x & 15)) * 16));
+        up[k] = *(lds_f32x4)(lds + x * (4 * COLS) + (((c + kLanes) ^ (x & 15)) * 16));
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -387,38 +390,43 @@ __device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
   return TileId{g * 8 + (t - g * group) % h, (t - g * group) / h};
 }
 
+// The 128 x 128 tile's ring of four stages: an object a stage and operand, so
+// that the compiler sees which copies a read has to wait for.
+struct Ring {
+  lds_bytes a0, a1, a2, a3, b0, b1, b2, b3, s0, s1, s2, s3;
+};
+#define FFN_RING(ring, scales)                                                        \
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[128 * kRow], sa1[128 * kRow]; \
+  __shared__ __attribute__((aligned(1024))) uint8_t sa2[128 * kRow], sa3[128 * kRow]; \
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[128 * kRow], sb1[128 * kRow]; \
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[128 * kRow], sb3[128 * kRow]; \
+  __shared__ __attribute__((aligned(16))) uint8_t ss0[scales], ss1[scales];           \
+  __shared__ __attribute__((aligned(16))) uint8_t ss2[scales], ss3[scales];           \
+  const Ring ring = {(lds_bytes)sa0, (lds_bytes)sa1, (lds_bytes)sa2, (lds_bytes)sa3,  \
+                     (lds_bytes)sb0, (lds_bytes)sb1, (lds_bytes)sb2, (lds_bytes)sb3,  \
+                     (lds_bytes)ss0, (lds_bytes)ss1, (lds_bytes)ss2, (lds_bytes)ss3};
+
+#if defined(__HIP_DEVICE_COMPILE__)
 // Tile of 128 x (2 x 64): four waves (2 x 2) of 64 rows x (2 x 32) columns, for
 // launches that leave CUs idle: a ring of four stages, copied three ahead,
-// and one barrier a stage. blockIdx.y is the work-group's share of K.
+// and one barrier a stage. The stages from `first`, at most `share` of them.
 template <Kind KA, Kind KB, bool MX, Epilogue EPI>
-__global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
-#if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int64_t id, int first,
+                                          int share) {
   constexpr int NW = 4, HRA = 128, HRB = 64, FA = 4, FB = 2;
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
   constexpr int kCols = kPaired ? HRB : 2 * HRB;  // output columns
   typedef Half<KA, HRA, NW> HA;
   typedef Half<KB, HRB, NW> HB;
-  // an object a stage and operand: the compiler then sees which copies a read has to wait for
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[HA::kBytes], sa1[HA::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sa2[HA::kBytes], sa3[HA::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[2 * HB::kBytes], sb1[2 * HB::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb2[2 * HB::kBytes], sb3[2 * HB::kBytes];
-  constexpr int kScales = MX ? 8 * (HRA + 2 * HRB) : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t ss0[kScales], ss1[kScales];
-  __shared__ __attribute__((aligned(16))) uint8_t ss2[kScales], ss3[kScales];
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t rows = p.m_end - p.m_first;
   const int64_t tm = (rows + HRA - 1) / HRA, tn = (p.N + kCols - 1) / kCols;
-  const TileId t = tile_of(blockIdx.x, tm, tn);
+  const TileId t = tile_of(id, tm, tn);
   const int64_t m0 = p.m_first + t.m * HRA, n0 = t.n * kCols;
-  const int first = blockIdx.y * share;  // stages [first, first + count)
   const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
   const int count = stages - first < share ? stages - first : share;
-  if constexpr (EPI == kPartial || EPI == kPartialPaired)
-    p.out = (float*)p.out + ((int64_t)blockIdx.y * rows - p.m_first) * p.N * (kPaired ? 2 : 1);
-
   HA a;
   HB b0, b1;
   Lane<KA, HRA, NW> la;
@@ -454,9 +462,9 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
   constexpr int kCopies = HA::kPer + 2 * HB::kPer;
   auto copy = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
-    uint8_t* sa = buf == 0 ? sa0 : buf == 1 ? sa1 : buf == 2 ? sa2 : sa3;
-    uint8_t* sb = buf == 0 ? sb0 : buf == 1 ? sb1 : buf == 2 ? sb2 : sb3;
-    uint8_t* ss = buf == 0 ? ss0 : buf == 1 ? ss1 : buf == 2 ? ss2 : ss3;
+    const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
+    const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
+    const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
     if constexpr (MX) {
       if (wave == 0) sca.template copy<HRA>(ss, s, lane);
       if (wave == 1) scb0.template copy<HRB>(ss + 8 * HRA, s, lane);
@@ -468,9 +476,9 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
   };
   auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
-    const uint8_t* sa = buf == 0 ? sa0 : buf == 1 ? sa1 : buf == 2 ? sa2 : sa3;
-    const uint8_t* sb = buf == 0 ? sb0 : buf == 1 ? sb1 : buf == 2 ? sb2 : sb3;
-    const uint8_t* ss = buf == 0 ? ss0 : buf == 1 ? ss1 : buf == 2 ? ss2 : ss3;
+    const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
+    const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
+    const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
     wait_vm<2 * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
@@ -513,29 +521,63 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
   const int r = lane & 15, q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < FA; ++i) {  // 32 rows of 128 columns an object
-    uint8_t* row = (i < 2 ? (wm ? sa2 : sa0) : (wm ? sa3 : sa1)) + ((i & 1) * 16 + r) * 512;
+    const lds_bytes row = (i < 2 ? (wm ? at.a2 : at.a0) : (wm ? at.a3 : at.a1)) + ((i & 1) * 16 + r) * 512;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < FB; ++j)
-        *(f32x4*)(row + (((h * 16 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][i][j];
+        *(lds_f32x4)(row + (((h * 16 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][i][j];
   }
   wait_lgkm0();
   __builtin_amdgcn_s_barrier();
-  store_rows<EPI, 128>(p, wave < 2 ? (wave == 0 ? sa0 : sa1) : (wave == 2 ? sa2 : sa3),
+  store_rows<EPI, 128>(p, wave < 2 ? (wave == 0 ? at.a0 : at.a1) : (wave == 2 ? at.a2 : at.a3),
                        m0 + wave * 32, n0, lane);
+}
+#endif
+
+template <Kind KA, Kind KB, bool MX, Epilogue EPI>
+__global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (EPI == kPartial || EPI == kPartialPaired)  // blockIdx.y: the share
+    p.out = (float*)p.out + ((int64_t)blockIdx.y * (p.m_end - p.m_first) - p.m_first) * p.N *
+                                (EPI == kPartialPaired ? 2 : 1);
+  FFN_RING(ring, MX ? 256 * 8 : 16)
+  tile_body<KA, KB, MX, EPI>(p, ring, blockIdx.x, blockIdx.y * share, share);
 #endif
 }
 
-// Adds the shares of K in their order and finishes: one lane four columns of a
-// row; eight lanes a block where h is quantised.
+// The backward pass's last three products in one launch: the tiles of each,
+// share by share, follow those of the one before.
+struct Gradients {
+  Product product[3];  // dx (NN), dw13, dw2 (TN); aux: the shares' sums, if any
+  int first[3];        // their first work-groups
+  int tiles[3], share[3];
+};
+__global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FFN_RING(ring, 16)
+  const int group = blockIdx.x;
+  const int i = uniform(group < g.first[1] ? 0 : group < g.first[2] ? 1 : 2);
+  const int id = uniform((group - g.first[i]) % g.tiles[i]);
+  const int share = uniform((group - g.first[i]) / g.tiles[i]);
+  Product p = g.product[i];
+  if (p.aux) p.aux = (float*)p.aux + share * p.M * p.N;
+  if (i == 0)
+    tile_body<KC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+  else
+    tile_body<RC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+#endif
+}
+#undef FFN_RING
+
+// Adds the shares of K in their order and finishes: one lane (u of the product's)
+// four columns of a row; eight lanes a block where h is quantised.
 template <Epilogue EPI>
-__global__ __launch_bounds__(256) void join_kernel(const Product p, const float* __restrict__ sums,
-                                                   int shares) {
+__device__ __forceinline__ void join_quad(const Product& p, const float* __restrict__ sums,
+                                          int shares, int64_t u) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx;
   const int64_t quads = p.N / 4;
-  const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t rows = p.m_end - p.m_first;
   if (u >= rows * quads) return;  // N is a multiple of 32 where lanes work together
   const int64_t row = u / quads, m = p.m_first + row, n = (u - row * quads) * 4;
@@ -559,13 +601,25 @@ __global__ __launch_bounds__(256) void join_kernel(const Product p, const float*
   }
 #endif
 }
+template <Epilogue EPI>
+__global__ __launch_bounds__(256) void join_kernel(const Product p, const float* __restrict__ sums,
+                                                   int shares) {
+  join_quad<EPI>(p, sums, shares,
+                 ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x);
+}
+__global__ __launch_bounds__(256) void gradients_join_kernel(const Gradients g, const int s0,
+                                                             const int s1, const int s2) {
+  const int i = (int)blockIdx.x < g.first[1] ? 0 : (int)blockIdx.x < g.first[2] ? 1 : 2;
+  join_quad<kStoreBf16>(g.product[i], (const float*)g.product[i].aux, i == 0 ? s0 : i == 1 ? s1 : s2,
+                        (int64_t)((int)blockIdx.x - g.first[i]) * 256 + threadIdx.x);
+}
 
 // Tile of (AH x 128) x (2 x 128), eight waves (2 x 4), each 64 rows of every A
 // half x 32 columns of both B halves. A phase is one A half against both B
 // halves, 32 MFMAs (512 cycles) a wave. The two waves of a SIMD run half a
 // phase apart: one reads fragments and issues copies while the other's MFMAs
-// run, with a barrier after each of the two parts. A half tile is copied into its own place as soon as the phase that
-// read it is over.
+// run, with a barrier after each of the two parts. A half tile is copied into
+// its own place as soon as the phase that read it is over.
 //
 //   AH  buffers  phase  reads      copies                 waits for (at its end)
 //   2   2        0      A0 B0 B1   A1 of stage s + 1      A1 of s
@@ -574,7 +628,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Product p, const float*
 //
 // A part's LDS reads complete before its barrier, so the place is free for the
 // copies of the next phase; a copy is waited for before a barrier that every
-// wave passes ahead of its reads. Copies have 1.5 (AH = 1: 2) stages to arrive.
+// wave passes ahead of its reads. Copies have 1.25 (AH = 1: 2) stages to arrive.
 template <int AH, Kind KA, Kind KB, bool MX, Epilogue EPI>
 __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -585,15 +639,19 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   typedef Half<KB, HR, NW> HB;
   constexpr int kCopies = HA::kPer;  // per half tile and wave
   // an object a half tile: the compiler then sees which copies a read has to wait for
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[HA::kBytes], sb0[HB::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sc0[HB::kBytes], sa1[HA::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb1[HB::kBytes], sc1[HB::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t msa0[HA::kBytes], msb0[HB::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t msc0[HB::kBytes], msa1[HA::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t msb1[HB::kBytes], msc1[HB::kBytes];
   // AH = 2: the second A halves of the two buffers; AH = 1: the third buffer
-  __shared__ __attribute__((aligned(1024))) uint8_t sx0[HA::kBytes], sx1[HB::kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t sx2[AH == 1 ? HB::kBytes : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t msx0[HA::kBytes], msx1[HB::kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t msx2[AH == 1 ? HB::kBytes : 16];
   constexpr int kScales = MX ? 8 * (AH + 2) * HR : 16;
-  __shared__ __attribute__((aligned(16))) uint8_t ss0[kScales], ss1[kScales];
-  __shared__ __attribute__((aligned(16))) uint8_t ss2[AH == 1 ? kScales : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t mss0[kScales], mss1[kScales];
+  __shared__ __attribute__((aligned(16))) uint8_t mss2[AH == 1 ? kScales : 16];
+  const lds_bytes sa0 = (lds_bytes)msa0, sb0 = (lds_bytes)msb0, sc0 = (lds_bytes)msc0;
+  const lds_bytes sa1 = (lds_bytes)msa1, sb1 = (lds_bytes)msb1, sc1 = (lds_bytes)msc1;
+  const lds_bytes sx0 = (lds_bytes)msx0, sx1 = (lds_bytes)msx1, sx2 = (lds_bytes)msx2;
+  const lds_bytes ss0 = (lds_bytes)mss0, ss1 = (lds_bytes)mss1, ss2 = (lds_bytes)mss2;
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -627,7 +685,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     scales[AH].init(p.b_scales, 0, n0, p.N, all, p.K);
     scales[AH + 1].init(p.b_scales, kPaired ? p.N : 0, kPaired ? n0 : n0 + HR, p.N, all, p.K);
   }
-  auto copy_scales = [&](uint8_t* ss, int stage) {
+  auto copy_scales = [&](lds_bytes ss, int stage) {
     if constexpr (MX) {
 #pragma unroll
       for (int i = 0; i < AH + 2; ++i)
@@ -682,10 +740,10 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     constexpr int two = (buf + 2) % 3;  // AH = 1: the buffer of stage s + 2
-    uint8_t* a_now = buf == 0 ? sa0 : buf == 1 ? sa1 : sx0;
-    uint8_t* b0_now = buf == 0 ? sb0 : buf == 1 ? sb1 : sx1;
-    uint8_t* b1_now = buf == 0 ? sc0 : buf == 1 ? sc1 : sx2;
-    uint8_t* ss_now = buf == 0 ? ss0 : buf == 1 ? ss1 : ss2;
+    const lds_bytes a_now = buf == 0 ? sa0 : buf == 1 ? sa1 : sx0;
+    const lds_bytes b0_now = buf == 0 ? sb0 : buf == 1 ? sb1 : sx1;
+    const lds_bytes b1_now = buf == 0 ? sc0 : buf == 1 ? sc1 : sx2;
+    const lds_bytes ss_now = buf == 0 ? ss0 : buf == 1 ? ss1 : ss2;
     fa.read(a_now, wm * 64, lane);
     fb0.read(b0_now, wn * 32, lane);
     fb1.read(b1_now, wn * 32, lane);
@@ -753,23 +811,23 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 
   // an A half at a time: 128 rows of 256 columns, 16 an object
   const int r = lane & 15, q = lane >> 4;
-  uint8_t* const w0 = wm ? sb1 : sa0;
-  uint8_t* const w1 = wm ? sc1 : sb0;
-  uint8_t* const w2 = wm ? sx0 : sc0;
-  uint8_t* const w3 = wm ? sx1 : sa1;
-  const uint8_t* mine = wave < 4 ? (wave < 2 ? (wave == 0 ? sa0 : sb0) : (wave == 2 ? sc0 : sa1))
+  const lds_bytes w0 = wm ? sb1 : sa0;
+  const lds_bytes w1 = wm ? sc1 : sb0;
+  const lds_bytes w2 = wm ? sx0 : sc0;
+  const lds_bytes w3 = wm ? sx1 : sa1;
+  const lds_bytes mine = wave < 4 ? (wave < 2 ? (wave == 0 ? sa0 : sb0) : (wave == 2 ? sc0 : sa1))
                                  : (wave < 6 ? (wave == 4 ? sb1 : sc1) : (wave == 6 ? sx0 : sx1));
 #pragma unroll
   for (int h = 0; h < AH; ++h) {
     __builtin_amdgcn_s_barrier();  // every wave is done with what the LDS held
 #pragma unroll
     for (int i = 0; i < FA; ++i) {
-      uint8_t* row = (i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : w3) + r * 1024;
+      const lds_bytes row = (i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : w3) + r * 1024;
 #pragma unroll
       for (int hb = 0; hb < 2; ++hb)
 #pragma unroll
         for (int j = 0; j < FB; ++j)
-          *(f32x4*)(row + (((hb * 32 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][hb][i][j];
+          *(lds_f32x4)(row + (((hb * 32 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][hb][i][j];
     }
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
@@ -836,6 +894,34 @@ hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, vo
   if (layout == kTN && epilogue == kStoreBf16)
     return launch<kTN, false, kStoreBf16>(p, split, stream);
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_gradients(const GradientsPlan& plan, const Product (&products)[3], void* split,
+                            hipStream_t stream) {
+  Gradients g = {};
+  int groups = 0;
+  for (int i = 0; i < 3; ++i) {
+    const Cut& c = plan.cut[i];
+    g.product[i] = products[i];
+    g.product[i].m_end = products[i].M;
+    g.product[i].aux = c.shares > 1 ? (char*)split + plan.sums[i] : nullptr;
+    g.first[i] = groups;
+    g.tiles[i] = (int)c.groups;
+    g.share[i] = c.share;
+    groups += (int)c.groups * c.shares;
+  }
+  hipLaunchKernelGGL(gradients_kernel, dim3(groups), dim3(256), 0, stream, g);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !plan.bytes) return e;
+  groups = 0;
+  for (int i = 0; i < 3; ++i) {
+    g.first[i] = groups;
+    if (plan.cut[i].shares > 1)
+      groups += (int)((products[i].M * (products[i].N / 4) + 255) / 256);
+  }
+  hipLaunchKernelGGL(gradients_join_kernel, dim3(groups), dim3(256), 0, stream, g,
+                     plan.cut[0].shares, plan.cut[1].shares, plan.cut[2].shares);
+  return hipGetLastError();
 }
 
 hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,

@@ -18,6 +18,7 @@ enum Epilogue {
   kSwigluF32 = 5,   // out fp32 h [M, N]
   kPartial = 6,     // a share of K: fp32 sums [share][M, N] in out
   kPartialPaired = 7,  // fp32 gate and up sums [share][M, 2N]
+  kStoreOrSums = 8,    // as kStoreBf16, or where aux is given fp32 sums [share][M, N] there
 };
 
 // D[m, n] = sum_k A(m, k) B(n, k). An operand is "K contiguous" (element
@@ -56,6 +57,7 @@ hipError_t launch_product(Layout layout, Epilogue epilogue, const Product& p, vo
 // MXFP4 operands, both K contiguous; K a multiple of 32
 hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
                              hipStream_t stream);
+
 // How a tiled product is cut (ffn_plan.cpp): the tile (0: 128 x 128, 1: 128 x
 // 256, 2: 256 x 256; half the columns where gate and up pair), its work-groups,
 // and for tile 0 the shares of K, `share` stages each.
@@ -74,6 +76,19 @@ Plan plan_of(Epilogue epilogue, int64_t M, int64_t N, int64_t K, Layout layout, 
 size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
                          bool mx);
 double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
+
+// The backward pass's last three products (dx: NN; dw13, dw2: TN; bf16 results)
+// in one launch of 128 x 128 tiles, each with its own shares of K, and one that
+// adds the sums: `together` where that is the faster way. sums: where in
+// `split` (`bytes` in all) the sums of a product with shares lie.
+struct GradientsPlan {
+  bool together = false;
+  Cut cut[3];
+  size_t sums[3] = {}, bytes = 0;
+};
+GradientsPlan gradients_plan(int64_t tokens, int64_t hidden, int64_t inter);
+hipError_t launch_gradients(const GradientsPlan& plan, const Product (&products)[3], void* split,
+                            hipStream_t stream);
 
 // The same products for a few rows (ffn_small.hip), both operands K contiguous
 // and dense. A: as the product takes it, or rows to be quantised to MXFP4.

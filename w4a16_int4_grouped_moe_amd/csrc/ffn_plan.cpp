@@ -90,6 +90,56 @@ double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int6
   return plan_of(epilogue, M, N, K, layout, mx).time;
 }
 
+// All three shares of K are cut to about one length. In one launch no product
+// waits for another: a round is as long as the longest share, more rounds are
+// the CUs' parts of all the work and about half a share with some CUs idle.
+// Whole backward pass, three launches -> one (microseconds): 201 tokens at
+// 1000/680 43 -> 29, 1000 at 1000/680 68 -> 43, 2000 at 512/128 47 -> 29, 700 at
+// 2048/768 67 -> 47; where tiles are many the three win (4096 at 7168/2048), and
+// near the border the estimate is off by up to 3% (3000 at 1000/680 103 -> 107).
+GradientsPlan gradients_plan(int64_t tokens, int64_t hidden, int64_t inter) {
+  const int64_t sizes[3][3] = {{tokens, hidden, 2 * inter},
+                               {2 * inter, hidden, tokens},
+                               {hidden, inter, tokens}};  // M, N, K
+  GradientsPlan best;
+  if (tokens == 0) return best;
+  const Rate& rate = kRates[1];
+  int64_t tiles[3], stages[3], all = 0, longest = 0;
+  double least = 0;  // of the products by themselves
+  for (int i = 0; i < 3; ++i) {
+    const int64_t M = sizes[i][0], N = sizes[i][1], K = sizes[i][2];
+    tiles[i] = ((M + 127) / 128) * ((N + 127) / 128);
+    stages[i] = (K + 63) / 64;
+    all += tiles[i];
+    longest = std::max(longest, stages[i]);
+    least += product_time(i ? kTN : kNN, kStoreBf16, M, (int32_t)N, K, false);
+  }
+  if (all > 1024) return best;
+  for (int64_t length = longest; length >= 2; length -= (length + 3) / 4) {
+    GradientsPlan plan;
+    plan.together = true;
+    int64_t groups = 0;
+    double work = 0, most = 0;
+    for (int i = 0; i < 3; ++i) {
+      Cut& c = plan.cut[i];
+      const int64_t shares = (stages[i] + length - 1) / length;
+      const int64_t share = (stages[i] + shares - 1) / shares;
+      c = Cut{0, (int)((stages[i] + share - 1) / share), (int)share, tiles[i]};
+      c.time = share * rate.stage[0] + rate.fixed[0];
+      groups += c.groups * c.shares;
+      work += c.time * c.groups * c.shares / 256;
+      most = std::max(most, c.time);
+      plan.sums[i] = plan.bytes;
+      if (c.shares > 1) plan.bytes += 4 * sizes[i][0] * sizes[i][1] * c.shares;
+    }
+    if (groups > 1024) break;
+    const double time = (groups <= 256 ? most : work + most / 2) +
+                        (plan.bytes ? 6.0 + 2 * plan.bytes / 4e6 : 0.0);
+    if (time < least) least = time, best = plan;
+  }
+  return best;
+}
+
 bool rows_fit(const Product& p, bool mx, AType a, bool paired) {
   const int64_t kb = mx ? p.K / 2 : 2 * p.K;
   return p.M >= 1 && p.M <= (a == kABf16 ? 16 : kMaxRows) &&
