@@ -393,17 +393,20 @@ __device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
 // The 128 x 128 tile's ring of four stages: an object a stage and operand, so
 // that the compiler sees which copies a read has to wait for.
 struct Ring {
-  lds_bytes a0, a1, a2, a3, b0, b1, b2, b3, s0, s1, s2, s3;
+  lds_bytes a0, a1, a2, a3, b0, b1, b2, b3, c0, c1, c2, c3, s0, s1, s2, s3;
 };
 #define FFN_RING(ring, scales)                                                        \
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[128 * kRow], sa1[128 * kRow]; \
   __shared__ __attribute__((aligned(1024))) uint8_t sa2[128 * kRow], sa3[128 * kRow]; \
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[128 * kRow], sb1[128 * kRow]; \
-  __shared__ __attribute__((aligned(1024))) uint8_t sb2[128 * kRow], sb3[128 * kRow]; \
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[64 * kRow], sb1[64 * kRow];   \
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[64 * kRow], sb3[64 * kRow];   \
+  __shared__ __attribute__((aligned(1024))) uint8_t sc0[64 * kRow], sc1[64 * kRow];   \
+  __shared__ __attribute__((aligned(1024))) uint8_t sc2[64 * kRow], sc3[64 * kRow];   \
   __shared__ __attribute__((aligned(16))) uint8_t ss0[scales], ss1[scales];           \
   __shared__ __attribute__((aligned(16))) uint8_t ss2[scales], ss3[scales];           \
   const Ring ring = {(lds_bytes)sa0, (lds_bytes)sa1, (lds_bytes)sa2, (lds_bytes)sa3,  \
                      (lds_bytes)sb0, (lds_bytes)sb1, (lds_bytes)sb2, (lds_bytes)sb3,  \
+                     (lds_bytes)sc0, (lds_bytes)sc1, (lds_bytes)sc2, (lds_bytes)sc3,  \
                      (lds_bytes)ss0, (lds_bytes)ss1, (lds_bytes)ss2, (lds_bytes)ss3};
 
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -464,6 +467,7 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     constexpr int buf = decltype(buffer)::value;
     const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
     const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
+    const lds_bytes sc = buf == 0 ? at.c0 : buf == 1 ? at.c1 : buf == 2 ? at.c2 : at.c3;
     const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
     if constexpr (MX) {
       if (wave == 0) sca.template copy<HRA>(ss, s, lane);
@@ -472,12 +476,13 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     }
     a.copy(sa, s, wave, la);
     b0.copy(sb, s, wave, lb);
-    b1.copy(sb + HB::kBytes, s, wave, lb);
+    b1.copy(sc, s, wave, lb);
   };
   auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
     const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
+    const lds_bytes sc = buf == 0 ? at.c0 : buf == 1 ? at.c1 : buf == 2 ? at.c2 : at.c3;
     const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
     wait_vm<2 * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
     wait_lgkm0();
@@ -489,7 +494,7 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     Frags<KB, HRB, FB> fb0, fb1;
     fa.read(sa, wm * 64, lane);
     fb0.read(sb, wn * 32, lane);
-    fb1.read(sb + HB::kBytes, wn * 32, lane);
+    fb1.read(sc, wn * 32, lane);
     u32x2 sm = {};
     uint32_t sn0 = 0, sn1 = 0;
     if constexpr (MX) {

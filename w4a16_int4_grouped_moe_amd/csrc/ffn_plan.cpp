@@ -18,7 +18,7 @@ struct Rate {
   double stage[3], fixed[3];
 };
 constexpr Rate kRates[3] = {{{0.62, 0.88, 1.42}, {4.5, 4.5, 7.0}},
-                            {{0.92, 0.85, 1.42}, {4.0, 5.0, 7.0}},
+                            {{0.70, 0.85, 1.42}, {4.0, 5.0, 7.0}},
                             {{0.85, 1.20, 1.80}, {4.5, 4.5, 8.0}}};
 // The cheapest cut. Shares of K cost a launch and the sums' way to memory and
 // back (about 4 TB/s); of equals the larger tile.
@@ -33,18 +33,21 @@ Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx
   auto time = [&](int tile, int64_t groups, int64_t st) {
     return (double)((groups + 255) / 256) * (st * rate.stage[tile] + rate.fixed[tile]);
   };
+  // a tile's pre-activations on their way, which the join of shares reads at full rate
+  const double grad = epi == kSwigluGrad ? 4.0 : 0.0;
   const int64_t n[3] = {tiles(128, 128), tiles(128, 256), tiles(256, 256)};
   Cut best{2, 1, (int)stages, n[2]};
-  double least = time(2, n[2], stages);
-  if (time(1, n[1], stages) < least) {
-    least = time(1, n[1], stages);
+  double least = time(2, n[2], stages) + grad;
+  if (time(1, n[1], stages) + grad < least) {
+    least = time(1, n[1], stages) + grad;
     best = Cut{1, 1, (int)stages, n[1]};
   }
   for (int shares = 1; shares <= 32 && n[0] * shares <= 1024; ++shares) {
     const int64_t share = (stages + shares - 1) / shares;
     if (shares > 1 && (2 * shares > stages || share * (shares - 1) >= stages)) continue;
     const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
-    const double t = time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : 0.0);
+    const double t =
+        time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : grad);
     if (t < least) least = t, best = Cut{0, shares, (int)share, n[0]};
   }
   best.time = least;
@@ -94,9 +97,8 @@ double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int6
 // waits for another: a round is as long as the longest share, more rounds are
 // the CUs' parts of all the work and about half a share with some CUs idle.
 // Whole backward pass, three launches -> one (microseconds): 201 tokens at
-// 1000/680 43 -> 29, 1000 at 1000/680 68 -> 43, 2000 at 512/128 47 -> 29, 700 at
-// 2048/768 67 -> 47; where tiles are many the three win (4096 at 7168/2048), and
-// near the border the estimate is off by up to 3% (3000 at 1000/680 103 -> 107).
+// 1000/680 42 -> 29, 1000 at 1000/680 64 -> 38, 2000 at 512/128 46 -> 28, 700 at
+// 2048/768 62 -> 42, 8192 at 512/512 82 -> 71, 4096 at 2048/256 77 either way.
 GradientsPlan gradients_plan(int64_t tokens, int64_t hidden, int64_t inter) {
   const int64_t sizes[3][3] = {{tokens, hidden, 2 * inter},
                                {2 * inter, hidden, tokens},
