@@ -33,7 +33,7 @@
  *
  * Limits: hidden, inter and width at most 2^20; hidden and inter multiples of
  * 8 (bf16) or 32 (MXFP4), cols a multiple of 8, width a multiple of 32;
- * num_tokens and rows below 2^31.
+ * num_tokens and rows at most 2^31 - 256.
  */
 #ifndef MOE_FFN_H
 #define MOE_FFN_H
@@ -78,7 +78,8 @@ int moe_ffn_forward(const void *x, const void *w13, const void *w2, void *out, f
  * [T, H], dw13 [2I, H], dw2 [H, I], written (not added to). gate_up: what
  * moe_ffn_forward wrote for the same x and w13. The gradients of g and u and
  * the recomputed h are each rounded once to bf16 before the last products.
- * dx, or both of dw13 and dw2, may be NULL: that part is then not computed.
+ * dx, or both of dw13 and dw2, may be NULL: that part is then not computed (and
+ * the sums of the other may be added in another order).
  * T == 0 clears dw13 and dw2.
  */
 int moe_ffn_backward(const void *dout, const void *x, const float *gate_up, const void *w13,

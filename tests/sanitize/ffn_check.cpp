@@ -260,6 +260,19 @@ int main() {
   for (int64_t M : {1, 16, 127, 128, 129, 700, 4096, 4100, 7168, 131072, 3000000})
     for (int64_t N : {8, 64, 200, 680, 2048, 2112, 7168, 100000})
       for (int64_t K : {0, 8, 64, 200, 2048, 7168, 1 << 20, 2000000}) plan(M, N, K);
+  // the most rows, narrow enough to exist: every launch's lanes fit 32 bits
+  const int64_t most = (int64_t(1) << 31) - 256;
+  block(most, 8, 8);
+  block(most, 32, 32);
+  product(most, 8, 32);
+  for (int64_t n : {8, 32, 64, 72})
+    for (int64_t k : {8, 32, 64, 72})
+      for (int mx = 0; mx < 2; ++mx)
+        for (int l = 0; l < (mx ? 1 : 2); ++l)
+          for (ffn::Epilogue e : {ffn::kStoreBf16, ffn::kSwiglu}) {
+            const ffn::Plan p = ffn::plan_of(e, most, n, k, (ffn::Layout)l, mx);
+            expect(p.whole.groups <= 0x7fffff && p.rest.groups <= 0x7fffff, "lanes of a launch");
+          }
   std::printf("cases: %d launches: %d failed: %d\n", cases, launches, failed);
   return failed ? 1 : 0;
 }

@@ -72,6 +72,17 @@ def test_bad_sizes(lib, T, H, I, multiple):
             moe.MOE_ERR_SHAPE
 
 
+def test_the_largest_token_count(lib):
+    n = ctypes.c_size_t(0)
+    for kind, width in ((moe.MOE_FFN_FORWARD, 8), (moe.MOE_FFN_BACKWARD, 8),
+                        (moe.MOE_FFN_FORWARD_MXFP4, 32)):
+        for T, status in (((1 << 31) - 256, moe.MOE_OK), ((1 << 31) - 255, moe.MOE_ERR_SHAPE)):
+            p = problem(T, width, width)
+            assert lib.moe_ffn_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)) == status
+    for rows, status in (((1 << 31) - 256, moe.MOE_OK), ((1 << 31) - 255, moe.MOE_ERR_SHAPE)):
+        assert lib.moe_mxfp4_matmul_workspace_size(rows, 8, 32, 1, ctypes.byref(n)) == status
+
+
 def test_workspace_size_arguments(lib):
     n = ctypes.c_size_t(0)
     p = problem()

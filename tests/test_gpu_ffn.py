@@ -133,6 +133,54 @@ def test_backward_products_in_one_launch(T, H, I):
     assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("T,H,I", [(20, 696, 256), (201, 1000, 680), (300, 64, 64)])
+@pytest.mark.parametrize("part", ["dx", "weights"])
+def test_parts_of_the_gradients(T, H, I, part):
+    """dx alone, or dw13 and dw2 alone: those are right and nothing else is written."""
+    from w4a16_int4_grouped_moe_amd import _ffn
+
+    x, w13, w2, d = inputs(T, H, I, seed=13)
+    gu = x.float() @ w13.float().T
+    want = reference_backward(d, x, gu, w13, w2)
+    outs = [guarded(s, torch.bfloat16) for s in ((T, H), (2 * I, H), (H, I))]
+    asked = [part == "dx", part != "dx", part != "dx"]
+    p, need = _ffn._problem(T, H, I, moe.MOE_FFN_BACKWARD)
+    ws, ws_ok = guarded((need,), torch.uint8)
+    _ffn._launch(x.device, _ffn._library().moe_ffn_backward, d.data_ptr(), x.data_ptr(),
+                 gu.data_ptr(), w13.data_ptr(), w2.data_ptr(),
+                 *(o.data_ptr() if a else None for (o, _), a in zip(outs, asked)), p,
+                 ws.data_ptr(), need)
+    for (value, intact), (ref, tol), a in zip(outs, want, asked):
+        if a:
+            close(value, ref, tol)
+        else:
+            assert (value == 7).all()
+        assert intact()
+    assert ws_ok()
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    T, H, I = 201, 1000, 680
+    sets = [inputs(T, H, I, seed=s) for s in (14, 15)]
+
+    def step(x, w13, w2, d):
+        gu = torch.empty(T, 2 * I, device="cuda")
+        return (moe.ffn_forward(x, w13, w2, gate_up=gu), *moe.ffn_backward(d, x, gu, w13, w2))
+
+    alone = [step(*s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for stream, s in zip(streams, sets):
+            with torch.cuda.stream(stream):
+                got.append(step(*s))
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(v, w) for v, w in zip(a, b))
+
+
 def test_gradients_against_differences():
     """sum(out * dout) changes along a direction as the gradients say (central differences of the
     fp64 block; the gradients' own error is their bound summed over the direction)."""
