@@ -79,23 +79,23 @@ struct Half {
   static constexpr int kBytes = HR * kRow;
   static constexpr int kPer = Lane<KIND, HR, NW>::kPer;
   const uint8_t* base;
-  int64_t ld;
-  int64_t kleft;    // KC: bytes of a row (fits 32 bits); RC: k-rows
+  int64_t pitch;    // RC: bytes of a stage
+  int32_t end;      // KC: bytes of a row; RC: k-rows
+  int32_t span;     // RC: bytes from a k-row to the next, 0 where the half has no rows
   int32_t records;  // KC: bytes that may be read; RC: bytes of a k-row
 
   // rows [row0, row0 + HR) of an operand of `rows` rows; K: bytes per row (KC) or k-rows (RC),
   // of which the first `end` are read
-  __device__ __forceinline__ void init(const void* ptr, int64_t row0, int64_t rows, int64_t ld_,
-                                       int64_t K, int64_t end) {
-    ld = ld_;
-    kleft = end;
+  __device__ __forceinline__ void init(const void* ptr, int64_t row0, int64_t rows, int64_t ld,
+                                       int64_t K, int64_t end_) {
+    end = (int32_t)end_;
     const int64_t left = rows - row0;
     const int valid = left <= 0 ? 0 : left < HR ? (int)left : HR;
     base = (const uint8_t*)ptr + (valid ? row0 * (KIND == KC ? ld : 2) : 0);
     if constexpr (KIND == KC)
       records = valid ? (int32_t)((valid - 1) * ld + K) : 0;
     else
-      records = 2 * valid;
+      records = 2 * valid, span = valid ? (int32_t)ld : 0, pitch = 64 * ld;
   }
 
   __device__ __forceinline__ void copy(lds_bytes slot, int stage, int wave,
@@ -104,20 +104,20 @@ struct Half {
     if constexpr (KIND == KC) {
       const __amdgpu_buffer_rsrc_t res =
           __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records, kBufferFlags);
-      const int k0 = stage * kRow, end = (int)kleft - k0;
+      const int k0 = stage * kRow, left = end - k0;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const bool in = (at.piece ^ ((j & 1) * 64)) < end;
+        const bool in = (at.piece ^ ((j & 1) * 64)) < left;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_ptr)(dst + j * 1024), 16,
                                                  in ? at.off[j] + (uint32_t)k0 : kOut, 0, 0, 0);
       }
     } else {
-      const int64_t left = kleft - (int64_t)stage * 64;
-      const int32_t n =
-          left <= 0 ? 0 : (int32_t)(((left < 64 ? left : 64) - 1) * ld) + records;
+      // the end of the stage's last k-row; past K (by three stages at most) below 0. Without a
+      // branch, behind which the compiler would no longer know how many copies are in flight.
+      const int left = end - stage * 64;
+      const int bytes = ((left < 64 ? left : 64) - 1) * span + records;
       const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + (left > 0 ? (int64_t)stage * 64 * ld : 0)), 0, records ? n : 0,
-          kBufferFlags);
+          (void*)(base + stage * pitch), 0, bytes < 0 ? 0 : bytes, kBufferFlags);
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_ptr)(dst + j * 1024), 16, at.off[j],
@@ -197,28 +197,29 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB
 }
 #endif
 
-// The MXFP4 scales of a half tile's rows, one stage: 8 bytes a row, copied by
-// one wave (HR / 2 lanes of 16 bytes).
-struct HalfScales {
+// The MXFP4 scales that a wave copies, 8 bytes a row and stage: 64 rows of a
+// tile (or none), so that every wave has one such copy a stage in flight.
+struct WaveScales {
   const uint8_t* base;
   int64_t pitch;  // bytes of a stage
-  int32_t records;
-  int last;
-  // rows from row0 of a matrix whose `rows` rows from `first` are the half's operand
+  int32_t records, last, lanes, at;
+  // rows from row0 of an operand, which is `rows` rows from `first` of a matrix of `all`; at:
+  // their place in the LDS object
   __device__ __forceinline__ void init(const uint8_t* scales, int64_t first, int64_t row0,
-                                       int64_t rows, int64_t all, int64_t K) {
+                                       int64_t rows, int64_t all, int64_t K, int at_, bool any) {
     pitch = 8 * scale_rows(all);
     last = (int)scale_stages(K) - 1;
     const int64_t left = rows - row0;
-    records = left <= 0 ? 0 : (int32_t)((left < 128 ? scale_rows(left) : 128) * 8);
+    records = left <= 0 ? 0 : (int32_t)((left < 64 ? scale_rows(left) : 64) * 8);
     base = scales + (left > 0 ? first + row0 : 0) * 8;
+    lanes = any ? 32 : 0;
+    at = at_;
   }
-  template <int HR>
   __device__ __forceinline__ void copy(lds_bytes slot, int stage, int lane) const {
     const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
         (void*)(base + (stage < last ? stage : last) * pitch), 0, records, kBufferFlags);
-    if (lane < HR / 2)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_ptr)slot, 16, 16 * lane, 0, 0, 0);
+    if (lane < lanes)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(res, (lds_ptr)(slot + at), 16, 16 * lane, 0, 0, 0);
   }
 };
 
@@ -446,12 +447,13 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, kb, kb < eb ? kb : eb);
   else
     b1.init(p.b, n0 + HRB, p.N, p.ldb, kb, kb < eb ? kb : eb);
-  HalfScales sca, scb0, scb1;
+  WaveScales scales;  // waves 0 and 1: A's rows; 2 and 3: the halves of B's
   if constexpr (MX) {
+    const bool of_a = wave < 2;
     const int64_t all = kPaired ? 2 * (int64_t)p.N : p.N;
-    sca.init(p.a_scales, 0, m0, p.M, p.M, p.K);
-    scb0.init(p.b_scales, 0, n0, p.N, all, p.K);
-    scb1.init(p.b_scales, kPaired ? p.N : 0, kPaired ? n0 : n0 + HRB, p.N, all, p.K);
+    scales.init(of_a ? p.a_scales : p.b_scales, kPaired && wave == 3 ? p.N : 0,
+                of_a ? m0 + 64 * wave : kPaired || wave == 2 ? n0 : n0 + HRB, of_a ? p.M : p.N,
+                of_a ? p.M : all, p.K, wave * 512, true);
   }
 
   f32x4 acc[2][FA][FB];
@@ -462,7 +464,7 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
 #pragma unroll
       for (int j = 0; j < FB; ++j) acc[h][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  constexpr int kCopies = HA::kPer + 2 * HB::kPer;
+  constexpr int kCopies = HA::kPer + 2 * HB::kPer + (MX ? 1 : 0);  // a stage's, per wave
   auto copy = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
@@ -470,9 +472,7 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     const lds_bytes sc = buf == 0 ? at.c0 : buf == 1 ? at.c1 : buf == 2 ? at.c2 : at.c3;
     const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
     if constexpr (MX) {
-      if (wave == 0) sca.template copy<HRA>(ss, s, lane);
-      if (wave == 1) scb0.template copy<HRB>(ss + 8 * HRA, s, lane);
-      if (wave == 2) scb1.template copy<HRB>(ss + 8 * (HRA + HRB), s, lane);
+      scales.copy(ss, s, lane);
     }
     a.copy(sa, s, wave, la);
     b0.copy(sb, s, wave, lb);
@@ -682,21 +682,20 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     b1.init(p.b, n0 + HR, p.N, p.ldb, kb, kb);
   const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
 
-  HalfScales scales[4];  // A's halves, then B's; wave i copies the i-th
+  WaveScales scales;  // two waves a half: A's, then B's
   if constexpr (MX) {
+    const int half = wave >> 1, part = (wave & 1) * 64;
+    const bool of_a = half < AH;
     const int64_t all = kPaired ? 2 * (int64_t)p.N : p.N;
-    scales[0].init(p.a_scales, 0, m0, p.M, p.M, p.K);
-    if constexpr (AH == 2) scales[1].init(p.a_scales, 0, m0 + HR, p.M, p.M, p.K);
-    scales[AH].init(p.b_scales, 0, n0, p.N, all, p.K);
-    scales[AH + 1].init(p.b_scales, kPaired ? p.N : 0, kPaired ? n0 : n0 + HR, p.N, all, p.K);
+    scales.init(of_a ? p.a_scales : p.b_scales, kPaired && half == AH + 1 ? p.N : 0,
+                (of_a ? m0 + half * HR : kPaired || half == AH ? n0 : n0 + HR) + part,
+                of_a ? p.M : p.N, of_a ? p.M : all, p.K, wave * 512, half < AH + 2);
   }
   auto copy_scales = [&](lds_bytes ss, int stage) {
-    if constexpr (MX) {
-#pragma unroll
-      for (int i = 0; i < AH + 2; ++i)
-        if (wave == i) scales[i].template copy<HR>(ss + i * (8 * HR), stage, lane);
-    }
+    if constexpr (MX) scales.copy(ss, stage, lane);
   };
+  // every wave's copy of scales in flight beside the half tiles' (AH = 1: two waves have none)
+  constexpr int kOne = MX && AH == 2 ? 1 : 0;
 
   f32x4 acc[AH][2][FA][FB];
 #pragma unroll
@@ -716,7 +715,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   a0.copy(sa1, 1, wave, la);
   b0.copy(sb1, 1, wave, lb);
   b1.copy(sc1, 1, wave, lb);
-  wait_vm<(AH == 2 ? 4 : 3) * kCopies>();
+  wait_vm<(AH == 2 ? 4 : 3) * kCopies + kOne>();
   wait_lgkm0();
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
@@ -766,7 +765,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     if constexpr (AH == 2) {
       __builtin_amdgcn_sched_barrier(0);  // the reads first: copies wait for their queue
       a1.copy(buf ? sx0 : sx1, s + 1, wave, la);
-      wait_vm<4 * kCopies>();
+      wait_vm<4 * kCopies + kOne>();
       FFN_MEM_DONE
       FFN_MMA(0, sm)
       FFN_MMA_DONE
@@ -776,7 +775,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
       a0.copy(a_now, s + 2, wave, la);
       b0.copy(b0_now, s + 2, wave, lb);
       b1.copy(b1_now, s + 2, wave, lb);
-      wait_vm<4 * kCopies>();
+      wait_vm<4 * kCopies + kOne>();
       FFN_MEM_DONE
       FFN_MMA(1, sm1)
       FFN_MMA_DONE
@@ -786,7 +785,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
       a0.copy(two == 0 ? sa0 : two == 1 ? sa1 : sx0, s + 2, wave, la);
       b0.copy(two == 0 ? sb0 : two == 1 ? sb1 : sx1, s + 2, wave, lb);
       b1.copy(two == 0 ? sc0 : two == 1 ? sc1 : sx2, s + 2, wave, lb);
-      wait_vm<3 * kCopies>();
+      wait_vm<3 * kCopies + kOne>();
       FFN_MEM_DONE
       FFN_MMA(0, sm)
       FFN_MMA_DONE
