@@ -414,6 +414,10 @@ struct Ring {
 // Tile of 128 x (2 x 64): four waves (2 x 2) of 64 rows x (2 x 32) columns, for
 // launches that leave CUs idle: a ring of four stages, copied three ahead,
 // and one barrier a stage. The stages from `first`, at most `share` of them.
+// Bound by latency: 0.62 us a stage of bf16 (0.70 row contiguous, 0.85 MXFP4)
+// where its 32 MFMAs a wave are 0.21, and 4 to 4.5 us for the first copies and
+// the way out. 333 x 1360 x 1000 in 4 shares 10.8 us and 3.8 us for the sums (12
+// tiles of 256 x 256, 16 stages each: 30 us by the estimate).
 template <Kind KA, Kind KB, bool MX, Epilogue EPI>
 __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int64_t id, int first,
                                           int share) {
@@ -552,7 +556,8 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
 }
 
 // The backward pass's last three products in one launch: the tiles of each,
-// share by share, follow those of the one before.
+// share by share, follow those of the one before. 201 tokens at 1000/680, 232
+// work-groups: 11.8 us and 4 us for the sums (three launches and a join 31 us).
 struct Gradients {
   Product product[3];  // dx (NN), dw13, dw2 (TN); aux: the shares' sums, if any
   int first[3];        // their first work-groups
@@ -576,7 +581,8 @@ __global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
 #undef FFN_RING
 
 // Adds the shares of K in their order and finishes: one lane (u of the product's)
-// four columns of a row; eight lanes a block where h is quantised.
+// four columns of a row; eight lanes a block where h is quantised. Bound by its
+// launch and one trip to memory: 3 to 4 us for 333 x 1360 in 4 shares (9 MB).
 template <Epilogue EPI>
 __device__ __forceinline__ void join_quad(const Product& p, const float* __restrict__ sums,
                                           int shares, int64_t u) {
@@ -634,6 +640,18 @@ __global__ __launch_bounds__(256) void gradients_join_kernel(const Gradients g, 
 // A part's LDS reads complete before its barrier, so the place is free for the
 // copies of the next phase; a copy is waited for before a barrier that every
 // wave passes ahead of its reads. Copies have 1.25 (AH = 1: 2) stages to arrive.
+//
+// Bound by the matrix units at the clock that their power leaves (about 1.84
+// GHz): 4096 x 4096 x 7168 in 160 us, 1.5 PFLOP/s, MFMAs in three cycles of
+// four; MXFP4 60 us, 4.0 PFLOP/s, its scaled MFMAs 20 to 22 cycles instead of
+// 16. Without copies it would take 0.79 of that, without LDS reads 0.95. Tried
+// without gain: four phases of 16 MFMAs (8% slower), the barrier ahead of a
+// part's last MFMAs (8% slower), wave priorities, copies among the MFMAs (8%
+// slower), fetching ahead into L2 (5% slower), 32 x 32 MFMAs (in registers 1.49
+// against 2.03 PFLOP/s), and 256 x 224 tiles where they divide a product into
+// whole rounds (the same: CUs without a tile leave the others their power).
+// 128 x 256 (AH = 1) takes 0.88 us a stage where 256 x 256 takes 1.42, for sizes
+// whose rounds it fills better.
 template <int AH, Kind KA, Kind KB, bool MX, Epilogue EPI>
 __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
