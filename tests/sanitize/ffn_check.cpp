@@ -53,11 +53,12 @@ void outputs(ffn::Epilogue e, const ffn::Product& p) {
 }
 void cut(const ffn::Cut& c, bool pair, int64_t M, int64_t N, int64_t K, bool mx) {
   const int64_t stages = (K + (mx ? 255 : 63)) / (mx ? 256 : 64);
-  const int64_t rows = c.tile == 2 ? 256 : 128, cols = (c.tile == 0 ? 128 : 256) / (pair ? 2 : 1);
-  expect(c.tile >= 0 && c.tile <= 2, "tile");
+  const int64_t tile_rows[] = {128, 128, 256, 64}, tile_cols[] = {128, 256, 256, 64};
+  expect(c.tile >= 0 && c.tile <= 3, "tile");
+  const int64_t rows = tile_rows[c.tile], cols = tile_cols[c.tile] / (pair ? 2 : 1);
   expect(c.groups == ((M + rows - 1) / rows) * ((N + cols - 1) / cols), "work-groups");
-  expect(c.shares >= 1 && (c.tile == 0 || c.shares == 1), "shares");
-  if (c.tile == 0) {
+  expect(c.shares >= 1 && (c.tile == 0 || c.tile == 3 || c.shares == 1), "shares");
+  if (c.tile == 0 || c.tile == 3) {
     expect((int64_t)c.share * c.shares >= stages, "the shares cover K");
     expect(c.shares == 1 || (int64_t)c.share * (c.shares - 1) < stages, "no empty share");
   }

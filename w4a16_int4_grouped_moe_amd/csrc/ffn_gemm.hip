@@ -43,7 +43,9 @@ __device__ __forceinline__ s16x4 read_transposed(lds_bytes p) {
 // Where RC chunk c of k-row k of a half tile of HR rows lies: slot c ^ spread(k).
 template <int HR>
 __device__ __forceinline__ int spread(int k) {
-  return HR == 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+  return HR == 128 ? (k & 3) | ((k >> 1) & 4)
+         : HR == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2)
+                    : (k >> 3) & 1;
 }
 
 // What a lane copies of a half tile (HR rows x one stage, 1 KB a copy, NW
@@ -51,12 +53,12 @@ __device__ __forceinline__ int spread(int k) {
 template <Kind KIND, int HR, int NW>
 struct Lane {
   static constexpr int kPer = HR * kRow / 1024 / NW;  // copies per wave
-  static_assert(kPer >= 2 && kPer % 2 == 0, "copies come in pairs of row groups");
+  static_assert(kPer == 1 || kPer % 2 == 0, "a wave's copies start at an even row group, or one each");
   uint32_t off[kPer];
   int piece;  // KC: byte of this lane's piece in even copies (odd ones: ^ 64)
 
   __device__ __forceinline__ void init(int64_t ld, int wave, int lane) {
-    piece = ((lane & 7) ^ (lane >> 4)) * 16;
+    piece = (((lane & 7) ^ (lane >> 4)) * 16) ^ (kPer == 1 ? (wave & 1) * 64 : 0);
     constexpr int lanes = HR / 8;  // RC: lanes per k-row
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -112,9 +114,9 @@ struct Half {
                                                  in ? at.off[j] + (uint32_t)k0 : kOut, 0, 0, 0);
       }
     } else {
-      // the end of the stage's last k-row; past K (by three stages at most) below 0. Without a
+      // the end of the stage's last k-row; past K (by seven stages at most) below 0. Without a
       // branch, behind which the compiler would no longer know how many copies are in flight.
-      const int left = end - stage * 64;
+      const int left = (int)((uint32_t)end - 64u * (uint32_t)stage);
       const int bytes = ((left < 64 ? left : 64) - 1) * span + records;
       const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(base + stage * pitch), 0, bytes < 0 ? 0 : bytes, kBufferFlags);
@@ -125,6 +127,16 @@ struct Half {
     }
   }
 };
+
+// f(0), ..., f(N - 1), each a constant
+template <typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each(f, std::make_integer_sequence<int, N>{});
+}
 
 // A wave's fragments of a half tile: F sub-tiles of 16 rows from `first`, for
 // the stage's two MFMA steps. Lane (r = lane % 16, q = lane / 16) holds piece
@@ -178,7 +190,7 @@ template <bool MX, int FA, int FB, int... X>
 __device__ __forceinline__ void mma(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB],
                                     const u32x4 (&m)[2][FA], uint32_t sn, u32x2 sm,
                                     std::integer_sequence<int, X...>) {
-  static_assert(FA == 4 && FB == 2, "scale words");
+  static_assert(FA <= 4 && FB <= 2, "scale words");
   if constexpr (MX) {
     (mma_mx<FA, FB, X>(acc, n, m, sn, sm), ...);
   } else {
@@ -197,8 +209,9 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[FA][FB], const u32x4 (&n)[2][FB
 }
 #endif
 
-// The MXFP4 scales that a wave copies, 8 bytes a row and stage: 64 rows of a
+// The MXFP4 scales that a wave copies, 8 bytes a row and stage: ROWS rows of a
 // tile (or none), so that every wave has one such copy a stage in flight.
+template <int ROWS>
 struct WaveScales {
   const uint8_t* base;
   int64_t pitch;  // bytes of a stage
@@ -210,9 +223,9 @@ struct WaveScales {
     pitch = 8 * scale_rows(all);
     last = (int)scale_stages(K) - 1;
     const int64_t left = rows - row0;
-    records = left <= 0 ? 0 : (int32_t)((left < 64 ? scale_rows(left) : 64) * 8);
+    records = left <= 0 ? 0 : (int32_t)((left < ROWS ? scale_rows(left) : ROWS) * 8);
     base = scales + (left > 0 ? first + row0 : 0) * 8;
-    lanes = any ? 32 : 0;
+    lanes = any ? ROWS / 2 : 0;
     at = at_;
   }
   __device__ __forceinline__ void copy(lds_bytes slot, int stage, int lane) const {
@@ -233,8 +246,13 @@ __device__ __forceinline__ void read_scales(lds_bytes slot, int first, int lane,
   const lds_bytes at = slot + (first + (lane & 15)) * 8;
 #pragma unroll
   for (int i = 0; i < F; i += 2) {
-    const u32x2 a = *(lds_u32x2)(at + i * 16 * 8), b = *(lds_u32x2)(at + (i + 1) * 16 * 8);
+    const u32x2 a = *(lds_u32x2)(at + i * 16 * 8);
     const uint32_t lo = __builtin_amdgcn_perm(a[1], a[0], pick);
+    if constexpr (F == 1) {
+      word[0] = lo;
+      return;
+    }
+    const u32x2 b = *(lds_u32x2)(at + (i + 1) * 16 * 8);
     const uint32_t hi = __builtin_amdgcn_perm(b[1], b[0], pick);
     word[i / 2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
   }
@@ -330,20 +348,20 @@ __device__ __forceinline__ void emit_mx(const Product& p, int64_t m, int64_t n, 
 
 // A tile leaves through LDS as fp32 rows, so that memory sees whole rows: the
 // waves write their accumulators (16-byte piece c of row r at c ^ (r % 16)),
-// then each takes 16 KB of whole rows, a lane four columns of one (paired: of
-// its gate and its up columns). COLS: columns of a row in LDS; m0: the row of
-// the tile's matrix at `lds`.
-template <Epilogue EPI, int COLS>
+// then each takes ROWS whole rows, a lane four columns of one (paired: of its
+// gate and its up columns). COLS: columns of a row in LDS; m0: the row of the
+// tile's matrix at `lds`.
+template <Epilogue EPI, int ROWS, int COLS>
 __device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int64_t m0,
                                            int64_t n0, int lane) {
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
   constexpr int kLanes = COLS / (kPaired ? 8 : 4);  // a row's lanes
-  constexpr int kRowsAtOnce = 64 / kLanes, kRows = 16384 / (4 * COLS);
-  constexpr int kBatch = kPaired ? 4 : 8;
+  constexpr int kRowsAtOnce = 64 / kLanes, kTurns = ROWS / kRowsAtOnce;
+  constexpr int kMost = kPaired ? 4 : 8, kBatch = kTurns < kMost ? kTurns : kMost;
   const int c = lane % kLanes;
   const int64_t n = n0 + 4 * c;
 #pragma unroll
-  for (int t = 0; t < kRows / kRowsAtOnce; t += kBatch) {
+  for (int t = 0; t < kTurns; t += kBatch) {
     f32x4 v[kBatch], up[kBatch], g[kBatch];
     if constexpr (EPI == kSwigluGrad) {  // a batch's pre-activations on their way together
 #pragma unroll
@@ -391,37 +409,42 @@ __device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
   return TileId{g * 8 + (t - g * group) % h, (t - g * group) / h};
 }
 
-// The 128 x 128 tile's ring of four stages: an object a stage and operand, so
-// that the compiler sees which copies a read has to wait for.
+// A small tile's ring of stages (four of 128 x 128, eight of 64 x 64): an object
+// a stage and half, so that the compiler sees which copies a read has to wait
+// for. `a` also holds the tile on its way out.
+template <int D>
 struct Ring {
-  lds_bytes a0, a1, a2, a3, b0, b1, b2, b3, c0, c1, c2, c3, s0, s1, s2, s3;
+  lds_bytes a[D], b[D], c[D], s[D];
 };
-#define FFN_RING(ring, scales)                                                        \
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[128 * kRow], sa1[128 * kRow]; \
-  __shared__ __attribute__((aligned(1024))) uint8_t sa2[128 * kRow], sa3[128 * kRow]; \
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[64 * kRow], sb1[64 * kRow];   \
-  __shared__ __attribute__((aligned(1024))) uint8_t sb2[64 * kRow], sb3[64 * kRow];   \
-  __shared__ __attribute__((aligned(1024))) uint8_t sc0[64 * kRow], sc1[64 * kRow];   \
-  __shared__ __attribute__((aligned(1024))) uint8_t sc2[64 * kRow], sc3[64 * kRow];   \
-  __shared__ __attribute__((aligned(16))) uint8_t ss0[scales], ss1[scales];           \
-  __shared__ __attribute__((aligned(16))) uint8_t ss2[scales], ss3[scales];           \
-  const Ring ring = {(lds_bytes)sa0, (lds_bytes)sa1, (lds_bytes)sa2, (lds_bytes)sa3,  \
-                     (lds_bytes)sb0, (lds_bytes)sb1, (lds_bytes)sb2, (lds_bytes)sb3,  \
-                     (lds_bytes)sc0, (lds_bytes)sc1, (lds_bytes)sc2, (lds_bytes)sc3,  \
-                     (lds_bytes)ss0, (lds_bytes)ss1, (lds_bytes)ss2, (lds_bytes)ss3};
+#define FFN_STAGE(i, tile, scales)                                            \
+  __shared__ __attribute__((aligned(1024))) uint8_t sa##i[(tile) * kRow];     \
+  __shared__ __attribute__((aligned(1024))) uint8_t sb##i[(tile) / 2 * kRow]; \
+  __shared__ __attribute__((aligned(1024))) uint8_t sc##i[(tile) / 2 * kRow]; \
+  __shared__ __attribute__((aligned(16))) uint8_t ss##i[scales];              \
+  ring.a[i] = (lds_bytes)sa##i, ring.b[i] = (lds_bytes)sb##i;                 \
+  ring.c[i] = (lds_bytes)sc##i, ring.s[i] = (lds_bytes)ss##i;
+#define FFN_STAGES4(tile, scales) \
+  FFN_STAGE(0, tile, scales)      \
+  FFN_STAGE(1, tile, scales) FFN_STAGE(2, tile, scales) FFN_STAGE(3, tile, scales)
+#define FFN_STAGES8(tile, scales) \
+  FFN_STAGES4(tile, scales)       \
+  FFN_STAGE(4, tile, scales)      \
+  FFN_STAGE(5, tile, scales) FFN_STAGE(6, tile, scales) FFN_STAGE(7, tile, scales)
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// Tile of 128 x (2 x 64): four waves (2 x 2) of 64 rows x (2 x 32) columns, for
-// launches that leave CUs idle: a ring of four stages, copied three ahead,
-// and one barrier a stage. The stages from `first`, at most `share` of them.
-// Bound by latency: 0.62 us a stage of bf16 (0.70 row contiguous, 0.85 MXFP4)
-// where its 32 MFMAs a wave are 0.21, and 4 to 4.5 us for the first copies and
-// the way out. 333 x 1360 x 1000 in 4 shares 10.8 us and 3.8 us for the sums (12
-// tiles of 256 x 256, 16 stages each: 30 us by the estimate).
-template <Kind KA, Kind KB, bool MX, Epilogue EPI>
-__device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int64_t id, int first,
-                                          int share) {
-  constexpr int NW = 4, HRA = 128, HRB = 64, FA = 4, FB = 2;
+// Tile of TS x (2 x TS / 2), TS = 128 or 64: four waves (2 x 2) of TS / 2 rows x (2
+// x TS / 4) columns, for launches that leave CUs idle: a ring of D stages, copied
+// D - 1 ahead, and one barrier a stage. The stages from `first`, at most `share`
+// of them. Bound by latency: a stage waits for its copy, so that 64 x 64 with
+// seven under way takes 0.32 us a stage (0.36 row contiguous, 0.40 MXFP4) where
+// 128 x 128 with three takes 0.62 (0.70, 0.85) for four times the work, its 32
+// MFMAs a wave being 0.21; 4 to 4.5 us besides, for the first copies and the way
+// out. The block on 333 tokens at 1000/680: 17.7 us with 64 x 64 tiles, 26.9 with
+// 128 x 128 in shares of K.
+template <int TS, Kind KA, Kind KB, bool MX, Epilogue EPI>
+__device__ __forceinline__ void tile_body(const Product& p, const Ring<512 / TS>& at, int64_t id,
+                                          int first, int share) {
+  constexpr int NW = 4, D = 512 / TS, HRA = TS, HRB = TS / 2, FA = TS / 32, FB = TS / 64;
   constexpr bool kPaired = EPI == kSwiglu || EPI == kSwigluMx || EPI == kPartialPaired;
   constexpr int kCols = kPaired ? HRB : 2 * HRB;  // output columns
   typedef Half<KA, HRA, NW> HA;
@@ -451,13 +474,13 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
     b1.init((const uint8_t*)p.b + p.N * p.ldb, n0, p.N, p.ldb, kb, kb < eb ? kb : eb);
   else
     b1.init(p.b, n0 + HRB, p.N, p.ldb, kb, kb < eb ? kb : eb);
-  WaveScales scales;  // waves 0 and 1: A's rows; 2 and 3: the halves of B's
+  WaveScales<HRB> scales;  // waves 0 and 1: A's rows; 2 and 3: the halves of B's
   if constexpr (MX) {
     const bool of_a = wave < 2;
     const int64_t all = kPaired ? 2 * (int64_t)p.N : p.N;
     scales.init(of_a ? p.a_scales : p.b_scales, kPaired && wave == 3 ? p.N : 0,
-                of_a ? m0 + 64 * wave : kPaired || wave == 2 ? n0 : n0 + HRB, of_a ? p.M : p.N,
-                of_a ? p.M : all, p.K, wave * 512, true);
+                of_a ? m0 + HRB * wave : kPaired || wave == 2 ? n0 : n0 + HRB, of_a ? p.M : p.N,
+                of_a ? p.M : all, p.K, wave * (8 * HRB), true);
   }
 
   f32x4 acc[2][FA][FB];
@@ -471,87 +494,79 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring& at, int6
   constexpr int kCopies = HA::kPer + 2 * HB::kPer + (MX ? 1 : 0);  // a stage's, per wave
   auto copy = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
-    const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
-    const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
-    const lds_bytes sc = buf == 0 ? at.c0 : buf == 1 ? at.c1 : buf == 2 ? at.c2 : at.c3;
-    const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
-    if constexpr (MX) {
-      scales.copy(ss, s, lane);
-    }
-    a.copy(sa, s, wave, la);
-    b0.copy(sb, s, wave, lb);
-    b1.copy(sc, s, wave, lb);
+    if constexpr (MX) scales.copy(at.s[buf], s, lane);
+    a.copy(at.a[buf], s, wave, la);
+    b0.copy(at.b[buf], s, wave, lb);
+    b1.copy(at.c[buf], s, wave, lb);
   };
   auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
-    const lds_bytes sa = buf == 0 ? at.a0 : buf == 1 ? at.a1 : buf == 2 ? at.a2 : at.a3;
-    const lds_bytes sb = buf == 0 ? at.b0 : buf == 1 ? at.b1 : buf == 2 ? at.b2 : at.b3;
-    const lds_bytes sc = buf == 0 ? at.c0 : buf == 1 ? at.c1 : buf == 2 ? at.c2 : at.c3;
-    const lds_bytes ss = buf == 0 ? at.s0 : buf == 1 ? at.s1 : buf == 2 ? at.s2 : at.s3;
-    wait_vm<2 * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
+    wait_vm<(D - 2) * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    copy(s + 3, std::integral_constant<int, (buf + 3) % 4>{});
+    copy(s + D - 1, std::integral_constant<int, (buf + D - 1) % D>{});
     __builtin_amdgcn_sched_barrier(0);
     Frags<KA, HRA, FA> fa;
     Frags<KB, HRB, FB> fb0, fb1;
-    fa.read(sa, wm * 64, lane);
-    fb0.read(sb, wn * 32, lane);
-    fb1.read(sc, wn * 32, lane);
+    fa.read(at.a[buf], wm * (16 * FA), lane);
+    fb0.read(at.b[buf], wn * (16 * FB), lane);
+    fb1.read(at.c[buf], wn * (16 * FB), lane);
     u32x2 sm = {};
     uint32_t sn0 = 0, sn1 = 0;
     if constexpr (MX) {
-      uint32_t w[2];
-      read_scales<FA>(ss, wm * 64, lane, w);
+      uint32_t w[2] = {};
+      read_scales<FA>(at.s[buf], wm * (16 * FA), lane, w);
       sm = u32x2{w[0], w[1]};
-      read_scales<FB>(ss, HRA + wn * 32, lane, &sn0);
-      read_scales<FB>(ss, HRA + HRB + wn * 32, lane, &sn1);
+      read_scales<FB>(at.s[buf], HRA + wn * (16 * FB), lane, &sn0);
+      read_scales<FB>(at.s[buf], HRA + HRB + wn * (16 * FB), lane, &sn1);
     }
     mma<MX>(acc[0], fb0.v, fa.v, sn0, sm, std::make_integer_sequence<int, 2 * FA * FB>{});
     mma<MX>(acc[1], fb1.v, fa.v, sn1, sm, std::make_integer_sequence<int, 2 * FA * FB>{});
     __builtin_amdgcn_sched_barrier(0);
   };
-  copy(first, std::integral_constant<int, 0>{});
-  copy(first + 1, std::integral_constant<int, 1>{});
-  copy(first + 2, std::integral_constant<int, 2>{});
+  each<D - 1>([&](auto i) { copy(first + decltype(i)::value, i); });
   int s = 0;
-  for (; s + 3 < count; s += 4) {
-    step(first + s, std::integral_constant<int, 0>{});
-    step(first + s + 1, std::integral_constant<int, 1>{});
-    step(first + s + 2, std::integral_constant<int, 2>{});
-    step(first + s + 3, std::integral_constant<int, 3>{});
-  }
-  if (s < count) step(first + s, std::integral_constant<int, 0>{});
-  if (s + 1 < count) step(first + s + 1, std::integral_constant<int, 1>{});
-  if (s + 2 < count) step(first + s + 2, std::integral_constant<int, 2>{});
+  for (; s + D <= count; s += D)
+    each<D>([&](auto i) { step(first + s + decltype(i)::value, i); });
+  each<D - 1>([&](auto i) {
+    if (s + decltype(i)::value < count) step(first + s + decltype(i)::value, i);
+  });
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
   __builtin_amdgcn_s_barrier();
   const int r = lane & 15, q = lane >> 4;
 #pragma unroll
-  for (int i = 0; i < FA; ++i) {  // 32 rows of 128 columns an object
-    const lds_bytes row = (i < 2 ? (wm ? at.a2 : at.a0) : (wm ? at.a3 : at.a1)) + ((i & 1) * 16 + r) * 512;
+  for (int i = 0; i < FA; ++i) {  // a quarter of the rows an object
+    constexpr int kPer = FA / 2;
+    const lds_bytes row = (wm ? at.a[2 + i / kPer] : at.a[i / kPer]) + ((i % kPer) * 16 + r) * (4 * TS);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int j = 0; j < FB; ++j)
-        *(lds_f32x4)(row + (((h * 16 + wn * 8 + j * 4 + q) ^ r) * 16)) = acc[h][i][j];
+        *(lds_f32x4)(row + (((h * (HRB / 4) + wn * (4 * FB) + j * 4 + q) ^ r) * 16)) = acc[h][i][j];
   }
   wait_lgkm0();
   __builtin_amdgcn_s_barrier();
-  store_rows<EPI, 128>(p, wave < 2 ? (wave == 0 ? at.a0 : at.a1) : (wave == 2 ? at.a2 : at.a3),
-                       m0 + wave * 32, n0, lane);
+  store_rows<EPI, TS / 4, TS>(
+      p, wave < 2 ? (wave == 0 ? at.a[0] : at.a[1]) : (wave == 2 ? at.a[2] : at.a[3]),
+      m0 + wave * (TS / 4), n0, lane);
 }
 #endif
 
-template <Kind KA, Kind KB, bool MX, Epilogue EPI>
+template <int TS, Kind KA, Kind KB, bool MX, Epilogue EPI>
 __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
 #if defined(__HIP_DEVICE_COMPILE__)
   if constexpr (EPI == kPartial || EPI == kPartialPaired)  // blockIdx.y: the share
     p.out = (float*)p.out + ((int64_t)blockIdx.y * (p.m_end - p.m_first) - p.m_first) * p.N *
                                 (EPI == kPartialPaired ? 2 : 1);
-  FFN_RING(ring, MX ? 256 * 8 : 16)
-  tile_body<KA, KB, MX, EPI>(p, ring, blockIdx.x, blockIdx.y * share, share);
+  Ring<512 / TS> ring;
+  if constexpr (TS == 128) {
+    FFN_STAGES4(128, MX ? 16 * 128 : 16)
+    tile_body<TS, KA, KB, MX, EPI>(p, ring, blockIdx.x, blockIdx.y * share, share);
+  } else {
+    FFN_STAGES8(64, MX ? 16 * 64 : 16)
+    tile_body<TS, KA, KB, MX, EPI>(p, ring, blockIdx.x, blockIdx.y * share, share);
+  }
 #endif
 }
 
@@ -565,7 +580,8 @@ struct Gradients {
 };
 __global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  FFN_RING(ring, 16)
+  Ring<4> ring;
+  FFN_STAGES4(128, 16)
   const int group = blockIdx.x;
   const int i = uniform(group < g.first[1] ? 0 : group < g.first[2] ? 1 : 2);
   const int id = uniform((group - g.first[i]) % g.tiles[i]);
@@ -573,12 +589,14 @@ __global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
   Product p = g.product[i];
   if (p.aux) p.aux = (float*)p.aux + share * p.M * p.N;
   if (i == 0)
-    tile_body<KC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+    tile_body<128, KC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
   else
-    tile_body<RC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+    tile_body<128, RC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
 #endif
 }
-#undef FFN_RING
+#undef FFN_STAGE
+#undef FFN_STAGES4
+#undef FFN_STAGES8
 
 // Adds the shares of K in their order and finishes: one lane (u of the product's)
 // four columns of a row; eight lanes a block where h is quantised. Bound by its
@@ -701,7 +719,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     b1.init(p.b, n0 + HR, p.N, p.ldb, kb, kb);
   const int stages = (int)((p.K + (MX ? 255 : 63)) / (MX ? 256 : 64));
 
-  WaveScales scales;  // two waves a half: A's, then B's
+  WaveScales<64> scales;  // two waves a half: A's, then B's
   if constexpr (MX) {
     const int half = wave >> 1, part = (wave & 1) * 64;
     const bool of_a = half < AH;
@@ -854,7 +872,7 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
     }
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
-    store_rows<EPI, 256>(p, mine, m0 + h * HR + wave * 16, n0, lane);
+    store_rows<EPI, 16, 256>(p, mine, m0 + h * HR + wave * 16, n0, lane);
     wait_lgkm0();
   }
 #endif
@@ -868,25 +886,35 @@ hipError_t join(const Product& p, const void* sums, int shares, hipStream_t stre
   return hipGetLastError();
 }
 
+template <int TS, Layout L, bool MX, Epilogue EPI>
+hipError_t launch_small(const Product& p, const Cut& c, dim3 grid, void* split,
+                        hipStream_t stream) {
+  constexpr Kind KA = L == kTN ? RC : KC, KB = L == kNT ? KC : RC;
+  constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
+  if (c.shares == 1) {
+    hipLaunchKernelGGL((tile_kernel<TS, KA, KB, MX, EPI>), grid, dim3(256), 0, stream, p, c.share);
+    return hipGetLastError();
+  }
+  Product part = p;
+  part.out = split;
+  hipLaunchKernelGGL((tile_kernel<TS, KA, KB, MX, paired ? kPartialPaired : kPartial>), grid,
+                     dim3(256), 0, stream, part, c.share);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : join<EPI>(p, split, c.shares, stream);
+}
+
 template <Layout L, bool MX, Epilogue EPI>
 hipError_t launch_cut(const Product& p, const Cut& c, void* split, hipStream_t stream) {
   constexpr Kind KA = L == kTN ? RC : KC, KB = L == kNT ? KC : RC;
-  constexpr bool paired = EPI == kSwiglu || EPI == kSwigluMx;
   if (c.groups > 0x7fffff) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)c.groups, c.shares);
   if (c.tile == 2) {
     hipLaunchKernelGGL((big_tile_kernel<2, KA, KB, MX, EPI>), grid, dim3(512), 0, stream, p);
   } else if (c.tile == 1) {
     hipLaunchKernelGGL((big_tile_kernel<1, KA, KB, MX, EPI>), grid, dim3(512), 0, stream, p);
-  } else if (c.shares == 1) {
-    hipLaunchKernelGGL((tile_kernel<KA, KB, MX, EPI>), grid, dim3(256), 0, stream, p, c.share);
   } else {
-    Product part = p;
-    part.out = split;
-    hipLaunchKernelGGL((tile_kernel<KA, KB, MX, paired ? kPartialPaired : kPartial>), grid,
-                       dim3(256), 0, stream, part, c.share);
-    const hipError_t e = hipGetLastError();
-    return e != hipSuccess ? e : join<EPI>(p, split, c.shares, stream);
+    return c.tile == 0 ? launch_small<128, L, MX, EPI>(p, c, grid, split, stream)
+                       : launch_small<64, L, MX, EPI>(p, c, grid, split, stream);
   }
   return hipGetLastError();
 }

@@ -59,8 +59,8 @@ hipError_t launch_product_mx(Epilogue epilogue, const Product& p, void* split,
                              hipStream_t stream);
 
 // How a tiled product is cut (ffn_plan.cpp): the tile (0: 128 x 128, 1: 128 x
-// 256, 2: 256 x 256; half the columns where gate and up pair), its work-groups,
-// and for tile 0 the shares of K, `share` stages each.
+// 256, 2: 256 x 256, 3: 64 x 64; half the columns where gate and up pair), its
+// work-groups, and for tiles 0 and 3 the shares of K, `share` stages each.
 struct Cut {
   int tile = 0, shares = 1, share = 1;
   int64_t groups = 0;

@@ -15,11 +15,11 @@ constexpr int kMxLds = 64 * 1024;  // an A quantised in LDS, codes and scales
 // widths 256 to 7168 (bf16 with K contiguous operands; with a row contiguous
 // one; MXFP4).
 struct Rate {
-  double stage[3], fixed[3];
+  double stage[4], fixed[4];
 };
-constexpr Rate kRates[3] = {{{0.62, 0.88, 1.42}, {4.5, 4.5, 7.0}},
-                            {{0.70, 0.85, 1.42}, {4.0, 5.0, 7.0}},
-                            {{0.85, 1.20, 1.80}, {4.5, 4.5, 8.0}}};
+constexpr Rate kRates[3] = {{{0.62, 0.88, 1.42, 0.32}, {4.5, 4.5, 7.0, 4.5}},
+                            {{0.70, 0.85, 1.42, 0.36}, {4.0, 5.0, 7.0, 4.5}},
+                            {{0.85, 1.20, 1.80, 0.40}, {4.5, 4.5, 8.0, 4.5}}};
 // The cheapest cut. Shares of K cost a launch and the sums' way to memory and
 // back (about 4 TB/s); of equals the larger tile.
 Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx) {
@@ -35,21 +35,22 @@ Cut cut_of(Epilogue epi, int64_t M, int64_t N, int64_t K, Layout layout, bool mx
   };
   // a tile's pre-activations on their way, which the join of shares reads at full rate
   const double grad = epi == kSwigluGrad ? 4.0 : 0.0;
-  const int64_t n[3] = {tiles(128, 128), tiles(128, 256), tiles(256, 256)};
+  const int64_t n[4] = {tiles(128, 128), tiles(128, 256), tiles(256, 256), tiles(64, 64)};
   Cut best{2, 1, (int)stages, n[2]};
   double least = time(2, n[2], stages) + grad;
   if (time(1, n[1], stages) + grad < least) {
     least = time(1, n[1], stages) + grad;
     best = Cut{1, 1, (int)stages, n[1]};
   }
-  for (int shares = 1; shares <= 32 && n[0] * shares <= 1024; ++shares) {
-    const int64_t share = (stages + shares - 1) / shares;
-    if (shares > 1 && (2 * shares > stages || share * (shares - 1) >= stages)) continue;
-    const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
-    const double t =
-        time(0, n[0] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : grad);
-    if (t < least) least = t, best = Cut{0, shares, (int)share, n[0]};
-  }
+  for (int tile : {0, 3})
+    for (int shares = 1; shares <= 32 && n[tile] * shares <= 1024; ++shares) {
+      const int64_t share = (stages + shares - 1) / shares;
+      if (shares > 1 && (2 * shares > stages || share * (shares - 1) >= stages)) continue;
+      const double sums = 4.0 * M * N * (paired ? 2 : 1) * shares;
+      const double t =
+          time(tile, n[tile] * shares, share) + (shares > 1 ? 3.0 + 2 * sums / 4e6 : grad);
+      if (t < least) least = t, best = Cut{tile, shares, (int)share, n[tile]};
+    }
   best.time = least;
   return best;
 }
