@@ -112,6 +112,31 @@ def test_backward(T, H, I):
         assert intact()
 
 
+# between them every tile of every product, with shares of its sums and without
+CUTS = [(66, 72, 72), (66, 232, 712), (2740, 72, 328), (4146, 232, 72), (66, 2120, 1224),
+        (3370, 4808, 72), (4146, 72, 936), (99, 3656, 1224), (2740, 72, 712), (4146, 1640, 168),
+        (151, 6312, 552), (2228, 3656, 72), (2740, 328, 1640)]
+
+
+@pytest.mark.parametrize("T,H,I", CUTS)
+def test_every_cut(T, H, I):
+    x, w13, w2, d = inputs(T, H, I, seed=16)
+    ref_gu, gu_tol, y, y_tol = reference_forward(x, w13, w2)
+    out, out_ok = guarded((T, H), torch.bfloat16)
+    gu, gu_ok = guarded((T, 2 * I), torch.float32)
+    ws, ws_ok = guarded((moe.ffn_workspace_size(T, H, I, moe.MOE_FFN_FORWARD),), torch.uint8)
+    close(moe.ffn_forward(x, w13, w2, out=out, gate_up=gu, workspace=ws), y, y_tol)
+    assert ((gu.double() - ref_gu).abs() <= gu_tol).all()
+    assert out_ok() and gu_ok() and ws_ok()
+    ws, ws_ok = guarded((moe.ffn_workspace_size(T, H, I, moe.MOE_FFN_BACKWARD),), torch.uint8)
+    outs = [guarded(s, torch.bfloat16) for s in ((T, H), (2 * I, H), (H, I))]
+    got = moe.ffn_backward(d, x, gu, w13, w2, *(o for o, _ in outs), workspace=ws)
+    for value, (ref, tol), (_, ok) in zip(got, reference_backward(d, x, gu, w13, w2), outs):
+        close(value, ref, tol)
+        assert ok()
+    assert ws_ok()
+
+
 @pytest.mark.parametrize("T,H,I", [(20, 696, 256), (201, 1000, 680), (1500, 1024, 256),
                                    (4000, 200, 64), (1000, 1000, 680), (300, 4096, 512)])
 def test_backward_products_in_one_launch(T, H, I):

@@ -105,7 +105,8 @@ def test_every_code_and_scale_reads_back():
 
 
 PRODUCTS = [(1, 8, 32), (1, 4096, 7168), (2, 264, 992), (7, 72, 256), (16, 512, 1024), (33, 136, 64),
-            (64, 128, 2048), (128, 128, 256), (129, 1000, 480), (300, 264, 7168), (777, 72, 992), (17, 1000, 992), (48, 264, 704), (64, 4096, 1024)]
+            (64, 128, 2048), (128, 128, 256), (129, 1000, 480), (300, 264, 7168), (777, 72, 992), (17, 1000, 992), (48, 264, 704), (64, 4096, 1024),
+            (151, 6304, 64), (791, 4800, 64), (2228, 3648, 64)]
 
 
 def product_close(got, a, b, n, rounded):
@@ -167,7 +168,8 @@ def test_scales_of_all_sizes(M):
 
 
 FFN = [(1, 32, 32), (1, 7168, 256), (3, 96, 64), (8, 512, 256), (40, 992, 160), (130, 256, 736), (257, 64, 96),
-       (20, 704, 256), (57, 1024, 2048), (64, 512, 160), (16, 7168, 2048)]
+       (20, 704, 256), (57, 1024, 2048), (64, 512, 160), (16, 7168, 2048), (66, 64, 64), (151, 6304, 64), (523, 64, 928), (1197, 64, 1632),
+       (4146, 64, 928), (2228, 3648, 64), (523, 4800, 928)]
 
 
 @pytest.mark.parametrize("T,H,I", FFN)
