@@ -578,10 +578,9 @@ struct Gradients {
   int first[3];        // their first work-groups
   int tiles[3], share[3];
 };
-__global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
+template <int TS>
+__device__ __forceinline__ void gradients_body(const Gradients& g, const Ring<512 / TS>& ring) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  Ring<4> ring;
-  FFN_STAGES4(128, 16)
   const int group = blockIdx.x;
   const int i = uniform(group < g.first[1] ? 0 : group < g.first[2] ? 1 : 2);
   const int id = uniform((group - g.first[i]) % g.tiles[i]);
@@ -589,9 +588,22 @@ __global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
   Product p = g.product[i];
   if (p.aux) p.aux = (float*)p.aux + share * p.M * p.N;
   if (i == 0)
-    tile_body<128, KC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+    tile_body<TS, KC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
   else
-    tile_body<128, RC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+    tile_body<TS, RC, RC, false, kStoreOrSums>(p, ring, id, share * g.share[i], g.share[i]);
+#endif
+}
+template <int TS>
+__global__ __launch_bounds__(256, 1) void gradients_kernel(const Gradients g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  Ring<512 / TS> ring;
+  if constexpr (TS == 128) {
+    FFN_STAGES4(128, 16)
+    gradients_body<TS>(g, ring);
+  } else {
+    FFN_STAGES8(64, 16)
+    gradients_body<TS>(g, ring);
+  }
 #endif
 }
 #undef FFN_STAGE
@@ -961,7 +973,10 @@ hipError_t launch_gradients(const GradientsPlan& plan, const Product (&products)
     g.share[i] = c.share;
     groups += (int)c.groups * c.shares;
   }
-  hipLaunchKernelGGL(gradients_kernel, dim3(groups), dim3(256), 0, stream, g);
+  if (plan.cut[0].tile == 0)
+    hipLaunchKernelGGL(gradients_kernel<128>, dim3(groups), dim3(256), 0, stream, g);
+  else
+    hipLaunchKernelGGL(gradients_kernel<64>, dim3(groups), dim3(256), 0, stream, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !plan.bytes) return e;
   groups = 0;

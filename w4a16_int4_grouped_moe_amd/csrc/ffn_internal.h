@@ -78,8 +78,8 @@ size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N,
 double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K, bool mx);
 
 // The backward pass's last three products (dx: NN; dw13, dw2: TN; bf16 results)
-// in one launch of 128 x 128 tiles, each with its own shares of K, and one that
-// adds the sums: `together` where that is the faster way. sums: where in
+// in one launch of 128 x 128 or 64 x 64 tiles, each with its own shares of K, and
+// one that adds the sums: `together` where that is the faster way. sums: where in
 // `split` (`bytes` in all) the sums of a product with shares lie.
 struct GradientsPlan {
   bool together = false;

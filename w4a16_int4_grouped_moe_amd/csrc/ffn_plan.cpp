@@ -97,9 +97,11 @@ double product_time(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int6
 // All three shares of K are cut to about one length. In one launch no product
 // waits for another: a round is as long as the longest share, more rounds are
 // the CUs' parts of all the work and about half a share with some CUs idle.
-// Whole backward pass, three launches -> one (microseconds): 201 tokens at
-// 1000/680 42 -> 29, 1000 at 1000/680 64 -> 38, 2000 at 512/128 46 -> 28, 700 at
-// 2048/768 62 -> 42, 8192 at 512/512 82 -> 71, 4096 at 2048/256 77 either way.
+// Whole backward pass, three launches -> one of 128 x 128 tiles (microseconds):
+// 201 tokens at 1000/680 42 -> 29, 1000 at 1000/680 64 -> 38, 2000 at 512/128 46 ->
+// 28, 700 at 2048/768 62 -> 42, 8192 at 512/512 82 -> 71, 4096 at 2048/256 77 either
+// way. 64 x 64 against 128 x 128 tiles, replayed from a graph: 20 tokens at 696/256
+// 13.4 and 16.9, 300 at 296/200 14.3 and 17.1.
 GradientsPlan gradients_plan(int64_t tokens, int64_t hidden, int64_t inter) {
   const int64_t sizes[3][3] = {{tokens, hidden, 2 * inter},
                                {2 * inter, hidden, tokens},
@@ -107,38 +109,44 @@ GradientsPlan gradients_plan(int64_t tokens, int64_t hidden, int64_t inter) {
   GradientsPlan best;
   if (tokens == 0) return best;
   const Rate& rate = kRates[1];
-  int64_t tiles[3], stages[3], all = 0, longest = 0;
+  int64_t stages[3], longest = 0;
   double least = 0;  // of the products by themselves
   for (int i = 0; i < 3; ++i) {
     const int64_t M = sizes[i][0], N = sizes[i][1], K = sizes[i][2];
-    tiles[i] = ((M + 127) / 128) * ((N + 127) / 128);
     stages[i] = (K + 63) / 64;
-    all += tiles[i];
     longest = std::max(longest, stages[i]);
     least += product_time(i ? kTN : kNN, kStoreBf16, M, (int32_t)N, K, false);
   }
-  if (all > 1024) return best;
-  for (int64_t length = longest; length >= 2; length -= (length + 3) / 4) {
-    GradientsPlan plan;
-    plan.together = true;
-    int64_t groups = 0;
-    double work = 0, most = 0;
+  for (int tile : {0, 3}) {
+    const int64_t size = tile ? 64 : 128;
+    int64_t tiles[3], all = 0;
     for (int i = 0; i < 3; ++i) {
-      Cut& c = plan.cut[i];
-      const int64_t shares = (stages[i] + length - 1) / length;
-      const int64_t share = (stages[i] + shares - 1) / shares;
-      c = Cut{0, (int)((stages[i] + share - 1) / share), (int)share, tiles[i]};
-      c.time = share * rate.stage[0] + rate.fixed[0];
-      groups += c.groups * c.shares;
-      work += c.time * c.groups * c.shares / 256;
-      most = std::max(most, c.time);
-      plan.sums[i] = plan.bytes;
-      if (c.shares > 1) plan.bytes += 4 * sizes[i][0] * sizes[i][1] * c.shares;
+      tiles[i] = ((sizes[i][0] + size - 1) / size) * ((sizes[i][1] + size - 1) / size);
+      all += tiles[i];
     }
-    if (groups > 1024) break;
-    const double time = (groups <= 256 ? most : work + most / 2) +
-                        (plan.bytes ? 6.0 + 2 * plan.bytes / 4e6 : 0.0);
-    if (time < least) least = time, best = plan;
+    if (all > 1024) continue;
+    for (int64_t length = longest; length >= 2; length -= (length + 3) / 4) {
+      GradientsPlan plan;
+      plan.together = true;
+      int64_t groups = 0;
+      double work = 0, most = 0;
+      for (int i = 0; i < 3; ++i) {
+        Cut& c = plan.cut[i];
+        const int64_t shares = (stages[i] + length - 1) / length;
+        const int64_t share = (stages[i] + shares - 1) / shares;
+        c = Cut{tile, (int)((stages[i] + share - 1) / share), (int)share, tiles[i]};
+        c.time = share * rate.stage[tile] + rate.fixed[tile];
+        groups += c.groups * c.shares;
+        work += c.time * c.groups * c.shares / 256;
+        most = std::max(most, c.time);
+        plan.sums[i] = plan.bytes;
+        if (c.shares > 1) plan.bytes += 4 * sizes[i][0] * sizes[i][1] * c.shares;
+      }
+      if (groups > 1024) break;
+      const double time = (groups <= 256 ? most : work + most / 2) +
+                          (plan.bytes ? 6.0 + 2 * plan.bytes / 4e6 : 0.0);
+      if (time < least) least = time, best = plan;
+    }
   }
   return best;
 }
