@@ -60,7 +60,11 @@ struct MxRegion {
 
 // How a forward pass runs its products: tiled, or as the few-row kernels take
 // them; in MXFP4 these quantise A themselves, or find x quantised by a launch
-// ahead (more than 16 rows).
+// ahead (more than 16 rows). The tiled estimate is that of its products; with it
+// go what the launches' order costs and, in MXFP4, the launch that brings scales
+// into the order of the stages (kAhead*, measured at 20 to 64 rows; the few-row
+// kernels of codes have no launch ahead at all).
+constexpr double kAheadBf16 = 2.0, kAheadMx = 4.5, kAheadCodes = 6.0;
 enum Path { kTiled, kFew, kFewPrepared };
 
 Path path_of(const moe_ffn_problem* p, bool mx) {
@@ -81,7 +85,7 @@ Path path_of(const moe_ffn_problem* p, bool mx) {
       ffn::product_time(ffn::kNT, ffn::kStoreBf16, down.M, down.N, down.K, mx);
   const double rows = ffn::rows_time(up, mx, ffn::kAAsIs, true) +
                       ffn::rows_time(down, mx, mx ? ffn::kAF32 : ffn::kAAsIs, false);
-  return rows < tiled ? few : kTiled;
+  return rows < tiled + (mx ? kAheadMx : kAheadBf16) ? few : kTiled;
 }
 
 Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize) {
@@ -91,8 +95,7 @@ Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize) {
     return kFew;
   if (!ffn::rows_fit(d, true, ffn::kAAsIs, false)) return kTiled;
   const double tiled = ffn::product_time(ffn::kNT, ffn::kStoreF32, rows, cols, width, true);
-  // the given scales of a tiled product go through a launch too
-  return ffn::rows_time(d, true, ffn::kAAsIs, false) < tiled + (quantize ? 0.0 : 3.0)
+  return ffn::rows_time(d, true, ffn::kAAsIs, false) < tiled + (quantize ? kAheadMx : kAheadCodes)
              ? quantize ? kFewPrepared : kFew
              : kTiled;
 }

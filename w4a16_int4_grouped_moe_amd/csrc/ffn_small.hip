@@ -16,10 +16,10 @@
 //
 // Bound by memory and, below 100 MB, by how long a launch takes to fill and
 // drain it: one token at 7168/2048 reads 59 MB in 12.0 us (4.9 TB/s) and 29 MB
-// in 8.4 us (3.5 TB/s); MXFP4, 8 tokens, 16 MB in 11.0 us and 8 MB in 7.0 us. The
-// 128 x 128 tiles take 100 us for the token. Past 16 rows it is bound by the
-// loads' address path (64 cycles for 16 rows x 64 bytes) and wins up to 64 rows
-// where weights are narrow: 20 -> 13.5 us for 32 tokens at 696/256.
+// in 8.4 us (3.5 TB/s); MXFP4, 8 tokens, 16 MB in 11.0 us and 8 MB in 7.0 us.
+// Past 16 rows it is bound by the loads' address path (64 cycles for 16 rows x 64
+// bytes): 20 tokens at 1000/2000 13.3 us and 19.6 with tiles, at 7168/2048 33.4
+// and 27.7; 64 tokens at 1000/2000 18.9 and 19.8.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
