@@ -5,8 +5,6 @@ from __future__ import annotations
 import ctypes
 import functools
 
-import torch
-
 from . import _binding
 from ._binding import _check, _need
 
@@ -19,6 +17,8 @@ MOE_FFN_FORWARD_MXFP4 = 2
 
 MX_BLOCK = 32
 MAX_INT32 = 0x7fffffff
+
+torch = None  # loaded by an entry point's first check: sizes, constants and the build need none
 
 
 class FfnProblem(ctypes.Structure):
@@ -65,7 +65,14 @@ def _launch(device, fn, *args):
             _check(fn(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
+def _load_torch():
+    global torch
+    torch = _binding._torch()
+
+
 def _gpu(t, name):
+    if torch is None:
+        _load_torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -185,17 +192,19 @@ class Mxfp4:
     device = property(lambda self: self._codes.device)
 
 
-_TYPES = {torch.bfloat16: MOE_TYPE_BF16, torch.float16: MOE_TYPE_FP16,
-          torch.float32: MOE_TYPE_FP32}
-
-
 def _type_of(dtype):
-    if dtype not in _TYPES:
-        raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
-    return _TYPES[dtype]
+    if dtype is torch.bfloat16:
+        return MOE_TYPE_BF16
+    if dtype is torch.float16:
+        return MOE_TYPE_FP16
+    if dtype is torch.float32:
+        return MOE_TYPE_FP32
+    raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
 
 
 def _is_mx(q, name, device=None):
+    if torch is None:
+        _load_torch()
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4")
     if device is not None and q.device != device:
