@@ -33,7 +33,7 @@
  *
  * Limits: hidden, inter and width at most 2^20; hidden and inter multiples of
  * 8 (bf16) or 32 (MXFP4), cols a multiple of 8, width a multiple of 32;
- * num_tokens and rows at most 2^31 - 256.
+ * num_tokens, rows and cols at most 2^31 - 256.
  */
 #ifndef MOE_FFN_H
 #define MOE_FFN_H

@@ -256,7 +256,7 @@ int moe_mxfp4_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, i
   if (!bytes) return MOE_ERR_NULL;
   const int st = check_rows(rows, width);
   if (st != MOE_OK) return st;
-  if (cols <= 0 || cols % 8) return MOE_ERR_SHAPE;
+  if (cols <= 0 || cols > kMaxRows || cols % 8) return MOE_ERR_SHAPE;
   *bytes = 0;
   const Path path = rows == 0 ? kFew : path_of(rows, cols, width, quantize);
   if (path == kFewPrepared) *bytes = RowRegion(rows, width).bytes();
