@@ -918,7 +918,6 @@ hipError_t launch_small(const Product& p, const Cut& c, dim3 grid, void* split,
 template <Layout L, bool MX, Epilogue EPI>
 hipError_t launch_cut(const Product& p, const Cut& c, void* split, hipStream_t stream) {
   constexpr Kind KA = L == kTN ? RC : KC, KB = L == kNT ? KC : RC;
-  if (c.groups > 0x7fffff) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)c.groups, c.shares);
   if (c.tile == 2) {
     hipLaunchKernelGGL((big_tile_kernel<2, KA, KB, MX, EPI>), grid, dim3(512), 0, stream, p);
@@ -934,13 +933,12 @@ hipError_t launch_cut(const Product& p, const Cut& c, void* split, hipStream_t s
 template <Layout L, bool MX, Epilogue EPI>
 hipError_t launch(Product p, void* split, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  const Plan plan = plan_of(EPI, p.M, p.N, p.K, L, MX);
-  p.m_end = plan.first ? plan.first : p.M;
-  const hipError_t e = launch_cut<L, MX, EPI>(p, plan.whole, split, stream);
-  if (e != hipSuccess || !plan.first) return e;
-  p.m_first = plan.first;
-  p.m_end = p.M;
-  return launch_cut<L, MX, EPI>(p, plan.rest, split, stream);
+  return each_launch(plan_of(EPI, p.M, p.N, p.K, L, MX), p.M,
+                     [&](int64_t first, int64_t end, const Cut& cut) {
+                       p.m_first = first;
+                       p.m_end = end;
+                       return launch_cut<L, MX, EPI>(p, cut, split, stream);
+                     });
 }
 
 }  // namespace

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 namespace ffn {
 
 // What a product's epilogue does with its tile. "N" below is the product's
@@ -72,6 +74,29 @@ struct Plan {
   double time = 0;
 };
 Plan plan_of(Epilogue epilogue, int64_t M, int64_t N, int64_t K, Layout layout, bool mx);
+// f(first row, end of the rows, cut) for each launch of a plan's tiles. One holds
+// fewer than 2^32 lanes, 2^23 - 1 work-groups of 512: more tiles go row range by
+// row range. (A row of tiles fits: N is at most 2^31 - 256, and 2^20 where gate
+// and up pair. Cuts with shares of K have 1024 work-groups at most.)
+constexpr int64_t kMaxGroups = 0x7fffff;
+template <typename F>
+hipError_t each_launch(const Plan& plan, int64_t M, F&& f) {
+  constexpr int64_t tile_rows[] = {128, 128, 256, 64};
+  const int64_t split = plan.first ? plan.first : M;
+  for (int part = 0; part < (plan.first ? 2 : 1); ++part) {
+    Cut c = part ? plan.rest : plan.whole;
+    const int64_t end = part ? M : split, size = tile_rows[c.tile];
+    const int64_t across = c.groups / ((end - (part ? split : 0) + size - 1) / size);
+    const int64_t most = kMaxGroups / across * size;
+    for (int64_t m = part ? split : 0; m < end; m += most) {
+      const int64_t m_end = std::min(m + most, end);
+      c.groups = (m_end - m + size - 1) / size * across;
+      const hipError_t e = f(m, m_end, c);
+      if (e != hipSuccess) return e;
+    }
+  }
+  return hipSuccess;
+}
 // Bytes of the shares' sums (`split`), and the plan's time
 size_t product_workspace(Layout layout, Epilogue epilogue, int64_t M, int32_t N, int64_t K,
                          bool mx);
