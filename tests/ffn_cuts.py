@@ -40,6 +40,15 @@ MX_FFN = {
     (4101, 7168, 2048): {"up": "+3s", "down": "2"},
 }
 
+# the block on chosen values, each tile quantising h on its way out
+MX_VALUES = {
+    (150, 544, 64): {"up": "3"},
+    (150, 4128, 64): {"up": "3s"},
+    (20001, 544, 64): {"up": "0"},
+    (8319, 416, 224): {"up": "1"},
+    (40001, 544, 64): {"up": "2"},
+}
+
 # products with MXFP4 operands: rows, cols, width
 MX = {
     (65, 64, 32): "3",

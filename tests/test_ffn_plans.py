@@ -36,7 +36,8 @@ def plans(tmp_path_factory):
 
 
 def test_named_cuts(plans):
-    for kind, table in (("ffn", ffn_cuts.FFN), ("mxffn", ffn_cuts.MX_FFN)):
+    for kind, table in (("ffn", ffn_cuts.FFN), ("mxffn", ffn_cuts.MX_FFN),
+                        ("mxffn", ffn_cuts.MX_VALUES)):
         for sizes, cuts in plans(kind, list(table)).items():
             assert {n: cuts.get(n) for n in table[sizes]} == table[sizes], (kind, sizes, cuts)
     for sizes, cuts in plans("mx", list(ffn_cuts.MX)).items():
