@@ -202,6 +202,14 @@ def _type_of(dtype):
     raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
 
 
+def _dtype_of(out):
+    if out is None:
+        return torch.bfloat16
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    return out.dtype
+
+
 def _is_mx(q, name, device=None):
     if torch is None:
         _load_torch()
@@ -234,7 +242,7 @@ def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):
     """The values of q as dtype (default bfloat16; moe_mxfp4_dequantize)."""
     _is_mx(q, "q")
     if dtype is None:
-        dtype = torch.bfloat16 if out is None else out.dtype
+        dtype = _dtype_of(out)
     kind = _type_of(dtype)
     out = _result(out, "out", dtype, q.shape, q.device)
     _launch(q.device, _library().moe_mxfp4_dequantize, q.codes.data_ptr(), q.scales.data_ptr(),
@@ -268,7 +276,7 @@ def mxfp4_matmul(a, b: Mxfp4, out=None, dtype=None, workspace=None):
     if K != Kb:
         raise ValueError(f"a has width {K}, b {Kb}")
     if dtype is None:
-        dtype = torch.bfloat16 if out is None else out.dtype
+        dtype = _dtype_of(out)
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
     out = _result(out, "out", dtype, (M, N), dev)
