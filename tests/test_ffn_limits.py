@@ -36,3 +36,18 @@ def test_more_tiles_than_a_launch_holds(tmp_path):
     rc, out = run(exe)
     assert rc == 0, out[-4000:]
     assert "failed: 0" in out and "runtime error" not in out and "Sanitizer" not in out, out[-4000:]
+
+
+@pytest.mark.parametrize("wrap", [1 << 32, -(1 << 32), 1 << 64, -(1 << 64)])
+def test_sizes_that_c_would_wrap(lib, wrap):  # noqa: F811
+    """Python integers outside C's are refused, whatever they would be modulo 2^32 or 2^64."""
+    for i in range(4):
+        args = [4, 64, 32, moe.MOE_FFN_FORWARD]
+        args[i] += wrap if i else wrap << 32  # the first is an int64_t
+        with pytest.raises(ValueError):
+            moe.ffn_workspace_size(*args)
+    for i in range(3):
+        args = [4, 64, 32, True]
+        args[i] += wrap if i else wrap << 32  # the first is an int64_t
+        with pytest.raises(ValueError):
+            moe.mxfp4_matmul_workspace_size(*args)

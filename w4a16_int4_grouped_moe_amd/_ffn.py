@@ -17,6 +17,7 @@ MOE_FFN_FORWARD_MXFP4 = 2
 
 MX_BLOCK = 32
 MAX_INT32 = 0x7fffffff
+MAX_INT64 = 0x7fffffffffffffff
 
 torch = None  # loaded by an entry point's first check: sizes, constants and the build need none
 
@@ -101,12 +102,19 @@ def _scratch(workspace, need, device):
     return workspace
 
 
+def _in_range(**sizes):
+    """Sizes that a C int64_t (num_tokens, rows) or int holds: others would reach it wrapped."""
+    for name, n in sizes.items():
+        most = MAX_INT64 if name in ("num_tokens", "rows") else MAX_INT32
+        if not -most <= n <= most:
+            raise ValueError(f"{name} {n} is out of range")
+
+
 @functools.lru_cache(maxsize=4096)
 def _problem(num_tokens, hidden, inter, kind):
     """The sizes as the library takes them, and the workspace bytes (a pure
     function of the sizes)."""
-    if max(hidden, inter) > MAX_INT32:  # as a C int they would be others
-        raise ValueError(f"hidden {hidden} or inter {inter} is out of range")
+    _in_range(num_tokens=num_tokens, hidden=hidden, inter=inter, kind=kind)
     p = FfnProblem(num_tokens, hidden, inter)
     n = ctypes.c_size_t(0)
     _check(_library().moe_ffn_workspace_size(ctypes.byref(p), kind, ctypes.byref(n)))
@@ -253,8 +261,7 @@ def mxfp4_dequantize(q: Mxfp4, dtype=None, out=None):
 @functools.lru_cache(maxsize=4096)
 def mxfp4_matmul_workspace_size(rows: int, cols: int, width: int, quantize: bool) -> int:
     """Bytes of workspace of mxfp4_matmul (quantize: a is a bf16 tensor)."""
-    if max(cols, width) > MAX_INT32:
-        raise ValueError(f"cols {cols} or width {width} is out of range")
+    _in_range(rows=rows, cols=cols, width=width)
     n = ctypes.c_size_t(0)
     _check(_library().moe_mxfp4_matmul_workspace_size(rows, cols, width, int(quantize),
                                                       ctypes.byref(n)))
