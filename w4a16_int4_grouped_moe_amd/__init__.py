@@ -20,6 +20,9 @@ The shared expert's feed-forward block on its own, with gradients, and MXFP4
     w = mxfp4_dequantize(q)
     out = mxfp4_matmul(a, q)                         # a: Mxfp4 or bf16
     out = mxfp4_ffn_forward(x, w13_q, w2_q)
+
+No call records an autograd graph, also for tensors that require grad:
+ffn_backward is how the block's gradients are had.
 """
 from ._binding import (  # noqa: F401
     MOE_ERR_ALIGNMENT,

@@ -144,7 +144,8 @@ def ffn_forward(x, w13, w2, out=None, gate_up=None, workspace=None):
     """The gated feed-forward block (moe_ffn_forward): x bf16 [T, H], w13 bf16
     [2I, H] (gate rows, then up rows), w2 bf16 [H, I] -> out bf16 [T, H].
     gate_up: optional fp32 [T, 2I], receives the pre-activations that
-    ffn_backward reads."""
+    ffn_backward reads. Like every call here it takes the tensors' values alone:
+    autograd records nothing, also for tensors that require grad."""
     dev, T, H, I = _block(x, w13, w2)
     out = _result(out, "out", torch.bfloat16, (T, H), dev)
     if gate_up is not None:

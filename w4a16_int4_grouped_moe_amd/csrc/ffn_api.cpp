@@ -11,7 +11,7 @@ namespace {
 using ffn::Product;
 
 constexpr int32_t kMaxWidth = 1 << 20;
-constexpr int64_t kMaxRows = 0x7fffff00;  // whole 256-row tiles of a launch's 2^32 lanes
+constexpr int64_t kMaxRows = 0x7fffff00;  // whole 256-row tiles below 2^31
 
 size_t region(int64_t bytes) { return ((size_t)bytes + 255) / 256 * 256; }
 

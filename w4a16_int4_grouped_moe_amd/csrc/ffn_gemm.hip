@@ -267,7 +267,9 @@ __device__ __forceinline__ void put_scale(const Product& p, int64_t m, int64_t n
     for (int i = at + 1; i < 8; ++i) dst[i] = 127;
 }
 
-// Four columns from n of row m: `v`, or a gate and an up group.
+// Four columns from n of row m: `v`, or a gate and an up group. h is rounded to
+// bf16 here, once: it is the next product's operand, which the matrix units take in
+// 16 bits.
 template <Epilogue EPI>
 __device__ __forceinline__ void emit(const Product& p, int64_t m, int64_t n, const f32x4& v,
                                      const f32x4& up) {
@@ -296,7 +298,8 @@ __device__ __forceinline__ void emit(const Product& p, int64_t m, int64_t n, con
   }
 }
 
-// Four columns of dh -> the gradients of g and u, and h.
+// Four columns of dh -> the gradients of g and u, and h: operands of the last
+// products, rounded to bf16 once for the matrix units.
 __device__ __forceinline__ void emit_grad(const Product& p, int64_t m, int64_t n, const f32x4& v,
                                           const f32x4& g, const f32x4& u) {
   const int64_t N = p.N;
@@ -435,12 +438,14 @@ struct Ring {
 // Tile of TS x (2 x TS / 2), TS = 128 or 64: four waves (2 x 2) of TS / 2 rows x (2
 // x TS / 4) columns, for launches that leave CUs idle: a ring of D stages, copied
 // D - 1 ahead, and one barrier a stage. The stages from `first`, at most `share`
-// of them. Bound by latency: a stage waits for its copy, so that 64 x 64 with
-// seven under way takes 0.32 us a stage (0.36 row contiguous, 0.40 MXFP4) where
-// 128 x 128 with three takes 0.62 (0.70, 0.85) for four times the work, its 32
-// MFMAs a wave being 0.21; 4 to 4.5 us besides, for the first copies and the way
-// out. The block on 333 tokens at 1000/680: 17.7 us with 64 x 64 tiles, 26.9 with
-// 128 x 128 in shares of K.
+// of them. 64 x 64 with seven copies under way takes 0.32 us a stage (0.36 row
+// contiguous, 0.40 MXFP4) where 128 x 128 with three takes 0.62 (0.70, 0.85) for
+// four times the work, its 32 MFMAs a wave being 0.21; 4 to 4.5 us besides, for the
+// first copies and the way out. Neither memory nor the matrix units bound it: 333
+// tokens' gate and up at 1000/680 (10.5 us) keep the matrix units busy in 10% of
+// the cycles; a wave issues in 34% of its cycles, waits for copies, LDS and the
+// barrier in 40%, for its turn to issue in 25%. The block on them: 17.0 us with 64
+// x 64 tiles, 26.9 with 128 x 128 in shares of K.
 template <int TS, Kind KA, Kind KB, bool MX, Epilogue EPI>
 __device__ __forceinline__ void tile_body(const Product& p, const Ring<512 / TS>& at, int64_t id,
                                           int first, int share) {
@@ -572,7 +577,8 @@ __global__ __launch_bounds__(256, 1) void tile_kernel(Product p, int share) {
 
 // The backward pass's last three products in one launch: the tiles of each,
 // share by share, follow those of the one before. 201 tokens at 1000/680, 232
-// work-groups: 11.8 us and 4 us for the sums (three launches and a join 31 us).
+// work-groups: 11.5 us and 3.9 us for the sums (three launches and a join 31 us);
+// the matrix units are busy in 10% of the cycles.
 struct Gradients {
   Product product[3];  // dx (NN), dw13, dw2 (TN); aux: the shares' sums, if any
   int first[3];        // their first work-groups
@@ -671,11 +677,13 @@ __global__ __launch_bounds__(256) void gradients_join_kernel(const Gradients g, 
 // copies of the next phase; a copy is waited for before a barrier that every
 // wave passes ahead of its reads. Copies have 1.25 (AH = 1: 2) stages to arrive.
 //
-// Bound by the matrix units at the clock that their power leaves (about 1.84
-// GHz): 4096 x 4096 x 7168 in 160 us, 1.5 PFLOP/s, MFMAs in 87% of the cycles,
-// no LDS bank conflicts; MXFP4 60 us, 4.0 PFLOP/s, its scaled MFMAs 20 to 22
-// cycles instead of 16. Without copies it took 0.79 of that (the power goes into
-// the clock), without LDS reads 0.95. Tried
+// Bound by the matrix units at the clock that their power leaves (1.78 to 1.88
+// GHz): 4096 x 4096 x 7168 in 160 us, 1.5 PFLOP/s, MFMAs in 85 to 87% of the cycles,
+// no LDS bank conflicts. MXFP4 60 us, 4.0 PFLOP/s, MFMAs in 51 to 55% of the cycles
+// (7.2 PFLOP/s in registers): a wave waits for copies, LDS or a barrier in 30% of
+// its cycles (bf16 21%), its first phase reading all the scales beside the larger
+// half of the fragments. Without copies the bf16 product took 0.79 of its time (the
+// power goes into the clock), without LDS reads 0.95. Tried
 // without gain: four phases of 16 MFMAs (8% slower), the barrier ahead of a
 // part's last MFMAs (8% slower), wave priorities, copies among the MFMAs (8%
 // slower), fetching ahead into L2 (5% slower), 32 x 32 MFMAs (in registers 1.49

@@ -10,16 +10,21 @@
 // waves' sums are added in LDS, in wave order.
 //
 // An A that is to be quantised (bf16, or the fp32 h of the block) is quantised
-// by the work-group into LDS: its loads go out first, then the ring's, so the
-// conversion runs under the first weights' latency. Every work-group repeats
-// it, which for a few rows costs less than a launch of its own.
+// by the work-group into LDS, four pieces a thread at a time; the ring's loads go
+// out ahead of the last four's conversion, so a longer A is waited for first (8
+// rows of 7168: three trips to memory before the first weights are asked for).
+// Every work-group repeats it.
 //
-// Bound by memory and, below 100 MB, by how long a launch takes to fill and
-// drain it: one token at 7168/2048 reads 59 MB in 12.0 us (4.9 TB/s) and 29 MB
-// in 8.4 us (3.5 TB/s); MXFP4, 8 tokens, 16 MB in 11.0 us and 8 MB in 7.0 us.
-// Past 16 rows it is bound by the loads' address path (64 cycles for 16 rows x 64
-// bytes): 20 tokens at 1000/2000 13.3 us and 19.6 with tiles, at 7168/2048 33.4
-// and 27.7; 64 tokens at 1000/2000 18.9 and 19.8.
+// bf16 is bound by memory and, below 100 MB, by how long a launch takes to fill
+// and drain it: one token at 7168/2048 reads 59 MB in 12.6 us (4.7 TB/s) and 29
+// MB in 8.8 us (3.3 TB/s). MXFP4 is bound by the way of A ahead of the weights: 8
+// tokens at 7168/2048 16 MB in 11.1 us and 8 MB in 7.1 us, a wave waiting in 55%
+// of its cycles. Past 16 rows it is bound by the loads' address path (64 cycles
+// for 16 rows x 64 bytes; 32 x 4096 x 7168 in MXFP4 13.8 us, a wave waiting for
+// its turn to issue in 62% of its cycles): 20 tokens at 1000/2000 13.3 us and 19.6
+// with tiles, at 7168/2048 33.4 and 27.7; 64 tokens at 1000/2000 18.9 and 19.8.
+// Its LDS conflicts (the sums' rows lie 64 bytes apart) are 200 to 450 cycles of a
+// work-group's 8000 to 35000.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(const P
       if constexpr (EPI == kSwigluF32) {
         ((float*)p.out)[at] = h;
       } else {
-        ((uint16_t*)p.out)[at] = (uint16_t)pack2(h, 0.f);
+        ((uint16_t*)p.out)[at] = (uint16_t)pack2(h, 0.f);  // as the matrix units take it
         if (p.aux) {
           float* gu = (float*)p.aux + (int64_t)m * 2 * N + n0 + j;
           gu[0] = g;

@@ -6,8 +6,8 @@
 // The largest magnitude is compared as bits (an unsigned maximum orders
 // magnitudes, infinities and NaN on top), so e is its exponent field less 2,
 // and v_cvt_scalef32_pk_fp4_f32 divides by 2^e, rounds to nearest even and
-// saturates. Bound by memory: 4096 x 7168 of fp32 (133 MB) 21.6 us each way, 6.1
-// TB/s; 8 x 7168 of bf16 2.3 us, a launch.
+// saturates. Bound by memory: 4096 x 7168 of fp32 (133 MB) 22.5 us to codes and
+// 22.9 us back, 5.9 and 5.8 TB/s; 8 x 7168 of bf16 2.4 us, a launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -82,7 +82,9 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const void* __restri
 // The first work-groups copy scales into the order by stage, one wave 64 rows
 // of four stages (the rows' bytes come in runs of 32 and leave 512 at a time);
 // they wait on memory, so they start ahead of those that quantise x. 4096 x 7168
-// of bf16 with a matrix's scales (77 MB) 15.6 us, 4.9 TB/s.
+// of bf16 with a matrix's scales (77 MB) 16.2 us, 4.8 TB/s. Rows of K/32 bytes
+// that start anywhere are gathered byte by byte: 55 KB (777 and 1000 rows of 992)
+// take 5.4 us, a wave waiting in 82% of its cycles.
 struct Prepare {
   const void* x;
   int64_t units, rows;
