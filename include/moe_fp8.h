@@ -1,0 +1,129 @@
+/*
+ * moe_fp8.h -- C ABI of the FP8 block operators beside the W4A16 MoE layer
+ * (MI355X, gfx950): quantisation, products with their gradients, and the routed
+ * experts on FP8 weights.
+ *
+ * A matrix [rows, width] in FP8 is codes (e4m3, one byte a value: sign, 4
+ * exponent bits of bias 7, 3 mantissa bits, largest 448, 0x7f and 0xff NaN)
+ * [rows, width] and one fp32 scale for each block of values, which multiplies
+ * them. Two kinds of blocks, `block`:
+ *
+ *   1     1 x 128, along a row (activations, gradients): scales
+ *         [ceil(width / 128), rows] -- all rows' scales of 128 columns together
+ *   128   128 x 128 (weights): scales [ceil(rows / 128), ceil(width / 128)]
+ *
+ * The last block of a row or column may be short. Quantisation gives scales
+ * that are powers of two; products take any.
+ *
+ *   scale = 2^e, e the least integer with max |v| <= 448 * 2^e, at least -126
+ *           (a block of zeros: 1)
+ *   code  = nearest e4m3 of v / scale, ties to the even code
+ *   a block that holds an infinity or a NaN: scale NaN, codes 0; its values
+ *   read back as NaN
+ *
+ * Conventions are moe_w4a16.h's: dense row-major device tensors, 16-byte
+ * aligned (scales: 4-byte aligned); the caller owns every buffer and the
+ * workspace; nothing is allocated or kept, the host never waits, launches go
+ * to `stream` on the current device and may be captured into a HIP graph;
+ * calls that share a workspace (two captured graphs, too) must not overlap;
+ * every argument error is found on the host before any launch and returned
+ * as one of moe_w4a16.h's status codes. Outputs must not overlap inputs.
+ * Results do not depend on anything but the inputs: no atomics, and the same
+ * call gives the same bits.
+ *
+ * Limits: width at most 2^20 and a multiple of 16; cols a multiple of 8; rows
+ * and cols at most 2^31 - 256. Types are moe_ffn.h's MOE_TYPE_*.
+ */
+#ifndef MOE_FP8_H
+#define MOE_FP8_H
+
+#include "moe_ffn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MOE_FP8_ROW_BLOCKS 1
+#define MOE_FP8_SQUARE_BLOCKS 128
+
+/* x [rows, width] of `type` -> codes, scales. rows == 0 is a no-op. */
+int moe_fp8_quantize(const void *x, int32_t type, int64_t rows, int32_t width, int32_t block,
+                     uint8_t *codes, float *scales, void *stream);
+
+/* The values of codes and scales, rounded once to `type`: out [rows, width]. */
+int moe_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t rows, int32_t width,
+                       int32_t block, int32_t type, void *out, void *stream);
+
+/* Bytes of workspace of moe_fp8_matmul; quantize: whether a is bf16. */
+int moe_fp8_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, int quantize,
+                                  size_t *bytes);
+
+/*
+ * out [rows, cols] = A B^T, rounded once to out_type (MOE_TYPE_BF16 or
+ * MOE_TYPE_FP32). The products of a block of 128 are summed in fp32, multiplied
+ * by the product of the two scales, and added to the others' in fp32. B: codes
+ * and scales of [cols, width], blocks as b_block says. A [rows, width]: codes
+ * and scales in 1 x 128 blocks, or bf16 with a_scales NULL, which is quantised
+ * as by moe_fp8_quantize. rows == 0 is a no-op.
+ */
+int moe_fp8_matmul(const void *a, const float *a_scales, const uint8_t *b, const float *b_scales,
+                   int32_t b_block, int64_t rows, int32_t cols, int32_t width, int32_t out_type,
+                   void *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace of moe_fp8_matmul_backward. */
+int moe_fp8_matmul_backward_workspace_size(int64_t rows, int32_t cols, int32_t width,
+                                           size_t *bytes);
+
+/*
+ * Gradients of sum(out * dout), out = A B^T, with respect to A and B, written
+ * (not added to), of out_type (MOE_TYPE_BF16 or MOE_TYPE_FP32):
+ *
+ *   da [rows, width] = Q(dout) B         Q: 1 x 128 blocks along the axis that is
+ *   db [cols, width] = Q(dout^T) Q(a^T)^T   summed over: cols for da, rows for db
+ *
+ * dout bf16 [rows, cols]; a bf16 [rows, width]; b codes and scales in 128 x 128
+ * blocks of [cols, width]. da or db may be NULL: it is then not computed, and
+ * what only it reads (da: b; db: a) may be NULL. rows == 0 clears db.
+ */
+int moe_fp8_matmul_backward(const void *dout, const void *a, const uint8_t *b,
+                            const float *b_scales, int64_t rows, int32_t cols, int32_t width,
+                            int32_t out_type, void *da, void *db, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Sizes of the FP8 experts (host struct, read during the call only). */
+typedef struct {
+  int64_t num_tokens;  /* T >= 0 */
+  int32_t hidden;      /* H, a multiple of 128 */
+  int32_t inter;       /* I, a multiple of 128 */
+  int32_t num_experts; /* E local experts, 1 .. MOE_MAX_EXPERTS */
+  int32_t expert_base; /* global id of local expert 0 */
+  int32_t top_k;       /* 1 .. MOE_MAX_TOP_K */
+} moe_fp8_experts_problem;
+
+/* Bytes of workspace of moe_fp8_experts_forward (host only). */
+int moe_fp8_experts_workspace_size(const moe_fp8_experts_problem *p, size_t *bytes);
+
+/*
+ * The routed experts on FP8 weights:
+ *
+ *   out[t] = bf16( sum_{j < k, id local} w_tj W2_e q(silu(W1_e q(x_t)) * (W3_e q(x_t))) )
+ *
+ * with e = topk_ids[t, j] - expert_base, q the quantisation in 1 x 128 blocks (h
+ * from its fp32 value), W1 = rows [0, I) and W3 = rows [I, 2I) of W13; ids
+ * outside [expert_base, expert_base + E), -1 included, contribute nothing,
+ * duplicates are summed, weights are applied as given, slots in their order. x
+ * bf16 [T, H]; topk_ids int32 [T, k]; topk_weights fp32 [T, k]; w13 codes
+ * [E, 2I, H] and scales [E, 2I/128, H/128]; w2 codes [E, H, I] and scales
+ * [E, H/128, I/128]; out bf16 [T, H]. T == 0 is a no-op.
+ *
+ * A shared expert is one more expert, with weight 1 in a slot of every token.
+ */
+int moe_fp8_experts_forward(const void *x, const int32_t *topk_ids, const float *topk_weights,
+                            const uint8_t *w13, const float *w13_scales, const uint8_t *w2,
+                            const float *w2_scales, void *out, const moe_fp8_experts_problem *p,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

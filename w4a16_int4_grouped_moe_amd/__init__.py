@@ -21,8 +21,19 @@ The shared expert's feed-forward block on its own, with gradients, and MXFP4
     out = mxfp4_matmul(a, q)                         # a: Mxfp4 or bf16
     out = mxfp4_ffn_forward(x, w13_q, w2_q)
 
+FP8 with a scale for each block of 128 (include/moe_fp8.h), and the router's
+balance loss (include/moe_balance.h):
+
+    q = fp8_quantize(w, block=128)                   # Fp8: codes, scales
+    w = fp8_dequantize(q)
+    out = fp8_matmul(a, q)                           # a: Fp8 or bf16
+    da, dw = fp8_matmul_backward(dout, a, q)
+    out = fp8_experts_forward(x, topk_ids, topk_weights, w13_q, w2_q)
+    loss, counts, tokens = balance_loss(scores, topk_ids, mask=None, seq_offsets=None)
+    dscores = balance_loss_backward(dloss, scores, counts, tokens, top_k)
+
 No call records an autograd graph, also for tensors that require grad:
-ffn_backward is how the block's gradients are had.
+the *_backward calls are how gradients are had.
 """
 from ._binding import (  # noqa: F401
     MOE_ERR_ALIGNMENT,
@@ -71,4 +82,25 @@ from ._ffn import (  # noqa: F401
     mxfp4_matmul,
     mxfp4_matmul_workspace_size,
     mxfp4_quantize,
+)
+from ._fp8 import (  # noqa: F401
+    MOE_FP8_ROW_BLOCKS,
+    MOE_FP8_SQUARE_BLOCKS,
+    Fp8,
+    Fp8ExpertsProblem,
+    fp8_dequantize,
+    fp8_experts_forward,
+    fp8_experts_workspace_size,
+    fp8_matmul,
+    fp8_matmul_backward,
+    fp8_matmul_backward_workspace_size,
+    fp8_matmul_workspace_size,
+    fp8_quantize,
+)
+from ._balance import (  # noqa: F401
+    MOE_MAX_SEQUENCES,
+    BalanceProblem,
+    balance_loss,
+    balance_loss_backward,
+    balance_workspace_size,
 )

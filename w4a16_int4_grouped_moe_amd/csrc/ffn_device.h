@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 // the host pass sees the kernels' stubs alone
 #if !defined(__HIP_DEVICE_COMPILE__)
 #pragma clang diagnostic ignored "-Wunused-function"
@@ -66,6 +68,32 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t exponent) {
 // and saturate; checked over all bytes, borders included.
 __device__ __forceinline__ float mx_unit(uint32_t scale) {
   return __builtin_bit_cast(float, scale << 23);
+}
+
+// f(0), ..., f(N - 1), each a constant
+template <typename F, int... I>
+__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each(f, std::make_integer_sequence<int, N>{});
+}
+
+// The tile of this work-group. Work-group i runs on XCD i % 8: each XCD takes
+// a run of consecutive tiles, and tiles run through groups of 8 row tiles, so
+// that the tiles an XCD holds at one time share rows of A and of B in its L2.
+struct TileId {
+  int64_t m, n;
+};
+__device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
+  const int64_t total = tm * tn;
+  const int64_t per = total / 8, rest = total % 8;
+  const int64_t x = id % 8, i = id / 8;
+  const int64_t t = x * per + (x < rest ? x : rest) + i;
+  const int64_t group = 8 * tn, g = t / group;
+  const int64_t h = tm - g * 8 < 8 ? tm - g * 8 : 8;
+  return TileId{g * 8 + (t - g * group) % h, (t - g * group) / h};
 }
 
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -22,8 +22,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <utility>
-
 #include "ffn_device.h"
 #include "ffn_internal.h"
 
@@ -127,16 +125,6 @@ struct Half {
     }
   }
 };
-
-// f(0), ..., f(N - 1), each a constant
-template <typename F, int... I>
-__device__ __forceinline__ void each(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
-  each(f, std::make_integer_sequence<int, N>{});
-}
 
 // A wave's fragments of a half tile: F sub-tiles of 16 rows from `first`, for
 // the stage's two MFMA steps. Lane (r = lane % 16, q = lane / 16) holds piece
@@ -394,22 +382,6 @@ __device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int6
       }
     }
   }
-}
-
-// The tile of this work-group. Work-group i runs on XCD i % 8: each XCD takes
-// a run of consecutive tiles, and tiles run through groups of 8 row tiles, so
-// that the tiles an XCD holds at one time share rows of A and of B in its L2.
-struct TileId {
-  int64_t m, n;
-};
-__device__ __forceinline__ TileId tile_of(int64_t id, int64_t tm, int64_t tn) {
-  const int64_t total = tm * tn;
-  const int64_t per = total / 8, rest = total % 8;
-  const int64_t x = id % 8, i = id / 8;
-  const int64_t t = x * per + (x < rest ? x : rest) + i;
-  const int64_t group = 8 * tn, g = t / group;
-  const int64_t h = tm - g * 8 < 8 ? tm - g * 8 : 8;
-  return TileId{g * 8 + (t - g * group) % h, (t - g * group) / h};
 }
 
 // A small tile's ring of stages (four of 128 x 128, eight of 64 x 64): an object

@@ -1,0 +1,405 @@
+// fp8.hip -- FP8 block quantisation, its inverse, and the transposes that the
+// gradients read (gfx950).
+//
+// One pass over memory each. The largest magnitude is compared as bits (an
+// unsigned maximum orders magnitudes, infinities and NaN on top); the scale is a
+// power of two, so that dividing by it is exact and v_cvt_pk_fp8_f32 rounds once.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "../../include/moe_fp8.h"
+#include "fp8_device.h"
+#include "fp8_internal.h"
+
+namespace fp8 {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Eight values of x from `unit` eights
+template <int TYPE>
+__device__ __forceinline__ void load8(const void* x, int64_t unit, float* v) {
+  if constexpr (TYPE == MOE_TYPE_FP32) {
+    const f32x4* p = (const f32x4*)x + 2 * unit;
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  } else {
+    const u32x4 w = ((const u32x4*)x)[unit];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (TYPE == MOE_TYPE_BF16) {
+        v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
+      } else {
+        const h16x2 h = __builtin_bit_cast(h16x2, (uint32_t)w[i]);
+        v[2 * i] = (float)h[0], v[2 * i + 1] = (float)h[1];
+      }
+    }
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ void store8(void* x, int64_t unit, const float* v) {
+  if constexpr (TYPE == MOE_TYPE_FP32) {
+    f32x4* o = (f32x4*)x + 2 * unit;
+    o[0] = f32x4{v[0], v[1], v[2], v[3]};
+    o[1] = f32x4{v[4], v[5], v[6], v[7]};
+  } else {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x2 p = {v[2 * i], v[2 * i + 1]};
+      if constexpr (TYPE == MOE_TYPE_BF16)
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, bf16x2));
+      else
+        w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p, h16x2));
+    }
+    ((u32x4*)x)[unit] = w;
+  }
+}
+
+__device__ __forceinline__ uint32_t top8(const float* v) {
+  uint32_t top = magnitude(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = larger(top, magnitude(v[i]));
+  return top;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t with_lane(uint32_t v) {
+  return larger(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+// The largest of 16 neighbouring lanes
+__device__ __forceinline__ uint32_t top_of_16(uint32_t v) {
+  v = with_lane<0xB1>(v);   // lane ^ 1
+  v = with_lane<0x4E>(v);   // lane ^ 2
+  v = with_lane<0x141>(v);  // mirrored in eights
+  return with_lane<0x140>(v);  // mirrored in sixteens
+}
+
+__device__ __forceinline__ u32x2 codes8(const float* v, uint32_t field) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float inverse = scale_inverse(field);
+  const u32x2 c = {pack4(v, inverse), pack4(v + 4, inverse)};
+  return field == 255 ? u32x2{0, 0} : c;
+#else
+  return u32x2{};
+#endif
+}
+
+// 1 x 128 blocks: 16 lanes a block, a work-group 16 rows of NB blocks, so that the
+// scales of a stage leave 16 at a time. out_units: eights of a row of codes, those past
+// the values zeros.
+template <int TYPE, int NB>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __restrict__ x,
+                                                                 int64_t rows, int32_t width,
+                                                                 int32_t out_units,
+                                                                 uint8_t* __restrict__ codes,
+                                                                 float* __restrict__ scales) {
+  const int32_t blocks = (width + kBlock - 1) / kBlock, units = width / 8;
+  const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 16 + (threadIdx.x >> 4);
+  const int b0 = blockIdx.x * NB, at = threadIdx.x & 15;
+  if (row >= rows) return;  // all 16 lanes of a row
+  float v[NB][8];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int u = (b0 + i) * 16 + at;
+    if (u < units) {
+      load8<TYPE>(x, row * units + u, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int u = (b0 + i) * 16 + at;
+    const uint32_t field = scale_field(top_of_16(top8(v[i])));
+    if (u < out_units) ((u32x2*)codes)[row * out_units + u] = codes8(v[i], field);
+    if (at == 0 && b0 + i < blocks) scales[(int64_t)(b0 + i) * rows + row] = scale_value(field);
+  }
+}
+
+// 128 x 128 blocks: a work-group a block, its values in registers
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void quantize_square_kernel(const void* __restrict__ x,
+                                                                   int64_t rows, int32_t width,
+                                                                   uint8_t* __restrict__ codes,
+                                                                   float* __restrict__ scales) {
+  __shared__ uint32_t tops[kThreads / 64];
+  const int32_t units = width / 8, u = blockIdx.x * 16 + (threadIdx.x & 15);
+  const int64_t block_row = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (block_row * kBlock >= rows) return;
+  const int64_t row0 = block_row * kBlock + (threadIdx.x >> 4);
+  float v[8][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (u < units && row0 + 16 * i < rows) {
+      load8<TYPE>(x, (row0 + 16 * i) * units + u, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = larger(top, top8(v[i]));
+  top = top_of_16(top);
+  top = larger(top, __shfl_xor(top, 16));
+  top = larger(top, __shfl_xor(top, 32));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = larger(larger(tops[0], tops[1]), larger(tops[2], tops[3]));
+  const uint32_t field = scale_field(top);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (u < units && row0 + 16 * i < rows)
+      ((u32x2*)codes)[(row0 + 16 * i) * units + u] = codes8(v[i], field);
+  if (threadIdx.x == 0) scales[block_row * gridDim.x + blockIdx.x] = scale_value(field);
+}
+
+// 16 rows of NB blocks a work-group, as the codes were made
+template <int TYPE, int NB, bool SQUARE>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                              const float* __restrict__ scales,
+                                                              int64_t rows, int32_t width,
+                                                              void* __restrict__ out) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int32_t blocks = (width + kBlock - 1) / kBlock, units = width / 8;
+  const int64_t row = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * 16 + (threadIdx.x >> 4);
+  const int b0 = blockIdx.x * NB, at = threadIdx.x & 15;
+  if (row >= rows) return;
+  u32x2 c[NB];
+  float s[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int u = (b0 + i) * 16 + at;
+    if (u >= units) continue;
+    c[i] = ((const u32x2*)codes)[row * units + u];
+    s[i] = scales[SQUARE ? row / kBlock * blocks + b0 + i : (int64_t)(b0 + i) * rows + row];
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const int u = (b0 + i) * 16 + at;
+    if (u >= units) continue;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][j], false);
+      const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[i][j], true);
+      v[4 * j] = lo[0] * s[i], v[4 * j + 1] = lo[1] * s[i];
+      v[4 * j + 2] = hi[0] * s[i], v[4 * j + 3] = hi[1] * s[i];
+    }
+    store8<TYPE>(out, row * units + u, v);
+  }
+#endif
+}
+
+// A tile of 128 rows on its way to being 128 bytes of a column: 32 words of four
+// rows, columns 33 words apart, so that 64 lanes that write or read one word each of
+// eight columns meet 64 banks.
+[[maybe_unused]] constexpr int kPitch = 33;
+
+// 128 rows x 64 columns a work-group: a thread four rows of eight columns
+__global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(
+    const void* __restrict__ x, int64_t rows, int32_t width, uint8_t* __restrict__ codes,
+    float* __restrict__ scales) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ uint32_t words[64 * kPitch];
+  __shared__ uint32_t tops[kThreads / 64][64];
+  const int32_t units = width / 8;
+  const int g = threadIdx.x >> 3, c8 = threadIdx.x & 7, u = blockIdx.x * 8 + c8;
+  const int64_t block = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (block * kBlock >= rows) return;
+  const int64_t row0 = block * kBlock + 4 * g;
+  float v[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (u < units && row0 + i < rows) {
+      load8<MOE_TYPE_BF16>(x, (row0 + i) * units + u, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+  uint32_t top[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    top[j] = larger(larger(magnitude(v[0][j]), magnitude(v[1][j])),
+                    larger(magnitude(v[2][j]), magnitude(v[3][j])));
+    top[j] = larger(top[j], __shfl_xor(top[j], 8));
+    top[j] = larger(top[j], __shfl_xor(top[j], 16));
+    top[j] = larger(top[j], __shfl_xor(top[j], 32));
+    if ((threadIdx.x & 63) < 8) tops[threadIdx.x >> 6][c8 * 8 + j] = top[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int c = c8 * 8 + j;
+    const uint32_t field =
+        scale_field(larger(larger(tops[0][c], tops[1][c]), larger(tops[2][c], tops[3][c])));
+    const float col[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
+    words[c * kPitch + g] = field == 255 ? 0 : pack4(col, scale_inverse(field));
+    if (g == 0 && u < units) scales[block * width + u * 8 + j] = scale_value(field);
+  }
+  __syncthreads();
+  const int64_t pitch = blocks_of(rows) * kBlock;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = i * 8 + (threadIdx.x >> 5), w = threadIdx.x & 31;
+    const int64_t col = (int64_t)blockIdx.x * 64 + c;
+    if (col < width)
+      *(uint32_t*)(codes + col * pitch + block * kBlock + 4 * w) = words[c * kPitch + w];
+  }
+#endif
+}
+
+// 128 rows x 128 columns of codes a work-group: a thread four rows of 16 columns
+__global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __restrict__ codes,
+                                                             int64_t rows, int32_t width,
+                                                             uint8_t* __restrict__ out) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ uint32_t words[128 * kPitch];
+  const int32_t units = width / 16;
+  const int g = threadIdx.x >> 3, c16 = threadIdx.x & 7, u = blockIdx.x * 8 + c16;
+  const int64_t block = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
+  if (block * kBlock >= rows) return;
+  const int64_t row0 = block * kBlock + 4 * g;
+  u32x4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = u < units && row0 + i < rows ? ((const u32x4*)codes)[(row0 + i) * units + u]
+                                        : u32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // bytes (row i, column 4 j + b) -> word of column 4 j + b
+    const uint32_t lo01 = __builtin_amdgcn_perm(v[1][j], v[0][j], 0x05010400u);
+    const uint32_t hi01 = __builtin_amdgcn_perm(v[1][j], v[0][j], 0x07030602u);
+    const uint32_t lo23 = __builtin_amdgcn_perm(v[3][j], v[2][j], 0x05010400u);
+    const uint32_t hi23 = __builtin_amdgcn_perm(v[3][j], v[2][j], 0x07030602u);
+    uint32_t* w = words + (c16 * 16 + 4 * j) * kPitch + g;
+    w[0] = __builtin_amdgcn_perm(lo23, lo01, 0x05040100u);
+    w[kPitch] = __builtin_amdgcn_perm(lo23, lo01, 0x07060302u);
+    w[2 * kPitch] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
+    w[3 * kPitch] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
+  }
+  __syncthreads();
+  const int64_t pitch = blocks_of(rows) * kBlock;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int c = i * 8 + (threadIdx.x >> 5), w = threadIdx.x & 31;
+    const int64_t col = (int64_t)blockIdx.x * 128 + c;
+    if (col < width)
+      *(uint32_t*)(out + col * pitch + block * kBlock + 4 * w) = words[c * kPitch + w];
+  }
+#endif
+}
+
+// `down` work-groups of rows over y and z (65535 a dimension at most); across fits x
+dim3 grid_of(int64_t across, int64_t down) {
+  const int64_t z = (down + 65534) / 65535;
+  return dim3((unsigned)across, (unsigned)((down + z - 1) / z), (unsigned)z);
+}
+
+template <typename F>
+hipError_t with_type(int32_t type, F&& f) {
+  if (type == MOE_TYPE_BF16)
+    f(std::integral_constant<int, MOE_TYPE_BF16>{});
+  else if (type == MOE_TYPE_FP16)
+    f(std::integral_constant<int, MOE_TYPE_FP16>{});
+  else
+    f(std::integral_constant<int, MOE_TYPE_FP32>{});
+  return hipGetLastError();
+}
+__global__ __launch_bounds__(kThreads) void clear_kernel(u32x4* __restrict__ out, int64_t units) {
+  const int64_t u = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x;
+  if (u < units) out[u] = u32x4{0, 0, 0, 0};
+}
+
+// Blocks of a row that a work-group takes: four, with their loads in flight together, once
+// that still leaves work-groups for every CU
+bool four_blocks(int64_t rows, int32_t width) {
+  return (rows + 15) / 16 * ((blocks_of(width) + 3) / 4) >= 512;
+}
+template <int TYPE>
+void quantize_rows(const void* x, int64_t rows, int32_t width, int32_t out_units, uint8_t* codes,
+                   float* scales, hipStream_t stream) {
+  const int64_t blocks = blocks_of(width), down = (rows + 15) / 16;
+  if (four_blocks(rows, width))
+    hipLaunchKernelGGL((quantize_rows_kernel<TYPE, 4>), grid_of((blocks + 3) / 4, down),
+                       dim3(kThreads), 0, stream, x, rows, width, out_units, codes, scales);
+  else
+    hipLaunchKernelGGL((quantize_rows_kernel<TYPE, 1>), grid_of(blocks, down), dim3(kThreads), 0,
+                       stream, x, rows, width, out_units, codes, scales);
+}
+
+}  // namespace
+
+hipError_t launch_quantize(const void* x, int32_t type, int64_t rows, int32_t width, int32_t block,
+                           uint8_t* codes, float* scales, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  return with_type(type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    if (block != 1)
+      hipLaunchKernelGGL((quantize_square_kernel<TYPE>), grid_of(blocks_of(width), blocks_of(rows)),
+                         dim3(kThreads), 0, stream, x, rows, width, codes, scales);
+    else
+      quantize_rows<TYPE>(x, rows, width, width / 8, codes, scales, stream);
+  });
+}
+
+hipError_t launch_quantize_padded(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                                  float* scales, hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  quantize_rows<MOE_TYPE_BF16>(x, rows, width, (int32_t)blocks_of(width) * (kBlock / 8), codes,
+                               scales, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_clear(void* out, int64_t bytes, hipStream_t stream) {
+  const int64_t units = bytes / 16, groups = (units + kThreads - 1) / kThreads;
+  if (groups == 0) return hipSuccess;
+  hipLaunchKernelGGL(clear_kernel, grid_of((groups + 65534) / 65535, groups < 65535 ? groups : 65535),
+                     dim3(kThreads), 0, stream, (u32x4*)out, units);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize(const uint8_t* codes, const float* scales, int64_t rows,
+                             int32_t width, int32_t block, int32_t type, void* out,
+                             hipStream_t stream) {
+  if (rows == 0) return hipSuccess;
+  const bool four = four_blocks(rows, width);
+  const dim3 grid = grid_of(four ? (blocks_of(width) + 3) / 4 : blocks_of(width), (rows + 15) / 16);
+  return with_type(type, [&](auto t) {
+    constexpr int TYPE = decltype(t)::value;
+    if (block != 1 && four)
+      hipLaunchKernelGGL((dequantize_kernel<TYPE, 4, true>), grid, dim3(kThreads), 0, stream,
+                         codes, scales, rows, width, out);
+    else if (block != 1)
+      hipLaunchKernelGGL((dequantize_kernel<TYPE, 1, true>), grid, dim3(kThreads), 0, stream,
+                         codes, scales, rows, width, out);
+    else if (four)
+      hipLaunchKernelGGL((dequantize_kernel<TYPE, 4, false>), grid, dim3(kThreads), 0, stream,
+                         codes, scales, rows, width, out);
+    else
+      hipLaunchKernelGGL((dequantize_kernel<TYPE, 1, false>), grid, dim3(kThreads), 0, stream,
+                         codes, scales, rows, width, out);
+  });
+}
+
+hipError_t launch_quantize_transposed(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                                      float* scales, hipStream_t stream) {
+  hipLaunchKernelGGL(quantize_transposed_kernel, grid_of((width + 63) / 64, blocks_of(rows)),
+                     dim3(kThreads), 0, stream, x, rows, width, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_transpose(const uint8_t* codes, int64_t rows, int32_t width, uint8_t* out,
+                            hipStream_t stream) {
+  hipLaunchKernelGGL(transpose_kernel, grid_of(blocks_of(width), blocks_of(rows)), dim3(kThreads),
+                     0, stream, codes, rows, width, out);
+  return hipGetLastError();
+}
+
+}  // namespace fp8

@@ -1,0 +1,86 @@
+// fp8_internal.h -- what the FP8 block operators' host code and kernels share.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8 {
+
+constexpr int kBlock = 128;  // values of a row under one scale; bytes of a stage of K
+__host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+// x [rows, width] (type: MOE_TYPE_*) -> codes [rows, width], scales (see moe_fp8.h)
+hipError_t launch_quantize(const void* x, int32_t type, int64_t rows, int32_t width, int32_t block,
+                           uint8_t* codes, float* scales, hipStream_t stream);
+// The same in 1 x 128 blocks of x bf16 [rows, width], width a multiple of 8: rows of codes
+// 128 blocks_of(width) bytes apart, zeros behind the values
+hipError_t launch_quantize_padded(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                                  float* scales, hipStream_t stream);
+hipError_t launch_clear(void* out, int64_t bytes, hipStream_t stream);  // a multiple of 16
+hipError_t launch_dequantize(const uint8_t* codes, const float* scales, int64_t rows,
+                             int32_t width, int32_t block, int32_t type, void* out,
+                             hipStream_t stream);
+// x bf16 [rows, width] -> its transpose in 1 x 128 blocks along the rows: codes [width, pitch],
+// pitch = 128 blocks_of(rows), zeros behind the rows; scales [blocks_of(rows), width]
+hipError_t launch_quantize_transposed(const void* x, int64_t rows, int32_t width, uint8_t* codes,
+                                      float* scales, hipStream_t stream);
+// codes [rows, width] -> [width, pitch], as above
+hipError_t launch_transpose(const uint8_t* codes, int64_t rows, int32_t width, uint8_t* out,
+                            hipStream_t stream);
+
+// D[m, n] = sum over the stages (128 bytes of a row) of sa(m, stage) sb(n, stage) times the
+// stage's sum of A(m, k) B(n, k).
+constexpr int64_t kMaxGroups = 0x7fffff;  // of 512 lanes in a launch of fewer than 2^32
+enum Mode {
+  kSquare = 0,   // B's scales: 128 x 128 blocks
+  kRowScales = 1,  // B's scales: 1 x 128 blocks
+  kTokens = 2,   // experts, square scales: A's rows are the tokens of bucketed pairs
+  kBuckets = 3,  // experts, square scales: A's rows are bucket rows
+};
+enum Epilogue {
+  kStoreBf16 = 0,
+  kStoreF32 = 1,
+  kSwiglu = 2,   // kTokens: B's rows [0, N) gate, [N, 2N) up; out codes of h, aux its scales
+  kPairs = 3,    // kBuckets: out fp32, a bucket row's at its pair's row
+  kPartial = 4,  // a share of K: fp32 sums [share][M, N]
+};
+
+struct Product {
+  const uint8_t* a;
+  const uint8_t* b;
+  const float* a_scales;  // [stage][a_rows]
+  const float* b_scales;  // block row n / 128 (square) or row n (rows), and stage, at these pitches
+  int64_t lda, ldb;       // bytes from a row to the next
+  int64_t M;
+  int32_t N;
+  int64_t K;
+  int64_t a_rows, sb_row, sb_stage;
+  void* out = nullptr;
+  float* aux = nullptr;
+  int64_t m_first = 0, m_end = 0;  // set by a launch: the rows it computes
+  // experts: the buckets (see moe_w4a16_align) of blocks as high as the tile, and the pairs;
+  // B and its scales are each expert's after the other
+  const int32_t* sorted = nullptr;
+  const int32_t* block_expert = nullptr;
+  const int32_t* n_padded = nullptr;
+  int64_t pairs = 0;
+  int32_t top_k = 1;
+};
+// How a product is cut (fp8_plan.cpp): the tile (0: 128 x 128, 1: 128 x 256, 2: 256 x 256, 3: 64
+// x 64), its work-groups, and for tiles 0 and 3 the shares of K, `share` stages each. wide: fp32
+// results, which tile 2 has no registers for.
+struct Cut {
+  int tile = 0, shares = 1, share = 1;
+  int64_t groups = 0;
+  double time = 0;  // estimate, microseconds
+};
+Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K);
+// Bytes of the shares' sums (`split`, 16-byte aligned)
+size_t product_workspace(bool wide, int64_t M, int32_t N, int64_t K);
+hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* split,
+                          hipStream_t stream);
+// The experts' products (kSwiglu, kPairs) over buckets of block_m (128 or 256) rows; M: the
+// most bucket rows, one launch's
+hipError_t launch_experts(Epilogue epilogue, const Product& p, int64_t block_m,
+                          hipStream_t stream);
+
+}  // namespace fp8
