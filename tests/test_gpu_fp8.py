@@ -4,8 +4,9 @@ The product of two codes is exact; an fp32 sum of n of them with their scales (o
 product of the two scales, one for each block's multiply-add) is off by at most (n + 2) 2^-24 of the sum
 of their magnitudes. Products with bf16 results are summed by the FP8 matrix unit, which adds eight at a
 time and cuts each off at a multiple of 2^-13 of the power of two of the largest's exponents: seven such
-errors, below 2^-10 of the sum of magnitudes; and half a step, 2^-8 of the result. In the 2-norm the two
-roundings are 2^-8 / sqrt(3) = 0.00226 at most, and the cuts measured at 2.6e-5 for these inputs: 0.0024."""
+errors, below 2^-10 of the sum of magnitudes; and half a step, 2^-8 of the result. In the 2-norm of many
+results roundings are 2^-8 / sqrt(3) = 0.00226 at most (evenly spread errors of values just above a power
+of two), and the cuts, of either sign with their products, far below the 0.00014 left to 0.0024."""
 import pytest
 import torch
 
@@ -78,14 +79,14 @@ def borders():
 
 def test_quantize_borders():
     x = borders()
-    print(x.shape)
     for lay in (x.reshape(1, -1), x):  # along a row, and a block a row
         q = moe.fp8_quantize(lay.cuda())
         codes, scales = o.quantize(lay, 1)
         assert torch.equal(q.scales.cpu().double().nan_to_num(nan=7.0), scales.nan_to_num(nan=7.0))
         assert torch.equal(q.codes.view(torch.uint8).cpu(), codes)
         back = moe.fp8_dequantize(q, dtype=torch.float32).cpu()
-        assert torch.equal(back.double().nan_to_num(nan=7.0), o.values(codes, scales, 1).nan_to_num(nan=7.0))
+        want = o.values(codes, scales, 1).float()  # 256 * 2^120 is past fp32's largest: infinity
+        assert torch.equal(back.nan_to_num(nan=7.0, posinf=8.0), want.nan_to_num(nan=7.0, posinf=8.0))
     assert back[-3:].isnan().all() and not back[:-3].isnan().any()
     one = torch.ones(130, 144).index_fill_(0, torch.tensor([129]), float("nan")).cuda()
     s = moe.fp8_quantize(one, block=128).scales.cpu()
@@ -127,7 +128,8 @@ def product_close(got, a, b, n):
     tol = (n + 2) * U * (a.abs() @ b.abs().T) + 1e-30
     if got.dtype == torch.bfloat16:
         tol = tol + CUT * (a.abs() @ b.abs().T) + BF * ref.abs()
-        assert (got.double() - ref).norm() <= 0.0024 * ref.norm()
+        if ref.numel() >= 1000:
+            assert (got.double() - ref).norm() <= 0.0024 * ref.norm()
     err = (got.double() - ref).abs()
     assert (err <= tol).all(), (err / tol).max()
 

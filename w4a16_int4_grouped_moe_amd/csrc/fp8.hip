@@ -18,28 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight values of x from `unit` eights
-template <int TYPE>
-__device__ __forceinline__ void load8(const void* x, int64_t unit, float* v) {
-  if constexpr (TYPE == MOE_TYPE_FP32) {
-    const f32x4* p = (const f32x4*)x + 2 * unit;
-    const f32x4 a = p[0], b = p[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
-  } else {
-    const u32x4 w = ((const u32x4*)x)[unit];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (TYPE == MOE_TYPE_BF16) {
-        v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-        v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xffff0000u);
-      } else {
-        const h16x2 h = __builtin_bit_cast(h16x2, (uint32_t)w[i]);
-        v[2 * i] = (float)h[0], v[2 * i + 1] = (float)h[1];
-      }
-    }
-  }
-}
 template <int TYPE>
 __device__ __forceinline__ void store8(void* x, int64_t unit, const float* v) {
   if constexpr (TYPE == MOE_TYPE_FP32) {
@@ -58,34 +36,6 @@ __device__ __forceinline__ void store8(void* x, int64_t unit, const float* v) {
     }
     ((u32x4*)x)[unit] = w;
   }
-}
-
-__device__ __forceinline__ uint32_t top8(const float* v) {
-  uint32_t top = magnitude(v[0]);
-#pragma unroll
-  for (int i = 1; i < 8; ++i) top = larger(top, magnitude(v[i]));
-  return top;
-}
-template <int CTRL>
-__device__ __forceinline__ uint32_t with_lane(uint32_t v) {
-  return larger(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
-// The largest of 16 neighbouring lanes
-__device__ __forceinline__ uint32_t top_of_16(uint32_t v) {
-  v = with_lane<0xB1>(v);   // lane ^ 1
-  v = with_lane<0x4E>(v);   // lane ^ 2
-  v = with_lane<0x141>(v);  // mirrored in eights
-  return with_lane<0x140>(v);  // mirrored in sixteens
-}
-
-__device__ __forceinline__ u32x2 codes8(const float* v, uint32_t field) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const float inverse = scale_inverse(field);
-  const u32x2 c = {pack4(v, inverse), pack4(v + 4, inverse)};
-  return field == 255 ? u32x2{0, 0} : c;
-#else
-  return u32x2{};
-#endif
 }
 
 // 1 x 128 blocks: 16 lanes a block, a work-group 16 rows of NB blocks, so that the

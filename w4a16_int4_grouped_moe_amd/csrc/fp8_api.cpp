@@ -69,6 +69,19 @@ struct Quantized {
   size_t bytes() const { return codes + scales; }
 };
 
+// Which kernel a product takes: few rows, quantised on the way where they are bf16, or by a
+// launch ahead; or tiles
+enum Path { kFew, kFewPrepared, kTiled };
+Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize, bool square) {
+  if (!square) return kTiled;
+  if (fp8::rows_fit(quantize ? fp8::kBf16 : fp8::kCodes, rows, cols, width) && rows <= 16)
+    return kFew;
+  if (!fp8::rows_fit(fp8::kCodes, rows, cols, width)) return kTiled;
+  return fp8::rows_time(rows, cols, width) < fp8::cut_of(false, rows, cols, width).time
+             ? quantize ? kFewPrepared : kFew
+             : kTiled;
+}
+
 // The shares' sums of a product, of either type of result
 size_t split_of(int64_t rows, int32_t cols, int64_t width) {
   return region(std::max(fp8::product_workspace(false, rows, cols, width),
@@ -105,8 +118,14 @@ int check_experts(const moe_fp8_experts_problem* p) {
   return MOE_OK;
 }
 
-// Rows of a bucket's block: 256-row tiles where an expert has about as many
+// Rows of a bucket's block: a few where an expert has about one, for the kernels that stream
+// weights; 256-row tiles where it has about as many
 int32_t block_of(const moe_fp8_experts_problem* p) {
+  const int64_t P = p->num_tokens * p->top_k;
+  if (P <= 4 * (int64_t)p->num_experts &&
+      fp8::rows_fit(fp8::kBf16, fp8::kFewRows, 2 * (int64_t)p->inter, p->hidden) &&
+      fp8::rows_fit(fp8::kBf16, fp8::kFewRows, p->hidden, p->inter))
+    return fp8::kFewRows;
   return p->num_tokens * p->top_k >= 256 * (int64_t)p->num_experts ? 256 : 128;
 }
 
@@ -126,13 +145,14 @@ struct Experts {
         rows(blocks * block),
         qx(p->num_tokens, p->hidden),
         qh(rows, p->inter) {
+    const bool few = block == fp8::kFewRows;  // quantises x and h on the way
     size_t at = 0;
     const auto take = [&](size_t n) {
       const size_t here = at;
       at += n;
       return here;
     };
-    x = take(qx.bytes());
+    x = take(few ? 0 : qx.bytes());
     // the bucketing writes a block's padding whole, and needs no more than pairs + E (block - 1)
     sorted = take(region(4 * (pairs + std::min<int64_t>(pairs, p->num_experts) * (block - 1))));
     block_expert = take(region(4 * blocks));
@@ -140,7 +160,7 @@ struct Experts {
     scratch = take(pairs >= kAlignMultiMin
                        ? region(4 * moe::align_scratch_ints(pairs, p->num_experts))
                        : 0);
-    h = take(qh.bytes());
+    h = take(few ? region(4 * rows * p->inter) : qh.bytes());
     y = take(region(4 * pairs * p->hidden));
     bytes = p->num_tokens ? at : 0;
   }
@@ -194,7 +214,9 @@ int moe_fp8_matmul(const void* a, const float* a_scales, const uint8_t* b, const
   if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   hipStream_t s = (hipStream_t)stream;
   uint8_t* split = (uint8_t*)workspace;
-  if (!a_scales) {
+  const bool square = b_block == MOE_FP8_SQUARE_BLOCKS, quantize = !a_scales;
+  const Path path = path_of(rows, cols, width, quantize, square);
+  if (quantize && path != kFew) {
     const Quantized q(rows, width);
     uint8_t* codes = split;
     float* scales = (float*)(codes + q.codes);
@@ -205,12 +227,15 @@ int moe_fp8_matmul(const void* a, const float* a_scales, const uint8_t* b, const
     a = codes;
     a_scales = scales;
   }
-  const bool square = b_block == MOE_FP8_SQUARE_BLOCKS;
   Product d{(const uint8_t*)a, b, a_scales, b_scales, width, width, rows, cols, width};
   d.a_rows = rows;
   d.sb_row = square ? blocks_of(width) : 1;
   d.sb_stage = square ? 1 : cols;
   d.out = out;
+  if (path != kTiled)
+    return done(fp8::launch_rows(quantize && path == kFew ? fp8::kBf16 : fp8::kCodes,
+                                 out_type == MOE_TYPE_BF16 ? fp8::kStoreBf16 : fp8::kStoreF32, d,
+                                 s));
   return done(fp8::launch_product(square ? fp8::kSquare : fp8::kRowScales,
                                   out_type == MOE_TYPE_BF16 ? fp8::kStoreBf16 : fp8::kStoreF32, d,
                                   split, s));
@@ -315,8 +340,9 @@ int moe_fp8_experts_forward(const void* x, const int32_t* topk_ids, const float*
   float *xs = (float*)(xc + w.qx.codes), *hs = (float*)(hc + w.qh.codes);
   int32_t *sorted = (int32_t*)(ws + w.sorted), *blocks = (int32_t*)(ws + w.block_expert);
   int32_t* n_padded = (int32_t*)(ws + w.n_padded);
-  hipError_t e =
-      fp8::launch_quantize(x, MOE_TYPE_BF16, T, H, MOE_FP8_ROW_BLOCKS, xc, xs, s);
+  const bool few = w.block == fp8::kFewRows;
+  hipError_t e = hipSuccess;
+  if (!few) e = fp8::launch_quantize(x, MOE_TYPE_BF16, T, H, MOE_FP8_ROW_BLOCKS, xc, xs, s);
   if (e != hipSuccess) return done(e);
   if (w.pairs >= kAlignMultiMin)
     e = moe::launch_align_multi(topk_ids, w.pairs, E, p->expert_base, w.block, sorted, blocks,
@@ -336,7 +362,10 @@ int moe_fp8_experts_forward(const void* x, const int32_t* topk_ids, const float*
   up.n_padded = n_padded;
   up.pairs = w.pairs;
   up.top_k = p->top_k;
-  if ((e = fp8::launch_experts(fp8::kSwiglu, up, w.block, s)) != hipSuccess) return done(e);
+  if (few) up.a = (const uint8_t*)x;
+  e = few ? fp8::launch_experts_rows(fp8::kSwiglu, up, w.blocks, s)
+          : fp8::launch_experts(fp8::kSwiglu, up, w.block, s);
+  if (e != hipSuccess) return done(e);
   Product down = up;
   down.a = hc;
   down.b = w2;
@@ -348,7 +377,9 @@ int moe_fp8_experts_forward(const void* x, const int32_t* topk_ids, const float*
   down.sb_row = I / kBlock;
   down.out = ws + w.y;
   down.aux = nullptr;
-  if ((e = fp8::launch_experts(fp8::kPairs, down, w.block, s)) != hipSuccess) return done(e);
+  e = few ? fp8::launch_experts_rows(fp8::kPairs, down, w.blocks, s)
+          : fp8::launch_experts(fp8::kPairs, down, w.block, s);
+  if (e != hipSuccess) return done(e);
   return done(moe::launch_combine((const float*)(ws + w.y), nullptr, topk_ids, topk_weights,
                                   (uint16_t*)out, T, H, p->top_k, E, p->expert_base, s));
 }

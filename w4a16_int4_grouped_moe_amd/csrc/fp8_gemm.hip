@@ -31,8 +31,6 @@
 namespace fp8 {
 namespace {
 
-constexpr int kRow = kBlock;  // bytes of a row per stage
-
 __host__ __device__ constexpr bool is_experts(Mode m) { return m == kTokens || m == kBuckets; }
 
 // What a lane copies of HR rows x one stage (1 KB a copy, NW waves): rows from `row0` of an
@@ -124,137 +122,7 @@ struct WaveScales {
   }
 };
 
-typedef __attribute__((address_space(3))) float* lds_f32;
-typedef const __attribute__((address_space(4))) float* const_f32;
-
-// A wave's fragments of F sub-tiles of 16 rows from `first`
-template <int F>
-struct Frags {
-  u32x4 v[F][2];
-  __device__ __forceinline__ void read(lds_bytes slot, int first, int lane) {
-    const int q = lane >> 4;
-    const int b = (lane & 15) * kRow + ((q ^ ((lane >> 1) & 7)) * 16) + first * kRow;
-#pragma unroll
-    for (int i = 0; i < F; ++i)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        v[i][s] = *(lds_u32x4)(slot + (b ^ (s * 64)) + i * 16 * kRow);
-  }
-};
-
 #if defined(__HIP_DEVICE_COMPILE__)
-__device__ __forceinline__ i32x8 join8(const u32x4 (&v)[2]) {
-  return i32x8{(int)v[0][0], (int)v[0][1], (int)v[0][2], (int)v[0][3],
-               (int)v[1][0], (int)v[1][1], (int)v[1][2], (int)v[1][3]};
-}
-// a stage's products of 16 x 16, unscaled
-__device__ __forceinline__ f32x4 mfma8(const u32x4 (&n)[2], const u32x4 (&m)[2]) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join8(n), join8(m),
-                                                          f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0,
-                                                          0);
-}
-
-// B's scales of the columns that a lane holds: one, or four a sub-tile
-template <bool ROWS, int FB>
-struct ColumnScales {
-  float v[ROWS ? FB : 1][ROWS ? 4 : 1];
-  __device__ __forceinline__ void set(float s) {
-    if constexpr (!ROWS) v[0][0] = s;
-  }
-  __device__ __forceinline__ void read(lds_bytes at, int first, int lane) {
-    if constexpr (ROWS)
-#pragma unroll
-      for (int j = 0; j < FB; ++j) {
-        const f32x4 s = *(lds_f32x4)(at + (first + 16 * j + 4 * (lane >> 4)) * 4);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[j][r] = s[r];
-      }
-  }
-};
-
-// acc += the stage's products of 16 FA rows x 16 FB columns of H halves of B, with their
-// scales. An MFMA's result is used kLag MFMAs later.
-template <bool ROWS, int H, int FA, int FB>
-__device__ __forceinline__ void mma(f32x4 (&acc)[H][FA][FB], const Frags<FB> (&n)[H],
-                                    const Frags<FA>& m, const float (&sa)[FA],
-                                    const ColumnScales<ROWS, FB> (&sb)[H]) {
-  constexpr int kAll = H * FA * FB, kLag = kAll < 4 ? kAll : 4;
-  f32x4 t[kLag];
-  each<kAll + kLag>([&](auto index) {
-    constexpr int x = decltype(index)::value;
-    if constexpr (x >= kLag) {
-      constexpr int y = x - kLag, h = y / (FA * FB), i = y / FB % FA, j = y % FB;
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[h][i][j][r] = __builtin_fmaf(
-            t[y % kLag][r], sa[i] * sb[h].v[ROWS ? j : 0][ROWS ? r : 0], acc[h][i][j][r]);
-    }
-    if constexpr (x < kAll) t[x % kLag] = mfma8(n[x / (FA * FB)].v[x % FB], m.v[x / FB % FA]);
-    __builtin_amdgcn_sched_barrier(0);  // or the compiler moves a result's use up to its MFMA
-  });
-}
-
-// Eight codes as bf16, which holds every e4m3
-__device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi) {
-  return u32x4{
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
-}
-// The same with the products summed in fp32 as the matrix units do it for bf16: in quarters of
-// the stage, widened on the way.
-template <bool ROWS, int H, int FA, int FB>
-__device__ __forceinline__ void mma_wide(f32x4 (&acc)[H][FA][FB], const Frags<FB> (&n)[H],
-                                         const Frags<FA>& m, const float (&sa)[FA],
-                                         const ColumnScales<ROWS, FB> (&sb)[H]) {
-  f32x4 t[H][FA][FB];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    u32x4 nw[H][FB], mw[FA];
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-      mw[i] = widen(m.v[i][k / 2][k % 2 * 2], m.v[i][k / 2][k % 2 * 2 + 1]);
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int j = 0; j < FB; ++j)
-        nw[h][j] = widen(n[h].v[j][k / 2][k % 2 * 2], n[h].v[j][k / 2][k % 2 * 2 + 1]);
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int i = 0; i < FA; ++i)
-#pragma unroll
-        for (int j = 0; j < FB; ++j)
-          t[h][i][j] = mfma(nw[h][j], mw[i], k ? t[h][i][j] : f32x4{0.f, 0.f, 0.f, 0.f});
-  }
-#pragma unroll
-  for (int h = 0; h < H; ++h)
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-#pragma unroll
-      for (int j = 0; j < FB; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[h][i][j][r] = __builtin_fmaf(
-              t[h][i][j][r], sa[i] * sb[h].v[ROWS ? j : 0][ROWS ? r : 0], acc[h][i][j][r]);
-}
-
-// An MFMA has no side effect: this keeps the sums on this side of the barrier that follows
-template <int H, int FA, int FB>
-__device__ __forceinline__ void hold(f32x4 (&acc)[H][FA][FB]) {
-#pragma unroll
-  for (int h = 0; h < H; ++h)
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-#pragma unroll
-      for (int j = 0; j < FB; ++j) asm volatile("" : "+v"(acc[h][i][j]));
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t with_lane(uint32_t v) {
-  return larger(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
-}
 // Four h columns from n of row m, quantised with the 31 lanes that hold the rest of the block
 __device__ __forceinline__ void emit_h(const Product& p, int64_t m, int64_t n, const f32x4& g,
                                        const f32x4& u) {
@@ -265,10 +133,7 @@ __device__ __forceinline__ void emit_h(const Product& p, int64_t m, int64_t n, c
     h[r] = g[r] * sigmoid(g[r]) * u[r];
     top = larger(top, magnitude(h[r]));
   }
-  top = with_lane<0xB1>(top);   // lane ^ 1
-  top = with_lane<0x4E>(top);   // lane ^ 2
-  top = with_lane<0x141>(top);  // mirrored in eights
-  top = with_lane<0x140>(top);  // mirrored in sixteens
+  top = top_of_16(top);
   top = larger(top, __shfl_xor(top, 16));
   const uint32_t field = scale_field(top);
   const uint32_t c = field == 255 ? 0 : pack4(h, scale_inverse(field));

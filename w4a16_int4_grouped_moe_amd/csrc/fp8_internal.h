@@ -74,10 +74,21 @@ struct Cut {
   double time = 0;  // estimate, microseconds
 };
 Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K);
+double rows_time(int64_t M, int64_t N, int64_t K);  // of the few-row kernel on codes
 // Bytes of the shares' sums (`split`, 16-byte aligned)
 size_t product_workspace(bool wide, int64_t M, int32_t N, int64_t K);
 hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* split,
                           hipStream_t stream);
+// The same for a few rows of A (fp8_rows.hip): codes, or bf16 (experts' h: fp32) rows that are
+// quantised on the way; B's scales square, all of B (an expert's) below 2 GiB. rows_fit: whether
+// the kernel takes the sizes (experts: M = kFewRows, N of W13's 2 I rows or W2's).
+enum Source { kCodes = 0, kBf16 = 1, kF32 = 2 };
+constexpr int kMostRows = 64, kFewRows = 4;  // of codes; to quantise, and of an experts' bucket
+bool rows_fit(Source source, int64_t M, int64_t N, int64_t K);
+hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream);
+// kSwiglu: from x bf16 [T, H], h fp32 [bucket rows, I]; kPairs: from that h
+hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buckets,
+                               hipStream_t stream);
 // The experts' products (kSwiglu, kPairs) over buckets of block_m (128 or 256) rows; M: the
 // most bucket rows, one launch's
 hipError_t launch_experts(Epilogue epilogue, const Product& p, int64_t block_m,

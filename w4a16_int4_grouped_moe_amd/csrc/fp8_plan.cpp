@@ -41,6 +41,17 @@ Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// Microseconds: a launch and a work-group's start and end, then what a CU spends on its
+// work-groups' loads (a 16 x 64-byte load of A holds its address path 64 cycles, a line of B
+// 18 for 8 rows), or the weights' way from memory.
+double rows_time(int64_t M, int64_t N, int64_t K) {
+  const int64_t groups = (N + 15) / 16;
+  const int tiles = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const double busy = (double)((groups + 255) / 256) * blocks_of(K) * (36 + 128 * tiles) / 2400;
+  const double memory = (double)N * K / 4.5e6;
+  return 5.0 + (busy > memory ? busy : memory);
+}
+
 size_t product_workspace(bool wide, int64_t M, int32_t N, int64_t K) {
   if (M == 0) return 0;
   const Cut c = cut_of(wide, M, N, K);

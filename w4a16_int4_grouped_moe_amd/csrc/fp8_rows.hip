@@ -1,0 +1,309 @@
+// fp8_rows.hip -- the products for a few rows, and the experts' buckets of a few
+// (gfx950): decoding, where the time is the weights' way from memory.
+//
+// A work-group owns 16 weight rows (kSwiglu: 8 gate rows and their 8 up rows) and
+// all rows of A: one, two or four 16 x 16 MFMA tiles. Its eight waves take the
+// stages of K (128 bytes of a row, one block of scales) in turn. A wave copies its stage's rows into
+// LDS in whole 128-byte lines, kD stages ahead, into a place of its own: it waits
+// for its own copies alone and never for another wave. At the end the waves'
+// sums are added in LDS, in wave order.
+//
+// A is codes, read straight into the MFMA's layout; or bf16 (or the experts' fp32 h),
+// quantised by the work-group into LDS: its first loads go out ahead of the ring's.
+// Every work-group repeats it.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fp8_device.h"
+#include "fp8_internal.h"
+
+namespace fp8 {
+namespace {
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kD = 4;  // stages of a wave in flight
+constexpr int kSlot = 16 * kRow;  // bytes of a wave's stage
+constexpr int64_t kMostExtra = 64 * 1024;  // LDS beside the ring
+
+// LDS rows of a quantised A: 16 rows at one offset lie in distinct bank groups
+__host__ __device__ inline int code_stride(int64_t K) {
+  return (int)((K + 255) / 256 * 256 + 16);
+}
+
+// LDS beside the ring: `rows` quantised rows (fresh), and the scales of A and of B, by stage
+__host__ __device__ inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t K) {
+  return (fresh ? rows * code_stride(K) : 0) + 4 * (rows + 2) * blocks_of(K);
+}
+
+template <Source SRC, Epilogue EPI, int MT>
+__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool kPaired = EPI == kSwiglu, kExperts = EPI == kSwiglu || EPI == kPairs;
+  constexpr bool kWide = EPI == kStoreF32, kFresh = SRC != kCodes;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[kWaves * kSlot], ring1[kWaves * kSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring2[kWaves * kSlot], ring3[kWaves * kSlot];
+  // quantised A, then A's scales [row][stage] and B's (kSwiglu: gate, up) [stage]
+  extern __shared__ __attribute__((aligned(16))) uint8_t qa[];
+  static_assert(kD == 4, "ring objects");
+
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int K = (int)p.K, stages = (K + kRow - 1) / kRow;
+  const int N = p.N, n0 = blockIdx.x * (kPaired ? 8 : 16);
+  const int b_rows = kPaired ? 2 * N : N;
+  int M = (int)p.M;
+  int64_t first = 0;  // experts: the bucket's first row
+  if constexpr (kExperts) {
+    first = (int64_t)blockIdx.y * kFewRows;
+    if (first >= *p.n_padded) return;  // the grid is sized for the most buckets
+    const int64_t e = uniform(p.block_expert[blockIdx.y]);
+    p.b += e * b_rows * p.ldb;
+    p.b_scales += e * (b_rows / kBlock) * p.sb_row;
+    M = 0;  // a bucket's pairs come first
+    while (M < kFewRows && (uint64_t)(int64_t)p.sorted[first + M] < (uint64_t)p.pairs) ++M;
+  }
+
+  // copies: rows 8 j + lane / 8 of the 16, whole lines, piece c of row x at c ^ ((x >> 1) & 7)
+  const int piece = ((lane & 7) ^ (lane >> 4)) * 16;
+  uint32_t woff[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int x = 8 * j + (lane >> 3);
+    const int row = kPaired ? (j == 0 ? n0 + x : N + n0 + x - 8) : n0 + x;
+    woff[j] = row < b_rows ? (uint32_t)(row * p.ldb) + (piece ^ (j * 64)) : kOut;
+  }
+  const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)p.b, 0, (int32_t)((b_rows - 1) * p.ldb + K), kBufferFlags);
+  const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)p.a, 0, kFresh ? 0 : (int32_t)((M - 1) * p.lda + K), kBufferFlags);
+  uint32_t xoff[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    xoff[i] = 16 * i + r < M ? (uint32_t)((16 * i + r) * p.lda) + 16 * q : kOut;
+
+  u32x4 x[kFresh ? 1 : kD][MT][2];
+  // a stage's loads, all of them always issued, so that a wave's waits can count them
+  constexpr int kLoads = 2 + (kFresh ? 0 : 2 * MT);
+  auto load = [&](auto slot, int s) {
+    constexpr int d = decltype(slot)::value;
+    const bool live = s < stages;
+    const lds_bytes dst = (lds_bytes)(d == 0 ? ring0 : d == 1 ? ring1 : d == 2 ? ring2 : ring3) +
+                          wave * kSlot;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const bool in = live && (piece ^ (j * 64)) < K - s * kRow;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_ptr)(dst + j * 1024), 16,
+                                               in ? woff[j] + (uint32_t)(s * kRow) : kOut, 0, 0,
+                                               2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!kFresh) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const bool in = s * kRow + h * 64 + 16 * q < K;
+          x[d][i][h] = __builtin_amdgcn_raw_buffer_load_b128(
+              xres, in ? xoff[i] + (uint32_t)(s * kRow + h * 64) : kOut, 0, 0);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto fill = [&] { each<kD>([&](auto d) { load(d, wave + decltype(d)::value * kWaves); }); };
+
+  const int stride = code_stride(K), rows = kExperts ? kFewRows : M;
+  float* const as = (float*)(qa + (kFresh ? rows * stride : 0));
+  float* const bs = as + rows * stages;
+  // scales into LDS; the first ones are asked for ahead of the ring's copies
+  auto b_scale = [&](int i) {
+    const int up = i >= stages;
+    return p.b_scales[(int64_t)((up ? N + n0 : n0) / kBlock) * p.sb_row + i - up * stages];
+  };
+  const int b_count = (kPaired ? 2 : 1) * stages;
+  const float b_first = (int)threadIdx.x < b_count ? b_scale(threadIdx.x) : 0.f;
+  if constexpr (!kFresh) {
+    constexpr int kPre = 8;
+    float pre[kPre];
+    const int count = M * stages;
+#pragma unroll
+    for (int i = 0; i < kPre; ++i) {
+      const int at = i * kThreads + threadIdx.x;
+      pre[i] = at < count ? p.a_scales[at % stages * p.a_rows + at / stages] : 0.f;
+    }
+    fill();
+#pragma unroll
+    for (int i = 0; i < kPre; ++i) {
+      const int at = i * kThreads + threadIdx.x;
+      if (at < count) as[at] = pre[i];
+    }
+    for (int at = kPre * kThreads + threadIdx.x; at < count; at += kThreads)
+      as[at] = p.a_scales[at % stages * p.a_rows + at / stages];
+  } else {
+    // eights of a row over the threads, 16 a block; kAtOnce turns under way
+    constexpr int kType = SRC == kBf16 ? MOE_TYPE_BF16 : MOE_TYPE_FP32, kAtOnce = 4;
+    const int units = K / 8, turns = (stages * 16 + kThreads - 1) / kThreads;
+    const int total = M * turns;
+    for (int t = 0;; t += kAtOnce) {
+      float v[kAtOnce][8];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int row = (t + i) / turns, u = (t + i) % turns * kThreads + threadIdx.x;
+        if (t + i < total && u < units) {
+          int64_t src = row;
+          if constexpr (EPI == kSwiglu) src = p.sorted[first + row] / p.top_k;
+          if constexpr (EPI == kPairs) src = first + row;
+          load8<kType>(p.a, src * units + u, v[i]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+        }
+      }
+      if (t == 0) fill();
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int row = (t + i) / turns, u = (t + i) % turns * kThreads + threadIdx.x;
+        const uint32_t field = scale_field(top_of_16(top8(v[i])));
+        if (t + i < total && u < stages * 16) {
+          *(u32x2*)(qa + row * stride + u * 8) = codes8(v[i], field);
+          if ((u & 15) == 0) as[row * stages + u / 16] = scale_value(field);
+        }
+      }
+      if (t + kAtOnce >= total) break;
+    }
+  }
+  if ((int)threadIdx.x < b_count) bs[threadIdx.x] = b_first;
+  for (int i = kThreads + threadIdx.x; i < b_count; i += kThreads) bs[i] = b_scale(i);
+  wait_lgkm0();
+  __builtin_amdgcn_s_barrier();  // (no wait for the ring's copies)
+  __builtin_amdgcn_sched_barrier(0);
+
+  f32x4 acc[1][MT][1];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[0][i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto step = [&](auto slot, int s) {
+    constexpr int d = decltype(slot)::value;
+    const lds_bytes src = (lds_bytes)(d == 0 ? ring0 : d == 1 ? ring1 : d == 2 ? ring2 : ring3) +
+                          wave * kSlot;
+    Frags<1> w[1];
+    Frags<MT> m;
+    float sa[MT];
+    ColumnScales<false, 1> cs[1];
+    wait_vm<(kD - 1) * kLoads>();  // this stage's copies have landed
+    __builtin_amdgcn_sched_barrier(0);
+    w[0].read(src, 0, lane);
+    cs[0].set(bs[kPaired && q >= 2 ? stages + s : s]);  // rows 4 q .. 4 q + 3: one square block
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if constexpr (kFresh) {
+        const int row = r < M ? r : 0;  // sums past the last row are not stored
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          m.v[i][h] = *(const u32x4*)(qa + row * stride + s * kRow + h * 64 + 16 * q);
+        sa[i] = as[row * stages + s];
+      } else {
+        m.v[i][0] = x[d][i][0], m.v[i][1] = x[d][i][1];
+        sa[i] = as[(16 * i + r < M ? 16 * i + r : 0) * stages + s];
+      }
+    }
+    if constexpr (kWide)
+      mma_wide<false, 1, MT, 1>(acc, w, m, sa, cs);
+    else
+      mma<false, 1, MT, 1>(acc, w, m, sa, cs);
+    hold(acc);
+    wait_lgkm0();  // the place is read before the next copy into it goes out
+    load(slot, s + kD * kWaves);
+  };
+  for (int s = wave; s < stages; s += kD * kWaves)
+    each<kD>([&](auto d) {
+      const int at = s + decltype(d)::value * kWaves;
+      if (at < stages) step(d, at);  // uniform: a wave's stages are its own
+    });
+
+  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row 16 i + r
+  wait_vm<0>();  // the copies past the last stage land before the LDS holds the sums
+  __syncthreads();
+  float* const sums = (float*)ring0;  // two tiles an object
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    float* const at = i < 2 ? sums : (float*)ring1;
+    *(f32x4*)&at[(wave * 2 + (i & 1)) * 256 + r * 16 + 4 * q] = acc[0][i][0];
+  }
+  __syncthreads();
+  if constexpr (kPaired) {
+    for (int i = threadIdx.x; i < 128; i += kThreads) {
+      const int m = i >> 3, j = i & 7;
+      if (m >= M) break;
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) {
+        g += sums[k * 512 + m * 16 + j];
+        u += sums[k * 512 + m * 16 + 8 + j];
+      }
+      ((float*)p.out)[(first + m) * N + n0 + j] = g * sigmoid(g) * u;
+    }
+  } else {
+    for (int i = threadIdx.x; i < 256 * MT; i += kThreads) {
+      const int m = i >> 4, n = n0 + (i & 15), tile = i >> 8;
+      if (m >= M) break;
+      if (n >= N) continue;
+      const float* const at = (tile < 2 ? sums : (const float*)ring1) + (tile & 1) * 256 + (i & 255);
+      float v = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) v += at[k * 512];
+      if constexpr (EPI == kPairs)
+        ((float*)p.out)[(int64_t)p.sorted[first + m] * N + n] = v;
+      else if constexpr (EPI == kStoreF32)
+        ((float*)p.out)[(int64_t)m * N + n] = v;
+      else
+        ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
+    }
+  }
+#endif
+}
+
+template <Source SRC, Epilogue EPI, int MT>
+hipError_t launch_tiles(const Product& p, int64_t buckets, hipStream_t stream) {
+  const unsigned groups = (p.N + (EPI == kSwiglu ? 7 : 15)) / (EPI == kSwiglu ? 8 : 16);
+  const int64_t rows = EPI == kSwiglu || EPI == kPairs ? kFewRows : p.M;
+  const size_t lds = extra_bytes(SRC != kCodes, rows, p.K);
+  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT>), dim3(groups, (unsigned)buckets), dim3(kThreads),
+                     lds, stream, p);
+  return hipGetLastError();
+}
+template <Source SRC, Epilogue EPI>
+hipError_t launch(const Product& p, hipStream_t stream) {
+  if constexpr (SRC == kCodes) {
+    if (p.M > 32) return launch_tiles<SRC, EPI, 4>(p, 1, stream);
+    if (p.M > 16) return launch_tiles<SRC, EPI, 2>(p, 1, stream);
+  }
+  return launch_tiles<SRC, EPI, 1>(p, 1, stream);
+}
+
+}  // namespace
+
+bool rows_fit(Source source, int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= (source == kCodes ? kMostRows : kFewRows) && N < (1 << 26) && N * K <= 0x7fffffff &&
+         extra_bytes(source != kCodes, M, K) <= kMostExtra;
+}
+
+hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream) {
+  if (source == kCodes)
+    return epilogue == kStoreBf16 ? launch<kCodes, kStoreBf16>(p, stream)
+                                  : launch<kCodes, kStoreF32>(p, stream);
+  if (source == kBf16)
+    return epilogue == kStoreBf16 ? launch<kBf16, kStoreBf16>(p, stream)
+                                  : launch<kBf16, kStoreF32>(p, stream);
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buckets,
+                               hipStream_t stream) {
+  if (epilogue == kSwiglu) return launch_tiles<kBf16, kSwiglu, 1>(p, buckets, stream);
+  if (epilogue == kPairs) return launch_tiles<kF32, kPairs, 1>(p, buckets, stream);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace fp8
