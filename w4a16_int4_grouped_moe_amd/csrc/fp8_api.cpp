@@ -119,14 +119,14 @@ int check_experts(const moe_fp8_experts_problem* p) {
 }
 
 // Rows of a bucket's block: a few where an expert has about one, for the kernels that stream
-// weights; 256-row tiles where it has about as many
+// weights; else a tile's (how many pairs are local, only the device knows)
 int32_t block_of(const moe_fp8_experts_problem* p) {
   const int64_t P = p->num_tokens * p->top_k;
   if (P <= 4 * (int64_t)p->num_experts &&
       fp8::rows_fit(fp8::kBf16, fp8::kFewRows, 2 * (int64_t)p->inter, p->hidden) &&
       fp8::rows_fit(fp8::kBf16, fp8::kFewRows, p->hidden, p->inter))
     return fp8::kFewRows;
-  return p->num_tokens * p->top_k >= 256 * (int64_t)p->num_experts ? 256 : 128;
+  return fp8::kBigRows;
 }
 
 struct Experts {
@@ -364,7 +364,7 @@ int moe_fp8_experts_forward(const void* x, const int32_t* topk_ids, const float*
   up.top_k = p->top_k;
   if (few) up.a = (const uint8_t*)x;
   e = few ? fp8::launch_experts_rows(fp8::kSwiglu, up, w.blocks, s)
-          : fp8::launch_experts(fp8::kSwiglu, up, w.block, s);
+          : fp8::launch_experts(fp8::kSwiglu, up, s);
   if (e != hipSuccess) return done(e);
   Product down = up;
   down.a = hc;
@@ -378,7 +378,7 @@ int moe_fp8_experts_forward(const void* x, const int32_t* topk_ids, const float*
   down.out = ws + w.y;
   down.aux = nullptr;
   e = few ? fp8::launch_experts_rows(fp8::kPairs, down, w.blocks, s)
-          : fp8::launch_experts(fp8::kPairs, down, w.block, s);
+          : fp8::launch_experts(fp8::kPairs, down, s);
   if (e != hipSuccess) return done(e);
   return done(moe::launch_combine((const float*)(ws + w.y), nullptr, topk_ids, topk_weights,
                                   (uint16_t*)out, T, H, p->top_k, E, p->expert_base, s));

@@ -31,8 +31,6 @@
 namespace fp8 {
 namespace {
 
-__host__ __device__ constexpr bool is_experts(Mode m) { return m == kTokens || m == kBuckets; }
-
 // What a lane copies of HR rows x one stage (1 KB a copy, NW waves): rows from `row0` of an
 // operand of `rows` rows, or those that `token` names.
 template <int HR, int NW>
@@ -198,54 +196,46 @@ __device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int6
 //   1   3        0      A0 B0 B1   all of s + 2           all of s + 1
 //
 // The scales travel with A0: they are read in the first phase.
-template <int AH, Mode MODE, Epilogue EPI, bool WIDE>
-__global__ __launch_bounds__(512, 2) void big_tile_kernel(Product p) {
+// An object a half tile and a stage's scales: the compiler then sees which copies a read has to
+// wait for. x: AH = 2: the second A halves of the two buffers; AH = 1: the third buffer.
+struct BigLds {
+  lds_bytes a0, b0, c0, a1, b1, c1, x0, x1, x2, s0, s1, s2;
+};
+#define FP8_BIG_LDS(third)                                                                  \
+  __shared__ __attribute__((aligned(1024))) uint8_t msa0[kHalf], msb0[kHalf], msc0[kHalf];  \
+  __shared__ __attribute__((aligned(1024))) uint8_t msa1[kHalf], msb1[kHalf], msc1[kHalf];  \
+  __shared__ __attribute__((aligned(1024))) uint8_t msx0[kHalf], msx1[kHalf];               \
+  __shared__ __attribute__((aligned(1024))) uint8_t msx2[(third) ? kHalf : 16];             \
+  __shared__ __attribute__((aligned(16))) uint8_t mss0[2048], mss1[2048];                   \
+  __shared__ __attribute__((aligned(16))) uint8_t mss2[(third) ? 2048 : 16];                \
+  const BigLds lds = {(lds_bytes)msa0, (lds_bytes)msb0, (lds_bytes)msc0, (lds_bytes)msa1,   \
+                      (lds_bytes)msb1, (lds_bytes)msc1, (lds_bytes)msx0, (lds_bytes)msx1,   \
+                      (lds_bytes)msx2, (lds_bytes)mss0, (lds_bytes)mss1, (lds_bytes)mss2};
+constexpr int kHalf = 128 * kRow;
+
 #if defined(__HIP_DEVICE_COMPILE__)
+// The tile at row tile tm_id, column tile tn_id; idle: this wave's rows are all padding
+template <int AH, Mode MODE, Epilogue EPI, bool WIDE>
+__device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m0, int64_t n0,
+                                         bool idle) {
   constexpr int NW = 8, HR = 128, FA = 4, FB = 2;
   constexpr bool kPaired = EPI == kSwiglu, kRows = MODE == kRowScales;
-  constexpr int kCols = kPaired ? HR : 2 * HR;
   typedef Operand<HR, NW> Half;
-  constexpr int kBytes = HR * kRow, kCopies = Half::kPer;
-  // an object a half tile: the compiler then sees which copies a read has to wait for
-  __shared__ __attribute__((aligned(1024))) uint8_t msa0[kBytes], msb0[kBytes], msc0[kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t msa1[kBytes], msb1[kBytes], msc1[kBytes];
-  // AH = 2: the second A halves of the two buffers; AH = 1: the third buffer
-  __shared__ __attribute__((aligned(1024))) uint8_t msx0[kBytes], msx1[kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t msx2[AH == 1 ? kBytes : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t mss0[2048], mss1[2048];
-  __shared__ __attribute__((aligned(16))) uint8_t mss2[AH == 1 ? 2048 : 16];
-  const lds_bytes sa0 = (lds_bytes)msa0, sb0 = (lds_bytes)msb0, sc0 = (lds_bytes)msc0;
-  const lds_bytes sa1 = (lds_bytes)msa1, sb1 = (lds_bytes)msb1, sc1 = (lds_bytes)msc1;
-  const lds_bytes sx0 = (lds_bytes)msx0, sx1 = (lds_bytes)msx1, sx2 = (lds_bytes)msx2;
-  const lds_bytes ss0 = (lds_bytes)mss0, ss1 = (lds_bytes)mss1, ss2 = (lds_bytes)mss2;
-
+  constexpr int kCopies = Half::kPer;
+  const lds_bytes sa0 = lds.a0, sb0 = lds.b0, sc0 = lds.c0, sa1 = lds.a1, sb1 = lds.b1;
+  const lds_bytes sc1 = lds.c1, sx0 = lds.x0, sx1 = lds.x1, sx2 = lds.x2;
+  const lds_bytes ss0 = lds.s0, ss1 = lds.s1, ss2 = lds.s2;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const int64_t tn = (p.N + kCols - 1) / kCols;
-  int64_t tm;
-  if constexpr (is_experts(MODE)) {
-    tm = *p.n_padded / (AH * HR);
-    if ((int64_t)blockIdx.x >= tm * tn) return;  // the grid is sized for the most buckets
-  } else {
-    tm = (p.m_end - p.m_first + AH * HR - 1) / (AH * HR);
-  }
-  const TileId t = tile_of(blockIdx.x, tm, tn);
-  const int64_t m0 = p.m_first + t.m * (AH * HR), n0 = t.n * kCols;
   const int stages = (int)((p.K + kRow - 1) / kRow);
-  const int64_t b_rows = kPaired ? 2 * (int64_t)p.N : p.N;
-  if constexpr (is_experts(MODE)) {
-    const int64_t e = uniform(p.block_expert[t.m]);
-    p.b += e * b_rows * p.ldb;
-    p.b_scales += e * (b_rows / kBlock) * p.sb_row;
-  }
 
   Half a[AH], b0, b1;
   WaveScales scales;  // waves 0 .. 2 AH - 1: A's rows; kRows: 4 .. 7: B's
   if constexpr (MODE == kTokens) {
     const int64_t tokens = p.a_rows;
     auto token = [&](int row) {
-      const int64_t pair = p.sorted[m0 + row];
-      return (uint64_t)pair < (uint64_t)p.pairs ? (int32_t)(pair / p.top_k) : -1;
+      const int32_t pair = p.sorted[m0 + row];
+      return (uint32_t)pair < (uint32_t)p.pairs ? pair / p.top_k : -1;
     };
 #pragma unroll
     for (int h = 0; h < AH; ++h)
@@ -309,11 +299,13 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(Product p) {
   __builtin_amdgcn_s_barrier();          \
   __builtin_amdgcn_sched_barrier(0);
 #define FP8_MMA(ah)                                              \
-  if constexpr (WIDE)                                            \
-    mma_wide<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);     \
-  else                                                           \
-    mma<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);          \
-  hold(acc[ah]);
+  if (!idle) {                                                   \
+    if constexpr (WIDE)                                          \
+      mma_wide<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);   \
+    else                                                         \
+      mma<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);        \
+    hold(acc[ah]);                                               \
+  }
 
   // stage s in buffer `buf`; its scales are read in its first phase, so that their place is
   // free for stage s + 2 in the second
@@ -328,16 +320,18 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(Product p) {
       cs[0].set(sq0[s * p.sb_stage]);
       cs[1].set(sq1[s * p.sb_stage]);
     }
-    fa.read(a_now, wm * 64, lane);
-    fb[0].read(b0_now, wn * 32, lane);
-    fb[1].read(b1_now, wn * 32, lane);
+    if (!idle) {
+      fa.read(a_now, wm * 64, lane);
+      fb[0].read(b0_now, wn * 32, lane);
+      fb[1].read(b1_now, wn * 32, lane);
 #pragma unroll
-    for (int h = 0; h < AH; ++h)
+      for (int h = 0; h < AH; ++h)
 #pragma unroll
-      for (int i = 0; i < FA; ++i)
-        sa[h][i] = *(lds_f32)(ss_now + (h * HR + wm * 64 + i * 16 + (lane & 15)) * 4);
-    cs[0].read(ss_now + 1024, wn * 32, lane);
-    cs[1].read(ss_now + 1024, HR + wn * 32, lane);
+        for (int i = 0; i < FA; ++i)
+          sa[h][i] = *(lds_f32)(ss_now + (h * HR + wm * 64 + i * 16 + (lane & 15)) * 4);
+      cs[0].read(ss_now + 1024, wn * 32, lane);
+      cs[1].read(ss_now + 1024, HR + wn * 32, lane);
+    }
     if constexpr (AH == 2) {
       __builtin_amdgcn_sched_barrier(0);  // the reads first: copies wait for their queue
       a[1].copy(buf ? sx0 : sx1, s + 1, wave);
@@ -414,8 +408,48 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(Product p) {
     store_rows<EPI, 16, 256>(p, mine, m0 + h * HR + wave * 16, n0, lane);
     wait_lgkm0();
   }
+}
+#endif
+
+template <int AH, Mode MODE, Epilogue EPI, bool WIDE>
+__global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8_BIG_LDS(AH == 1)
+  const int64_t tm = (p.m_end - p.m_first + AH * 128 - 1) / (AH * 128), tn = (p.N + 255) / 256;
+  const TileId t = tile_of(blockIdx.x, tm, tn);
+  big_tile<AH, MODE, EPI, WIDE>(p, lds, p.m_first + t.m * (AH * 128), t.n * 256, false);
 #endif
 }
+
+// The experts' products, a work-group a bucket block of 256 rows x 256 columns (kSwiglu: 128
+// gate, 128 up): a block of 128 pairs or fewer as a 128 x 256 tile, of 64 or fewer on half
+// the waves, which leaves the time to the weights' copies.
+template <Mode MODE, Epilogue EPI>
+__global__ __launch_bounds__(512, 2) void experts_kernel(Product p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  FP8_BIG_LDS(true)
+  constexpr int kCols = EPI == kSwiglu ? 128 : 256;
+  const int64_t tm = *p.n_padded / kBigRows, tn = (p.N + kCols - 1) / kCols;
+  if ((int64_t)blockIdx.x >= tm * tn) return;  // the grid is sized for the most buckets
+  const TileId t = tile_of(blockIdx.x, tm, tn);
+  const int64_t m0 = t.m * kBigRows, n0 = t.n * kCols;
+  const int64_t b_rows = EPI == kSwiglu ? 2 * (int64_t)p.N : p.N;
+  const int64_t e = uniform(p.block_expert[t.m]);
+  p.b += e * b_rows * p.ldb;
+  p.b_scales += e * (b_rows / kBlock) * p.sb_row;
+  // a block's pairs come first
+  const auto filled = [&](int row) {
+    return uniform((uint32_t)p.sorted[m0 + row] < (uint32_t)p.pairs) != 0;
+  };
+  if (filled(128)) {
+    big_tile<2, MODE, EPI, false>(p, lds, m0, n0, false);
+  } else {
+    const bool idle = (threadIdx.x >> 8) != 0 && !filled(64);
+    big_tile<1, MODE, EPI, false>(p, lds, m0, n0, uniform(idle) != 0);
+  }
+#endif
+}
+#undef FP8_BIG_LDS
 
 // A small tile's ring of stages (four of 128 x 128, eight of 64 x 64): an object
 // a stage and operand, so that the compiler sees which copies a read has to wait
@@ -561,7 +595,7 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ sum
 
 template <int AH, Mode MODE, Epilogue EPI, bool WIDE = false>
 hipError_t launch_big(Product p, hipStream_t stream) {
-  const int64_t cols = EPI == kSwiglu ? 128 : 256, tn = (p.N + cols - 1) / cols;
+  const int64_t tn = (p.N + 255) / 256;
   const int64_t most = kMaxGroups / tn * (AH * 128);
   for (int64_t m = 0; m < p.M; m += most) {
     p.m_first = m;
@@ -621,15 +655,16 @@ hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* 
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_experts(Epilogue epilogue, const Product& p, int64_t block_m,
-                          hipStream_t stream) {
+hipError_t launch_experts(Epilogue epilogue, const Product& p, hipStream_t stream) {
+  const int64_t cols = epilogue == kSwiglu ? 128 : 256;
+  const dim3 grid((unsigned)(p.M / kBigRows * ((p.N + cols - 1) / cols)));
   if (epilogue == kSwiglu)
-    return block_m == 256 ? launch_big<2, kTokens, kSwiglu>(p, stream)
-                          : launch_big<1, kTokens, kSwiglu>(p, stream);
-  if (epilogue == kPairs)
-    return block_m == 256 ? launch_big<2, kBuckets, kPairs>(p, stream)
-                          : launch_big<1, kBuckets, kPairs>(p, stream);
-  return hipErrorInvalidValue;
+    hipLaunchKernelGGL((experts_kernel<kTokens, kSwiglu>), grid, dim3(512), 0, stream, p);
+  else if (epilogue == kPairs)
+    hipLaunchKernelGGL((experts_kernel<kBuckets, kPairs>), grid, dim3(512), 0, stream, p);
+  else
+    return hipErrorInvalidValue;
+  return hipGetLastError();
 }
 
 }  // namespace fp8

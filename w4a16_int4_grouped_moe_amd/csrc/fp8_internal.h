@@ -89,9 +89,9 @@ hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipSt
 // kSwiglu: from x bf16 [T, H], h fp32 [bucket rows, I]; kPairs: from that h
 hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buckets,
                                hipStream_t stream);
-// The experts' products (kSwiglu, kPairs) over buckets of block_m (128 or 256) rows; M: the
-// most bucket rows, one launch's
-hipError_t launch_experts(Epilogue epilogue, const Product& p, int64_t block_m,
-                          hipStream_t stream);
+// The experts' products (kSwiglu, kPairs) over buckets of kBigRows rows; M: the most bucket
+// rows, a launch's of at most kMaxGroups tiles
+constexpr int kBigRows = 256;
+hipError_t launch_experts(Epilogue epilogue, const Product& p, hipStream_t stream);
 
 }  // namespace fp8
