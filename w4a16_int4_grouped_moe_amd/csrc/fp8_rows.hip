@@ -24,7 +24,6 @@ namespace fp8 {
 namespace {
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kD = 4;  // stages of a wave in flight
 constexpr int kSlot = 16 * kRow;  // bytes of a wave's stage
 constexpr int64_t kMostExtra = 64 * 1024;  // LDS beside the ring
 
@@ -38,16 +37,22 @@ __host__ __device__ inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t
   return (fresh ? rows * code_stride(K) : 0) + 4 * (rows + 2) * blocks_of(K);
 }
 
-template <Source SRC, Epilogue EPI, int MT>
+template <Source SRC, Epilogue EPI, int MT, int kD>
 __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu, kExperts = EPI == kSwiglu || EPI == kPairs;
   constexpr bool kWide = EPI == kStoreF32, kFresh = SRC != kCodes;
+  // an object a stage: the compiler then sees which copies a read has to wait for
   __shared__ __attribute__((aligned(1024))) uint8_t ring0[kWaves * kSlot], ring1[kWaves * kSlot];
-  __shared__ __attribute__((aligned(1024))) uint8_t ring2[kWaves * kSlot], ring3[kWaves * kSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring2[kWaves * kSlot];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring3[kD > 3 ? kWaves * kSlot : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring4[kD > 4 ? kWaves * kSlot : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring5[kD > 5 ? kWaves * kSlot : 16];
+  const lds_bytes ring[6] = {(lds_bytes)ring0, (lds_bytes)ring1, (lds_bytes)ring2,
+                             (lds_bytes)ring3, (lds_bytes)ring4, (lds_bytes)ring5};
   // quantised A, then A's scales [row][stage] and B's (kSwiglu: gate, up) [stage]
   extern __shared__ __attribute__((aligned(16))) uint8_t qa[];
-  static_assert(kD == 4, "ring objects");
+  static_assert(kD >= 3 && kD <= 6, "ring objects");
 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
@@ -90,8 +95,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   auto load = [&](auto slot, int s) {
     constexpr int d = decltype(slot)::value;
     const bool live = s < stages;
-    const lds_bytes dst = (lds_bytes)(d == 0 ? ring0 : d == 1 ? ring1 : d == 2 ? ring2 : ring3) +
-                          wave * kSlot;
+    const lds_bytes dst = ring[d] + wave * kSlot;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const bool in = live && (piece ^ (j * 64)) < K - s * kRow;
@@ -185,8 +189,7 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   for (int i = 0; i < MT; ++i) acc[0][i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto step = [&](auto slot, int s) {
     constexpr int d = decltype(slot)::value;
-    const lds_bytes src = (lds_bytes)(d == 0 ? ring0 : d == 1 ? ring1 : d == 2 ? ring2 : ring3) +
-                          wave * kSlot;
+    const lds_bytes src = ring[d] + wave * kSlot;
     Frags<1> w[1];
     Frags<MT> m;
     float sa[MT];
@@ -269,7 +272,8 @@ hipError_t launch_tiles(const Product& p, int64_t buckets, hipStream_t stream) {
   const unsigned groups = (p.N + (EPI == kSwiglu ? 7 : 15)) / (EPI == kSwiglu ? 8 : 16);
   const int64_t rows = EPI == kSwiglu || EPI == kPairs ? kFewRows : p.M;
   const size_t lds = extra_bytes(SRC != kCodes, rows, p.K);
-  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT>), dim3(groups, (unsigned)buckets), dim3(kThreads),
+  constexpr int kD = EPI == kSwiglu || EPI == kPairs ? 3 : MT == 1 ? 6 : MT == 2 ? 4 : 3;
+  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT, kD>), dim3(groups, (unsigned)buckets), dim3(kThreads),
                      lds, stream, p);
   return hipGetLastError();
 }
