@@ -2,7 +2,8 @@
 // (gfx950): decoding, where the time is the weights' way from memory.
 //
 // A work-group owns 16 weight rows (kSwiglu: 8 gate rows and their 8 up rows) and
-// all rows of A: one, two or four 16 x 16 MFMA tiles. Its eight waves take the
+// all rows of A: one, two or four 16 x 16 MFMA tiles; of the experts' short rows several such
+// slices, so that a quantised A serves longer streams. Its eight waves take the
 // stages of K (128 bytes of a row, one block of scales) in turn. A wave copies its stage's rows into
 // LDS in whole 128-byte lines, kD stages ahead, into a place of its own: it waits
 // for its own copies alone and never for another wave. At the end the waves'
@@ -32,13 +33,18 @@ __host__ __device__ inline int code_stride(int64_t K) {
   return (int)((K + 255) / 256 * 256 + 16);
 }
 
-// LDS beside the ring: `rows` quantised rows (fresh), and the scales of A and of B, by stage
-__host__ __device__ inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t K) {
-  return (fresh ? rows * code_stride(K) : 0) + 4 * (rows + 2) * blocks_of(K);
+// LDS beside the ring: `rows` quantised rows (fresh), the scales of A and of B, by stage, and
+// (fresh) the waves' sums of each slice
+__host__ __device__ inline int64_t sums_at(bool fresh, int64_t rows, int64_t K) {
+  return (fresh ? rows * code_stride(K) : 0) + (4 * (rows + 2) * blocks_of(K) + 15) / 16 * 16;
+}
+inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t K, int slices) {
+  return sums_at(fresh, rows, K) + (fresh ? slices * kWaves * rows * 64 : 0);
 }
 
 template <Source SRC, Epilogue EPI, int MT, int kD>
-__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product p) {
+__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product p,
+                                                                              const int slices) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu, kExperts = EPI == kSwiglu || EPI == kPairs;
   constexpr bool kWide = EPI == kStoreF32, kFresh = SRC != kCodes;
@@ -57,7 +63,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int K = (int)p.K, stages = (K + kRow - 1) / kRow;
-  const int N = p.N, n0 = blockIdx.x * (kPaired ? 8 : 16);
+  constexpr int kStep = kPaired ? 8 : 16;  // columns of a slice
+  const int N = p.N, n0 = blockIdx.x * kStep * slices;
   const int b_rows = kPaired ? 2 * N : N;
   int M = (int)p.M;
   int64_t first = 0;  // experts: the bucket's first row
@@ -92,16 +99,20 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   u32x4 x[kFresh ? 1 : kD][MT][2];
   // a stage's loads, all of them always issued, so that a wave's waits can count them
   constexpr int kLoads = 2 + (kFresh ? 0 : 2 * MT);
-  auto load = [&](auto slot, int s) {
+  // this wave's stages, slice after slice; the next one to load
+  const int per = wave < stages ? (stages - wave + kWaves - 1) / kWaves : 0, total = per * slices;
+  int next_s = wave, next_slice = 0;
+  auto load = [&](auto slot) {
     constexpr int d = decltype(slot)::value;
-    const bool live = s < stages;
     const lds_bytes dst = ring[d] + wave * kSlot;
+    const int s = next_s, slice = next_slice;
+    const bool live = slice < slices && s < stages;
+    const uint32_t from = (uint32_t)(slice * kStep * p.ldb) + (uint32_t)(s * kRow);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const bool in = live && (piece ^ (j * 64)) < K - s * kRow;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(wres, (lds_ptr)(dst + j * 1024), 16,
-                                               in ? woff[j] + (uint32_t)(s * kRow) : kOut, 0, 0,
-                                               2);
+                                               in ? woff[j] + from : kOut, 0, 0, 2);
     }
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!kFresh) {
@@ -115,8 +126,10 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
         }
       __builtin_amdgcn_sched_barrier(0);
     }
+    next_s += kWaves;
+    if (next_s >= stages) next_s = wave, ++next_slice;
   };
-  auto fill = [&] { each<kD>([&](auto d) { load(d, wave + decltype(d)::value * kWaves); }); };
+  auto fill = [&] { each<kD>([&](auto d) { load(d); }); };
 
   const int stride = code_stride(K), rows = kExperts ? kFewRows : M;
   float* const as = (float*)(qa + (kFresh ? rows * stride : 0));
@@ -149,13 +162,13 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
     // eights of a row over the threads, 16 a block; kAtOnce turns under way
     constexpr int kType = SRC == kBf16 ? MOE_TYPE_BF16 : MOE_TYPE_FP32, kAtOnce = 4;
     const int units = K / 8, turns = (stages * 16 + kThreads - 1) / kThreads;
-    const int total = M * turns;
+    const int all = M * turns;
     for (int t = 0;; t += kAtOnce) {
       float v[kAtOnce][8];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int row = (t + i) / turns, u = (t + i) % turns * kThreads + threadIdx.x;
-        if (t + i < total && u < units) {
+        if (t + i < all && u < units) {
           int64_t src = row;
           if constexpr (EPI == kSwiglu) src = p.sorted[first + row] / p.top_k;
           if constexpr (EPI == kPairs) src = first + row;
@@ -170,12 +183,12 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
       for (int i = 0; i < kAtOnce; ++i) {
         const int row = (t + i) / turns, u = (t + i) % turns * kThreads + threadIdx.x;
         const uint32_t field = scale_field(top_of_16(top8(v[i])));
-        if (t + i < total && u < stages * 16) {
+        if (t + i < all && u < stages * 16) {
           *(u32x2*)(qa + row * stride + u * 8) = codes8(v[i], field);
           if ((u & 15) == 0) as[row * stages + u / 16] = scale_value(field);
         }
       }
-      if (t + kAtOnce >= total) break;
+      if (t + kAtOnce >= all) break;
     }
   }
   if ((int)threadIdx.x < b_count) bs[threadIdx.x] = b_first;
@@ -217,51 +230,64 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
       mma<false, 1, MT, 1>(acc, w, m, sa, cs);
     hold(acc);
     wait_lgkm0();  // the place is read before the next copy into it goes out
-    load(slot, s + kD * kWaves);
+    load(slot);
   };
-  for (int s = wave; s < stages; s += kD * kWaves)
-    each<kD>([&](auto d) {
-      const int at = s + decltype(d)::value * kWaves;
-      if (at < stages) step(d, at);  // uniform: a wave's stages are its own
-    });
-
   // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row 16 i + r
-  wait_vm<0>();  // the copies past the last stage land before the LDS holds the sums
+  float* const kept = (float*)(qa + sums_at(kFresh, rows, K));  // fresh: [wave][slice][row][16]
+  int s = wave, slice = 0;
+  auto keep = [&] {
+    if (r < M) *(f32x4*)&kept[((wave * slices + slice) * rows + r) * 16 + 4 * q] = acc[0][0][0];
+    acc[0][0][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    ++slice;
+  };
+  for (int n = 0; n < total; n += kD)
+    each<kD>([&](auto d) {
+      if (n + decltype(d)::value >= total) return;  // uniform: a wave's stages are its own
+      step(d, s);
+      s += kWaves;
+      if (s < stages) return;
+      s = wave;
+      if constexpr (kFresh) keep();
+    });
+  if constexpr (kFresh)
+    while (slice < slices) keep();  // a wave without stages: zeros
+
+  wait_vm<0>();  // the copies past the last stage land before the LDS is given up or holds sums
   __syncthreads();
-  float* const sums = (float*)ring0;  // two tiles an object
+  const float* sums = kept;  // of wave 0; the others' `pitch` further each
+  int pitch = slices * rows * 16;
+  if constexpr (!kFresh) {  // two tiles an object
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    float* const at = i < 2 ? sums : (float*)ring1;
-    *(f32x4*)&at[(wave * 2 + (i & 1)) * 256 + r * 16 + 4 * q] = acc[0][i][0];
-  }
-  __syncthreads();
-  if constexpr (kPaired) {
-    for (int i = threadIdx.x; i < 128; i += kThreads) {
-      const int m = i >> 3, j = i & 7;
-      if (m >= M) break;
-      float g = 0.f, u = 0.f;
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) {
-        g += sums[k * 512 + m * 16 + j];
-        u += sums[k * 512 + m * 16 + 8 + j];
-      }
-      ((float*)p.out)[(first + m) * N + n0 + j] = g * sigmoid(g) * u;
+    for (int i = 0; i < MT; ++i) {
+      float* const at = i < 2 ? (float*)ring0 : (float*)ring1;
+      *(f32x4*)&at[(wave * 2 + (i & 1)) * 256 + r * 16 + 4 * q] = acc[0][i][0];
     }
-  } else {
-    for (int i = threadIdx.x; i < 256 * MT; i += kThreads) {
-      const int m = i >> 4, n = n0 + (i & 15), tile = i >> 8;
-      if (m >= M) break;
-      if (n >= N) continue;
-      const float* const at = (tile < 2 ? sums : (const float*)ring1) + (tile & 1) * 256 + (i & 255);
-      float v = 0.f;
+    __syncthreads();
+    sums = (const float*)ring0;
+    pitch = 512;
+  }
+  const int count = (kFresh ? slices * M : M) * kStep;
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    const int j = i % kStep, m = i / kStep % M, sl = i / (kStep * M);
+    const int n = n0 + sl * kStep + j;
+    if (n >= N) continue;
+    const float* at = sums + (sl * rows + m) * 16 + j;
+    if constexpr (!kFresh && MT == 4)
+      if (m >= 32) at = (const float*)ring1 + (m - 32) * 16 + j;
+    float v = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k) v += at[k * 512];
-      if constexpr (EPI == kPairs)
-        ((float*)p.out)[(int64_t)p.sorted[first + m] * N + n] = v;
-      else if constexpr (EPI == kStoreF32)
-        ((float*)p.out)[(int64_t)m * N + n] = v;
-      else
-        ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
+    for (int k = 0; k < kWaves; ++k) v += at[k * pitch];
+    if constexpr (kPaired) {
+      float u = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) u += at[k * pitch + 8];
+      ((float*)p.out)[(first + m) * N + n] = v * sigmoid(v) * u;
+    } else if constexpr (EPI == kPairs) {
+      ((float*)p.out)[(int64_t)p.sorted[first + m] * N + n] = v;
+    } else if constexpr (EPI == kStoreF32) {
+      ((float*)p.out)[(int64_t)m * N + n] = v;
+    } else {
+      ((uint16_t*)p.out)[(int64_t)m * N + n] = (uint16_t)pack2(v, 0.f);
     }
   }
 #endif
@@ -269,12 +295,21 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
 
 template <Source SRC, Epilogue EPI, int MT>
 hipError_t launch_tiles(const Product& p, int64_t buckets, hipStream_t stream) {
-  const unsigned groups = (p.N + (EPI == kSwiglu ? 7 : 15)) / (EPI == kSwiglu ? 8 : 16);
-  const int64_t rows = EPI == kSwiglu || EPI == kPairs ? kFewRows : p.M;
-  const size_t lds = extra_bytes(SRC != kCodes, rows, p.K);
-  constexpr int kD = EPI == kSwiglu || EPI == kPairs ? 3 : MT == 1 ? 6 : MT == 2 ? 4 : 3;
-  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT, kD>), dim3(groups, (unsigned)buckets), dim3(kThreads),
-                     lds, stream, p);
+  constexpr bool kExperts = EPI == kSwiglu || EPI == kPairs;
+  constexpr int kStep = EPI == kSwiglu ? 8 : 16;
+  constexpr int kD = kExperts ? 3 : MT == 1 ? 6 : MT == 2 ? 4 : 3;
+  const int64_t rows = kExperts ? kFewRows : p.M, all = (p.N + kStep - 1) / kStep;
+  // experts: as many slices as leave two work-groups for every CU, and two on it (N is a
+  // multiple of 128, and a work-group's columns lie in one block)
+  int slices = 1;
+  if (kExperts)
+    while (slices < 8 && all / (2 * slices) * buckets >= 512 &&
+           extra_bytes(true, rows, p.K, 2 * slices) + kD * kWaves * kSlot <= 80 * 1024)
+      slices *= 2;
+  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT, kD>),
+                     dim3((unsigned)((all + slices - 1) / slices), (unsigned)buckets),
+                     dim3(kThreads), extra_bytes(SRC != kCodes, rows, p.K, slices), stream, p,
+                     slices);
   return hipGetLastError();
 }
 template <Source SRC, Epilogue EPI>
@@ -289,8 +324,8 @@ hipError_t launch(const Product& p, hipStream_t stream) {
 }  // namespace
 
 bool rows_fit(Source source, int64_t M, int64_t N, int64_t K) {
-  return M >= 1 && M <= (source == kCodes ? kMostRows : kFewRows) && N < (1 << 26) && N * K <= 0x7fffffff &&
-         extra_bytes(source != kCodes, M, K) <= kMostExtra;
+  return M >= 1 && M <= (source == kCodes ? kMostRows : kFewRows) && N < (1 << 26) &&
+         N * K <= 0x7fffffff && extra_bytes(source != kCodes, M, K, 1) <= kMostExtra;
 }
 
 hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream) {
