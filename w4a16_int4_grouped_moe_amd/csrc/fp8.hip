@@ -39,12 +39,10 @@ __device__ __forceinline__ void store8(void* x, int64_t unit, const float* v) {
 }
 
 // 1 x 128 blocks: 16 lanes a block, a work-group 16 rows of NB blocks, so that the
-// scales of a stage leave 16 at a time. out_units: eights of a row of codes, those past
-// the values zeros.
+// scales of a stage leave 16 at a time.
 template <int TYPE, int NB>
 __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __restrict__ x,
                                                                  int64_t rows, int32_t width,
-                                                                 int32_t out_units,
                                                                  uint8_t* __restrict__ codes,
                                                                  float* __restrict__ scales) {
   const int32_t blocks = (width + kBlock - 1) / kBlock, units = width / 8;
@@ -66,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __r
   for (int i = 0; i < NB; ++i) {
     const int u = (b0 + i) * 16 + at;
     const uint32_t field = scale_field(top_of_16(top8(v[i])));
-    if (u < out_units) ((u32x2*)codes)[row * out_units + u] = codes8(v[i], field);
+    if (u < units) ((u32x2*)codes)[row * units + u] = codes8(v[i], field);
     if (at == 0 && b0 + i < blocks) scales[(int64_t)(b0 + i) * rows + row] = scale_value(field);
   }
 }
@@ -151,71 +149,91 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
 // eight columns meet 64 banks.
 [[maybe_unused]] constexpr int kPitch = 33;
 
-// 128 rows x 64 columns a work-group: a thread four rows of eight columns
-__global__ __launch_bounds__(kThreads) void quantize_transposed_kernel(
-    const void* __restrict__ x, int64_t rows, int32_t width, uint8_t* __restrict__ codes,
-    float* __restrict__ scales) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ uint32_t words[64 * kPitch];
-  __shared__ uint32_t tops[kThreads / 64][64];
-  const int32_t units = width / 8;
-  const int g = threadIdx.x >> 3, c8 = threadIdx.x & 7, u = blockIdx.x * 8 + c8;
-  const int64_t block = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
-  if (block * kBlock >= rows) return;
-  const int64_t row0 = block * kBlock + 4 * g;
-  float v[4][8];
+__device__ __forceinline__ void store_columns(const uint32_t* words, int64_t rows, int32_t width,
+                                              int64_t block, int64_t col0, uint8_t* codes) {
+  const int64_t pitch = blocks_of(rows) * kBlock;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (u < units && row0 + i < rows) {
-      load8<MOE_TYPE_BF16>(x, (row0 + i) * units + u, v[i]);
-    } else {
+    const int c = i * 32 + (threadIdx.x >> 3), w = (threadIdx.x & 7) * 4;
+    const uint32_t* p = words + c * kPitch + w;
+    const u32x4 v = {p[0], p[1], p[2], p[3]};
+    if (col0 + c < width) *(u32x4*)(codes + (col0 + c) * pitch + block * kBlock + 4 * w) = v;
+  }
+}
+
+// A block of 128 rows x 128 columns of x bf16, a thread four rows of 16 columns: quantised along
+// the columns into the transpose (see launch_prepare), and where row_codes is given along the
+// rows too, in rows of 128 blocks_of(width) bytes
+__device__ __forceinline__ void quantize_block(uint32_t* words, uint32_t (*tops)[128],
+                                               const void* x, int64_t rows, int32_t width,
+                                               int64_t block, int64_t column_block,
+                                               uint8_t* row_codes, float* row_scales,
+                                               uint8_t* codes, float* scales) {
+  const int32_t units = width / 8, across = (width + kBlock - 1) / kBlock;
+  const int g = threadIdx.x >> 3, c16 = threadIdx.x & 7;
+  const int64_t u = column_block * 16 + 2 * c16, row0 = block * kBlock + 4 * g;
+  float v[4][16];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (u + h < units && row0 + i < rows) {
+        load8<MOE_TYPE_BF16>(x, (row0 + i) * units + u + h, v[i] + 8 * h);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][8 * h + j] = 0.f;
+      }
+    }
+  if (row_codes) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t top = larger(top8(v[i]), top8(v[i] + 8));
+      top = with_lane<0xB1>(top);   // lane ^ 1
+      top = with_lane<0x4E>(top);   // lane ^ 2
+      top = with_lane<0x141>(top);  // mirrored in eights
+      const uint32_t field = scale_field(top);
+      const u32x2 lo = codes8(v[i], field), hi = codes8(v[i] + 8, field);
+      const int64_t row = row0 + i;
+      if (row < rows) {
+        *(u32x4*)(row_codes + (row * across + column_block) * kBlock + 16 * c16) =
+            u32x4{lo[0], lo[1], hi[0], hi[1]};
+        if (c16 == 0) row_scales[column_block * rows + row] = scale_value(field);
+      }
     }
   }
-  uint32_t top[8];
+  if (!codes) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    top[j] = larger(larger(magnitude(v[0][j]), magnitude(v[1][j])),
-                    larger(magnitude(v[2][j]), magnitude(v[3][j])));
-    top[j] = larger(top[j], __shfl_xor(top[j], 8));
-    top[j] = larger(top[j], __shfl_xor(top[j], 16));
-    top[j] = larger(top[j], __shfl_xor(top[j], 32));
-    if ((threadIdx.x & 63) < 8) tops[threadIdx.x >> 6][c8 * 8 + j] = top[j];
+  for (int j = 0; j < 16; ++j) {
+    uint32_t top = larger(larger(magnitude(v[0][j]), magnitude(v[1][j])),
+                          larger(magnitude(v[2][j]), magnitude(v[3][j])));
+    top = larger(top, __shfl_xor(top, 8));
+    top = larger(top, __shfl_xor(top, 16));
+    top = larger(top, __shfl_xor(top, 32));
+    if ((threadIdx.x & 63) < 8) tops[threadIdx.x >> 6][c16 * 16 + j] = top;
   }
   __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = c8 * 8 + j;
+  for (int j = 0; j < 16; ++j) {
+    const int c = c16 * 16 + j;
     const uint32_t field =
         scale_field(larger(larger(tops[0][c], tops[1][c]), larger(tops[2][c], tops[3][c])));
     const float col[4] = {v[0][j], v[1][j], v[2][j], v[3][j]};
     words[c * kPitch + g] = field == 255 ? 0 : pack4(col, scale_inverse(field));
-    if (g == 0 && u < units) scales[block * width + u * 8 + j] = scale_value(field);
+    if (g == 0 && column_block * kBlock + c < width)
+      scales[block * width + column_block * kBlock + c] = scale_value(field);
   }
   __syncthreads();
-  const int64_t pitch = blocks_of(rows) * kBlock;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = i * 8 + (threadIdx.x >> 5), w = threadIdx.x & 31;
-    const int64_t col = (int64_t)blockIdx.x * 64 + c;
-    if (col < width)
-      *(uint32_t*)(codes + col * pitch + block * kBlock + 4 * w) = words[c * kPitch + w];
-  }
-#endif
+  store_columns(words, rows, width, block, column_block * kBlock, codes);
 }
 
-// 128 rows x 128 columns of codes a work-group: a thread four rows of 16 columns
-__global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __restrict__ codes,
-                                                             int64_t rows, int32_t width,
-                                                             uint8_t* __restrict__ out) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __shared__ uint32_t words[128 * kPitch];
+// 128 rows x 128 columns of codes, transposed: a thread four rows of 16 columns
+__device__ __forceinline__ void transpose_block(uint32_t* words, const uint8_t* codes,
+                                                int64_t rows, int32_t width, int64_t block,
+                                                int64_t column_block, uint8_t* out) {
   const int32_t units = width / 16;
-  const int g = threadIdx.x >> 3, c16 = threadIdx.x & 7, u = blockIdx.x * 8 + c16;
-  const int64_t block = (int64_t)blockIdx.z * gridDim.y + blockIdx.y;
-  if (block * kBlock >= rows) return;
-  const int64_t row0 = block * kBlock + 4 * g;
+  const int g = threadIdx.x >> 3, c16 = threadIdx.x & 7;
+  const int64_t u = column_block * 8 + c16, row0 = block * kBlock + 4 * g;
   u32x4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -235,13 +253,31 @@ __global__ __launch_bounds__(kThreads) void transpose_kernel(const uint8_t* __re
     w[3 * kPitch] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
   }
   __syncthreads();
-  const int64_t pitch = blocks_of(rows) * kBlock;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = i * 8 + (threadIdx.x >> 5), w = threadIdx.x & 31;
-    const int64_t col = (int64_t)blockIdx.x * 128 + c;
-    if (col < width)
-      *(uint32_t*)(out + col * pitch + block * kBlock + 4 * w) = words[c * kPitch + w];
+  store_columns(words, rows, width, block, column_block * kBlock, out);
+}
+#endif
+
+// All that the gradients' products read, in one launch: blocks of 128 x 128 of B's codes, of
+// dout and of a
+__global__ __launch_bounds__(kThreads) void prepare_kernel(const Prepare p, const int64_t first_dout,
+                                                           const int64_t first_a,
+                                                           const int64_t end) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __shared__ uint32_t words[128 * kPitch];
+  __shared__ uint32_t tops[kThreads / 64][128];
+  const int64_t group = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (group >= end) return;
+  const int64_t wide = blocks_of(p.width), high = blocks_of(p.cols);
+  if (group < first_dout) {
+    transpose_block(words, p.b, p.cols, p.width, group / wide, group % wide, p.b_t);
+  } else if (group < first_a) {
+    const int64_t i = group - first_dout;
+    quantize_block(words, tops, p.dout, p.rows, p.cols, i / high, i % high, p.dout_codes,
+                   p.dout_scales, p.dout_t, p.dout_t_scales);
+  } else {
+    const int64_t i = group - first_a;
+    quantize_block(words, tops, p.a, p.rows, p.width, i / wide, i % wide, nullptr, nullptr, p.a_t,
+                   p.a_t_scales);
   }
 #endif
 }
@@ -273,15 +309,15 @@ bool four_blocks(int64_t rows, int32_t width) {
   return (rows + 15) / 16 * ((blocks_of(width) + 3) / 4) >= 512;
 }
 template <int TYPE>
-void quantize_rows(const void* x, int64_t rows, int32_t width, int32_t out_units, uint8_t* codes,
+void quantize_rows(const void* x, int64_t rows, int32_t width, uint8_t* codes,
                    float* scales, hipStream_t stream) {
   const int64_t blocks = blocks_of(width), down = (rows + 15) / 16;
   if (four_blocks(rows, width))
     hipLaunchKernelGGL((quantize_rows_kernel<TYPE, 4>), grid_of((blocks + 3) / 4, down),
-                       dim3(kThreads), 0, stream, x, rows, width, out_units, codes, scales);
+                       dim3(kThreads), 0, stream, x, rows, width, codes, scales);
   else
     hipLaunchKernelGGL((quantize_rows_kernel<TYPE, 1>), grid_of(blocks, down), dim3(kThreads), 0,
-                       stream, x, rows, width, out_units, codes, scales);
+                       stream, x, rows, width, codes, scales);
 }
 
 }  // namespace
@@ -295,16 +331,8 @@ hipError_t launch_quantize(const void* x, int32_t type, int64_t rows, int32_t wi
       hipLaunchKernelGGL((quantize_square_kernel<TYPE>), grid_of(blocks_of(width), blocks_of(rows)),
                          dim3(kThreads), 0, stream, x, rows, width, codes, scales);
     else
-      quantize_rows<TYPE>(x, rows, width, width / 8, codes, scales, stream);
+      quantize_rows<TYPE>(x, rows, width, codes, scales, stream);
   });
-}
-
-hipError_t launch_quantize_padded(const void* x, int64_t rows, int32_t width, uint8_t* codes,
-                                  float* scales, hipStream_t stream) {
-  if (rows == 0) return hipSuccess;
-  quantize_rows<MOE_TYPE_BF16>(x, rows, width, (int32_t)blocks_of(width) * (kBlock / 8), codes,
-                               scales, stream);
-  return hipGetLastError();
 }
 
 hipError_t launch_clear(void* out, int64_t bytes, hipStream_t stream) {
@@ -338,17 +366,14 @@ hipError_t launch_dequantize(const uint8_t* codes, const float* scales, int64_t 
   });
 }
 
-hipError_t launch_quantize_transposed(const void* x, int64_t rows, int32_t width, uint8_t* codes,
-                                      float* scales, hipStream_t stream) {
-  hipLaunchKernelGGL(quantize_transposed_kernel, grid_of((width + 63) / 64, blocks_of(rows)),
-                     dim3(kThreads), 0, stream, x, rows, width, codes, scales);
-  return hipGetLastError();
-}
-
-hipError_t launch_transpose(const uint8_t* codes, int64_t rows, int32_t width, uint8_t* out,
-                            hipStream_t stream) {
-  hipLaunchKernelGGL(transpose_kernel, grid_of(blocks_of(width), blocks_of(rows)), dim3(kThreads),
-                     0, stream, codes, rows, width, out);
+hipError_t launch_prepare(const Prepare& p, hipStream_t stream) {
+  const int64_t down = blocks_of(p.rows);
+  const int64_t first_dout = p.b_t ? blocks_of(p.cols) * blocks_of(p.width) : 0;
+  const int64_t first_a = first_dout + down * blocks_of(p.cols);
+  const int64_t end = first_a + (p.a_t ? down * blocks_of(p.width) : 0);
+  const int64_t y = (end + (1 << 20) - 1) >> 20;
+  hipLaunchKernelGGL(prepare_kernel, dim3((unsigned)((end + y - 1) / y), (unsigned)y),
+                     dim3(kThreads), 0, stream, p, first_dout, first_a, end);
   return hipGetLastError();
 }
 

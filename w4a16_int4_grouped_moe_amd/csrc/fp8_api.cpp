@@ -99,8 +99,7 @@ struct Gradients {
         a_t(width, rows, true),
         weights(region((int64_t)width * kBlock * blocks_of(cols))),
         split(std::max(split_of(rows, width, dout.pitch), split_of(cols, width, dout_t.pitch))) {}
-  size_t of_da() const { return dout.bytes() + weights; }
-  size_t of_db() const { return dout_t.bytes() + a_t.bytes(); }
+  size_t bytes() const { return dout.bytes() + weights + dout_t.bytes() + a_t.bytes() + split; }
 };
 
 // ---- the experts ----
@@ -247,7 +246,7 @@ int moe_fp8_matmul_backward_workspace_size(int64_t rows, int32_t cols, int32_t w
   const int st = check_product(rows, cols, width);
   if (st != MOE_OK) return st;
   const Gradients g(rows, cols, width);
-  *bytes = rows ? g.of_da() + g.of_db() + g.split : 0;
+  *bytes = rows ? g.bytes() : 0;
   return MOE_OK;
 }
 
@@ -270,39 +269,41 @@ int moe_fp8_matmul_backward(const void* dout, const void* a, const uint8_t* b,
     if (db && (st = check_pointers({a}, {})) != MOE_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, need)) != MOE_OK) return st;
   }
+  if (rows == 0) {
+    if (db) e = fp8::launch_clear(db, (int64_t)cols * width * (out_type == MOE_TYPE_BF16 ? 2 : 4), s);
+    return done(e);
+  }
   const Gradients g(rows, cols, width);
-  uint8_t* at = (uint8_t*)workspace;
-  uint8_t* const split = at + g.of_da() + g.of_db();
-  if (da && rows > 0) {
-    uint8_t* weights = at + g.dout.bytes();
-    float* scales = (float*)(at + g.dout.codes);
-    e = fp8::launch_transpose(b, cols, width, weights, s);
-    if (e == hipSuccess) e = fp8::launch_quantize_padded(dout, rows, cols, at, scales, s);
-    Product d{at, weights, scales, b_scales, g.dout.pitch, kBlock * blocks_of(cols),
+  uint8_t* const dout_codes = (uint8_t*)workspace;
+  uint8_t* const b_t = dout_codes + g.dout.bytes();
+  uint8_t* const dout_t = b_t + g.weights;
+  uint8_t* const a_t = dout_t + g.dout_t.bytes();
+  uint8_t* const split = a_t + g.a_t.bytes();
+  fp8::Prepare q{dout, a, b, rows, cols, width};
+  float* const dout_scales = (float*)(dout_codes + g.dout.codes);
+  float* const dout_t_scales = (float*)(dout_t + g.dout_t.codes);
+  float* const a_t_scales = (float*)(a_t + g.a_t.codes);
+  if (da) q.b_t = b_t, q.dout_codes = dout_codes, q.dout_scales = dout_scales;
+  if (db)
+    q.dout_t = dout_t, q.dout_t_scales = dout_t_scales, q.a_t = a_t, q.a_t_scales = a_t_scales;
+  e = fp8::launch_prepare(q, s);
+  if (da && e == hipSuccess) {
+    Product d{dout_codes, b_t, dout_scales, b_scales, g.dout.pitch, kBlock * blocks_of(cols),
               rows, width, g.dout.pitch};
     d.a_rows = rows;
     d.sb_row = 1;
     d.sb_stage = blocks_of(width);
     d.out = da;
-    if (e == hipSuccess) e = fp8::launch_product(fp8::kSquare, store, d, split, s);
-    if (e != hipSuccess) return done(e);
+    e = fp8::launch_product(fp8::kSquare, store, d, split, s);
   }
-  if (db && rows > 0) {
-    at += g.of_da();
-    float* dout_scales = (float*)(at + g.dout_t.codes);
-    uint8_t* a_codes = at + g.dout_t.bytes();
-    float* a_scales = (float*)(a_codes + g.a_t.codes);
-    e = fp8::launch_quantize_transposed(dout, rows, cols, at, dout_scales, s);
-    if (e == hipSuccess) e = fp8::launch_quantize_transposed(a, rows, width, a_codes, a_scales, s);
-    Product d{at, a_codes, dout_scales, a_scales, g.dout_t.pitch, g.a_t.pitch,
+  if (db && e == hipSuccess) {
+    Product d{dout_t, a_t, dout_t_scales, a_t_scales, g.dout_t.pitch, g.a_t.pitch,
               cols, width, g.dout_t.pitch};
     d.a_rows = cols;
     d.sb_row = 1;
     d.sb_stage = width;
     d.out = db;
-    if (e == hipSuccess) e = fp8::launch_product(fp8::kRowScales, store, d, split, s);
-  } else if (db) {
-    e = fp8::launch_clear(db, (int64_t)cols * width * (out_type == MOE_TYPE_BF16 ? 2 : 4), s);
+    e = fp8::launch_product(fp8::kRowScales, store, d, split, s);
   }
   return done(e);
 }

@@ -163,50 +163,63 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[H][FA][FB], const Frags<FB> (&n
   });
 }
 
-// Eight codes as bf16, which holds every e4m3
-__device__ __forceinline__ u32x4 widen(uint32_t lo, uint32_t hi) {
-  return u32x4{
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
-      __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
+// Two codes of a word as bf16, which holds every e4m3
+template <int HALF>
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  return __builtin_bit_cast(uint32_t,
+                            __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HALF != 0));
 }
-// The same with the products summed in fp32 as the matrix units do it for bf16: in quarters of
-// the stage, widened on the way.
+// Word W (two codes) of quarter K (eight codes) of a lane's 32, widened
+template <int K, int W>
+__device__ __forceinline__ uint32_t widen(const u32x4 (&v)[2]) {
+  return widen2<W % 2>(v[K / 2][K % 2 * 2 + W / 2]);
+}
+// Fragments widened to bf16, a quarter of the stage an MFMA operand
+template <int F>
+struct Wide {
+  u32x4 v[F][4];
+  __device__ __forceinline__ void set(const Frags<F>& f) {
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+      each<16>([&](auto x) {
+        constexpr int k = decltype(x)::value / 4, w = decltype(x)::value % 4;
+        v[i][k][w] = widen<k, w>(f.v[i]);
+      });
+  }
+};
+// The same with the products summed in fp32 as the matrix units do it for bf16. A is widened on
+// the way: beside each MFMA go its share of the next quarter's four conversions and one
+// multiply-add of the sub-tiles before.
 template <bool ROWS, int H, int FA, int FB>
-__device__ __forceinline__ void mma_wide(f32x4 (&acc)[H][FA][FB], const Frags<FB> (&n)[H],
+__device__ __forceinline__ void mma_wide(f32x4 (&acc)[H][FA][FB], const Wide<FB> (&n)[H],
                                          const Frags<FA>& m, const float (&sa)[FA],
                                          const ColumnScales<ROWS, FB> (&sb)[H]) {
-  f32x4 t[H][FA][FB];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    u32x4 nw[H][FB], mw[FA];
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-      mw[i] = widen(m.v[i][k / 2][k % 2 * 2], m.v[i][k / 2][k % 2 * 2 + 1]);
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int j = 0; j < FB; ++j)
-        nw[h][j] = widen(n[h].v[j][k / 2][k % 2 * 2], n[h].v[j][k / 2][k % 2 * 2 + 1]);
-#pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int i = 0; i < FA; ++i)
-#pragma unroll
-        for (int j = 0; j < FB; ++j)
-          t[h][i][j] = mfma(nw[h][j], mw[i], k ? t[h][i][j] : f32x4{0.f, 0.f, 0.f, 0.f});
-  }
-#pragma unroll
-  for (int h = 0; h < H; ++h)
-#pragma unroll
-    for (int i = 0; i < FA; ++i)
-#pragma unroll
-      for (int j = 0; j < FB; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[h][i][j][r] = __builtin_fmaf(
-              t[h][i][j][r], sa[i] * sb[h].v[ROWS ? j : 0][ROWS ? r : 0], acc[h][i][j][r]);
+  constexpr int C = H * FB, kAll = FA * 4 * C;  // MFMAs: sub-tile row, quarter, column
+  f32x4 t[2][C];
+  u32x4 now = {}, next = {};
+  each<4>([&](auto w) { now[decltype(w)::value] = widen<0, decltype(w)::value>(m.v[0]); });
+  const auto add = [&](auto row, auto element) {  // one value of a sub-tile row's sums
+    constexpr int i = decltype(row)::value, c = decltype(element)::value / 4;
+    constexpr int r = decltype(element)::value % 4, h = c / FB, j = c % FB;
+    acc[h][i][j][r] = __builtin_fmaf(
+        t[i & 1][c][r], sa[i] * sb[h].v[ROWS ? j : 0][ROWS ? r : 0], acc[h][i][j][r]);
+  };
+  each<kAll>([&](auto index) {
+    constexpr int x = decltype(index)::value, i = x / (4 * C), k = x / C % 4, c = x % C;
+    t[i & 1][c] = mfma(n[c / FB].v[c % FB][k], now, k ? t[i & 1][c] : f32x4{0.f, 0.f, 0.f, 0.f});
+    if constexpr (i * 4 + k + 1 < FA * 4) {
+      constexpr int ni = (i * 4 + k + 1) / 4, nk = (k + 1) % 4;
+      each<4 / C>([&](auto w) {
+        constexpr int word = c * (4 / C) + decltype(w)::value;
+        next[word] = widen<nk, word>(m.v[ni]);
+      });
+    }
+    if constexpr (i > 0)
+      add(std::integral_constant<int, i - 1>{}, std::integral_constant<int, x % (4 * C)>{});
+    if constexpr (c == C - 1) now = next;
+    __builtin_amdgcn_sched_barrier(0);
+  });
+  each<4 * C>([&](auto e) { add(std::integral_constant<int, FA - 1>{}, e); });
 }
 
 // An MFMA has no side effect: this keeps the sums on this side of the barrier that follows

@@ -286,6 +286,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
 
   Frags<FA> fa;
   Frags<FB> fb[2];
+  Wide<FB> wide[2];
   float sa[AH][FA];
   ColumnScales<kRows, FB> cs[2];
 
@@ -301,7 +302,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
 #define FP8_MMA(ah)                                              \
   if (!idle) {                                                   \
     if constexpr (WIDE)                                          \
-      mma_wide<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);   \
+      mma_wide<kRows, 2, FA, FB>(acc[ah], wide, fa, sa[ah], cs); \
     else                                                         \
       mma<kRows, 2, FA, FB>(acc[ah], fb, fa, sa[ah], cs);        \
     hold(acc[ah]);                                               \
@@ -355,6 +356,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
       a[0].copy(two == 0 ? sa0 : two == 1 ? sa1 : sx0, s + 2, wave);
       b0.copy(two == 0 ? sb0 : two == 1 ? sb1 : sx1, s + 2, wave);
       b1.copy(two == 0 ? sc0 : two == 1 ? sc1 : sx2, s + 2, wave);
+      if constexpr (WIDE) wide[0].set(fb[0]), wide[1].set(fb[1]);
       wait_vm<3 * kCopies + 1>();
       FP8_MEM_DONE
       FP8_MMA(0)
@@ -526,10 +528,13 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring<512 / TS>
     for (int i = 0; i < F; ++i)
       sa[i] = *(lds_f32)(at.s[buf] + ((wm * F + i) * 16 + (lane & 15)) * 4);
     cs[0].read(at.s[buf] + 512, wn * (16 * F), lane);
-    if constexpr (WIDE)
-      mma_wide<kRows, 1, F, F>(acc, fb, fa, sa, cs);
-    else
+    if constexpr (WIDE) {
+      Wide<F> wide[1];
+      wide[0].set(fb[0]);
+      mma_wide<kRows, 1, F, F>(acc, wide, fa, sa, cs);
+    } else {
       mma<kRows, 1, F, F>(acc, fb, fa, sa, cs);
+    }
     hold(acc);
     __builtin_amdgcn_sched_barrier(0);
   };

@@ -11,21 +11,30 @@ __host__ __device__ inline int64_t blocks_of(int64_t n) { return (n + kBlock - 1
 // x [rows, width] (type: MOE_TYPE_*) -> codes [rows, width], scales (see moe_fp8.h)
 hipError_t launch_quantize(const void* x, int32_t type, int64_t rows, int32_t width, int32_t block,
                            uint8_t* codes, float* scales, hipStream_t stream);
-// The same in 1 x 128 blocks of x bf16 [rows, width], width a multiple of 8: rows of codes
-// 128 blocks_of(width) bytes apart, zeros behind the values
-hipError_t launch_quantize_padded(const void* x, int64_t rows, int32_t width, uint8_t* codes,
-                                  float* scales, hipStream_t stream);
 hipError_t launch_clear(void* out, int64_t bytes, hipStream_t stream);  // a multiple of 16
 hipError_t launch_dequantize(const uint8_t* codes, const float* scales, int64_t rows,
                              int32_t width, int32_t block, int32_t type, void* out,
                              hipStream_t stream);
-// x bf16 [rows, width] -> its transpose in 1 x 128 blocks along the rows: codes [width, pitch],
-// pitch = 128 blocks_of(rows), zeros behind the rows; scales [blocks_of(rows), width]
-hipError_t launch_quantize_transposed(const void* x, int64_t rows, int32_t width, uint8_t* codes,
-                                      float* scales, hipStream_t stream);
-// codes [rows, width] -> [width, pitch], as above
-hipError_t launch_transpose(const uint8_t* codes, int64_t rows, int32_t width, uint8_t* out,
-                            hipStream_t stream);
+// What the gradients' products read: B's codes [cols, width] transposed (b_t), dout bf16 [rows,
+// cols] in 1 x 128 blocks (dout_codes) and its transpose in such blocks (dout_t), and a's
+// transpose (a bf16 [rows, width]). Rows of codes are 128 blocks_of(their width) bytes, zeros
+// behind the values; scales as moe_fp8.h has them. What is NULL is not computed (dout_codes or
+// dout_t is given).
+struct Prepare {
+  const void* dout;
+  const void* a;
+  const uint8_t* b;
+  int64_t rows;
+  int32_t cols, width;
+  uint8_t* b_t;
+  uint8_t* dout_codes;
+  float* dout_scales;
+  uint8_t* dout_t;
+  float* dout_t_scales;
+  uint8_t* a_t;
+  float* a_t_scales;
+};
+hipError_t launch_prepare(const Prepare& p, hipStream_t stream);
 
 // D[m, n] = sum over the stages (128 bytes of a row) of sa(m, stage) sb(n, stage) times the
 // stage's sum of A(m, k) B(n, k).

@@ -224,10 +224,13 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
         sa[i] = as[(16 * i + r < M ? 16 * i + r : 0) * stages + s];
       }
     }
-    if constexpr (kWide)
-      mma_wide<false, 1, MT, 1>(acc, w, m, sa, cs);
-    else
+    if constexpr (kWide) {
+      Wide<1> wide[1];
+      wide[0].set(w[0]);
+      mma_wide<false, 1, MT, 1>(acc, wide, m, sa, cs);
+    } else {
       mma<false, 1, MT, 1>(acc, w, m, sa, cs);
+    }
     hold(acc);
     wait_lgkm0();  // the place is read before the next copy into it goes out
     load(slot);
