@@ -308,6 +308,18 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
     hold(acc[ah]);                                               \
   }
 
+  // B's square scales of the next stage, asked for ahead of a phase's MFMAs: its scalar loads
+  // (each stage's from another line) would hold up the wait for the fragments
+  float sq_next0 = 0.f, sq_next1 = 0.f;
+  const auto ask = [&](int s) {
+    if constexpr (!kRows) {
+      const int64_t at = (s < stages ? s : stages - 1) * p.sb_stage;
+      sq_next0 = sq0[at];
+      sq_next1 = sq1[at];
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  ask(0);
   // stage s in buffer `buf`; its scales are read in its first phase, so that their place is
   // free for stage s + 2 in the second
   auto step = [&](int s, auto buffer) {
@@ -317,10 +329,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
     const lds_bytes b0_now = buf == 0 ? sb0 : buf == 1 ? sb1 : sx1;
     const lds_bytes b1_now = buf == 0 ? sc0 : buf == 1 ? sc1 : sx2;
     const lds_bytes ss_now = buf == 0 ? ss0 : buf == 1 ? ss1 : ss2;
-    if constexpr (!kRows) {
-      cs[0].set(sq0[s * p.sb_stage]);
-      cs[1].set(sq1[s * p.sb_stage]);
-    }
+    if constexpr (!kRows) cs[0].set(sq_next0), cs[1].set(sq_next1);
     if (!idle) {
       fa.read(a_now, wm * 64, lane);
       fb[0].read(b0_now, wn * 32, lane);
@@ -348,6 +357,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
       b1.copy(b1_now, s + 2, wave);
       wait_vm<4 * kCopies + 1>();
       FP8_MEM_DONE
+      ask(s + 1);
       FP8_MMA(AH - 1)
       FP8_MMA_DONE
     } else {
@@ -359,6 +369,7 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
       if constexpr (WIDE) wide[0].set(fb[0]), wide[1].set(fb[1]);
       wait_vm<3 * kCopies + 1>();
       FP8_MEM_DONE
+      ask(s + 1);
       FP8_MMA(0)
       FP8_MMA_DONE
     }
@@ -503,6 +514,7 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring<512 / TS>
 #pragma unroll
     for (int j = 0; j < F; ++j) acc[0][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  float sq_next = kRows ? 0.f : sq[first * p.sb_stage];
   constexpr int kCopies = 2 * Operand<TS, NW>::kPer + 1;  // a stage's, per wave
   auto copy = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
@@ -513,12 +525,14 @@ __device__ __forceinline__ void tile_body(const Product& p, const Ring<512 / TS>
   auto step = [&](int s, auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     ColumnScales<kRows, F> cs[1];
-    if constexpr (!kRows) cs[0].set(sq[s * p.sb_stage]);
+    if constexpr (!kRows) cs[0].set(sq_next);
     wait_vm<(D - 2) * kCopies>();  // stage s has landed; the reads of stage s - 1 are over
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     copy(s + D - 1, std::integral_constant<int, (buf + D - 1) % D>{});
+    if constexpr (!kRows)  // the next stage's, on its way during this one
+      sq_next = sq[(s + 1 < stages ? s + 1 : s) * p.sb_stage];
     __builtin_amdgcn_sched_barrier(0);
     Frags<F> fa, fb[1];
     float sa[F];
