@@ -1,6 +1,6 @@
 // balance.hip -- the router's balance loss, its counts and its gradient (gfx950).
 //
-// A wave takes a token at a time, lane l the experts l, l + 64, ...: softmax with
+// A wave takes tokens one after the other, lane l the experts l, l + 64, ...: softmax with
 // its maximum and sum over the wave, p added up in registers. A work-group's waves
 // add theirs in fp64 into a piece (one for each sequence that its tokens are in);
 // its ids are counted in LDS, by integer atomics, whose order changes nothing. A
@@ -54,14 +54,41 @@ __device__ __forceinline__ float wave_reduce(float v, float none, Op op) {
                             __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+// Row t of a matrix of S values as a resource (t the same for the wave): accesses past it read
+// zero and write nothing, so that the kernels need no branches
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_of(const void* matrix, int64_t t, int S) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)matrix + t * S), 0,
+                                           S * (int)sizeof(T), 0x00020000);
+}
 // The scores of token t in a lane's registers; experts past S: -inf
 template <int NI, typename T>
-__device__ __forceinline__ void load_scores(const T* __restrict__ scores, int64_t t, int S,
-                                            int lane, float (&v)[NI]) {
-  const T* row = scores + t * S;
+__device__ __forceinline__ void load_scores(const void* scores, int64_t t, int S, int lane,
+                                            float (&v)[NI]) {
+  const __amdgpu_buffer_rsrc_t row = row_of<T>(scores, t, S);
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-    v[i] = lane + 64 * i < S ? (float)row[lane + 64 * i] : -__builtin_inff();
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 64 * i;
+    float x;
+    if constexpr (sizeof(T) == 4)
+      x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(row, 4 * e, 0, 0));
+    else
+      x = (float)__builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(row, 2 * e, 0, 0));
+    v[i] = e < S ? x : -__builtin_inff();
+  }
+}
+template <int NI, typename T>
+__device__ __forceinline__ void store_scores(void* scores, int64_t t, int S, int lane,
+                                             const float (&v)[NI]) {
+  const __amdgpu_buffer_rsrc_t row = row_of<T>(scores, t, S);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = lane + 64 * i;
+    if constexpr (sizeof(T) == 4)
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[i]), row, 4 * e, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)v[i]), row, 2 * e, 0, 0);
+  }
 }
 
 // v: scores -> softmax. All of them -inf: zeros; +inf and NaN: NaN.
@@ -84,17 +111,20 @@ __device__ __forceinline__ void softmax(float (&v)[NI]) {
   for (int i = 0; i < NI; ++i) v[i] *= inv;
 }
 
-// The sequence that holds token t: the last b with offsets[b] <= t (-1: none)
-__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ offsets, int B, int64_t t) {
-  int lo = 0, hi = B + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (offsets[mid] <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+// The sequence that holds token t: the last b with offsets[b] <= t (-1: none). The whole wave
+// looks at 64 offsets at a time: one trip to memory for up to 63 sequences.
+__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ offsets, int B, int64_t t,
+                                           int lane) {
+  int first = 0, n = B + 1;
+  for (;;) {
+    const int step = (n + 63) / 64;
+    const int at = lane * step;
+    const int c = __popcll(__ballot(at < n && offsets[first + (at < n ? at : 0)] <= t));
+    if (c == 0) return first - 1;
+    first += (c - 1) * step;
+    n = n - (c - 1) * step < step ? n - (c - 1) * step : step;
+    if (step == 1) return first;
   }
-  return lo - 1;
 }
 
 struct Forward {
@@ -121,14 +151,14 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(const Forward f) {
   __shared__ float sums[kWaves][64 * NI];
   __shared__ int32_t hist[64 * NI + 1];
   __shared__ double all[ALONE ? 64 * NI : 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t first = (int64_t)blockIdx.x * f.per;
   const int64_t last = first + f.per < f.T ? first + f.per : f.T;
   const int S = f.S;
   int b0 = 0, b1 = 0;
   if (f.offsets) {
-    b0 = sequence_of(f.offsets, f.B, first);
-    b1 = sequence_of(f.offsets, f.B, last - 1);
+    b0 = sequence_of(f.offsets, f.B, first, lane);
+    b1 = sequence_of(f.offsets, f.B, last - 1, lane);
     if (b0 < 0) b0 = 0;
     if (b1 >= f.B) b1 = f.B - 1;
   }
@@ -147,7 +177,7 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(const Forward f) {
     for (int64_t t = lo + wave; t < hi; t += kWaves) {
       if (f.mask && !f.mask[t]) continue;
       float v[NI];
-      load_scores(((const T*)f.scores), t, S, lane, v);
+      load_scores<NI, T>(f.scores, t, S, lane, v);
       for (int j = lane; j < f.k; j += 64) {
         const int32_t e = f.ids[t * f.k + j];
         if ((uint32_t)e < (uint32_t)S) atomicAdd(&hist[e], 1);
@@ -209,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void sequences_kernel(const Forward f) {
   __shared__ double sums[kWaves][64];
   __shared__ int32_t counts[kWaves][64];
   __shared__ int32_t number[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x, S = f.S, e = blockIdx.y * 64 + lane;
   int64_t lo = 0, hi = f.T;
   if (f.offsets) {
@@ -245,7 +275,7 @@ __global__ __launch_bounds__(kThreads) void sequences_kernel(const Forward f) {
 __global__ __launch_bounds__(kThreads) void loss_kernel(const Forward f) {
   __shared__ double sums[kWaves];
   __shared__ int32_t live[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double s = 0;
   int32_t n = 0;
   for (int64_t i = threadIdx.x; i < (int64_t)f.B * f.columns; i += kThreads) s += f.parts[i];
@@ -276,7 +306,7 @@ template <int TYPE, int NI>
 __global__ __launch_bounds__(64 * kBackWaves) void gradient_kernel(const Backward f) {
   typedef typename Score<TYPE>::type T;
   __shared__ int32_t live[kBackWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int S = f.S;
   int n = 0;
   for (int b = threadIdx.x; b < f.B; b += 64 * kBackWaves) n += f.tokens[b] > 0;
@@ -292,19 +322,20 @@ __global__ __launch_bounds__(64 * kBackWaves) void gradient_kernel(const Backwar
   int64_t end = -1;          // where the sequence at `at` ends
   float c[NI], factor = 0.f;
   for (int64_t t = first + wave; t < last; t += kBackWaves) {
-    T* out = (T*)f.dscores + t * S;
+    float v[NI];
+    load_scores<NI, T>(f.scores, t, S, lane, v);  // also of tokens that take no part
     if (t >= end) {
       at = 0, end = f.T;
       if (f.offsets) {
-        at = sequence_of(f.offsets, f.B, t);
+        at = sequence_of(f.offsets, f.B, t, lane);
         if (at >= f.B) at = -1;
         end = at < 0 ? t + 1 : f.offsets[at + 1];
       }
     }
     if (at < 0 || (f.mask && !f.mask[t])) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (lane + 64 * i < S) out[lane + 64 * i] = (T)0.f;
+      for (int i = 0; i < NI; ++i) v[i] = 0.f;
+      store_scores<NI, T>(f.dscores, t, S, lane, v);
       continue;
     }
     if (at != loaded) {
@@ -316,16 +347,14 @@ __global__ __launch_bounds__(64 * kBackWaves) void gradient_kernel(const Backwar
       factor = (float)(scale / ((double)tokens * tokens));
       loaded = at;
     }
-    float v[NI];
-    load_scores(((const T*)f.scores), t, S, lane, v);
     softmax(v);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) dot += v[i] * c[i];
     dot = wave_reduce(dot, 0.f, [](float a, float b) { return a + b; });
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (lane + 64 * i < S) out[lane + 64 * i] = (T)(factor * v[i] * (c[i] - dot));
+    for (int i = 0; i < NI; ++i) v[i] *= factor * (c[i] - dot);
+    store_scores<NI, T>(f.dscores, t, S, lane, v);
   }
 }
 
