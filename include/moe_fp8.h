@@ -32,7 +32,8 @@
  * call gives the same bits.
  *
  * Limits: width at most 2^20 and a multiple of 16; cols a multiple of 8; rows
- * and cols at most 2^31 - 256. Types are moe_ffn.h's MOE_TYPE_*.
+ * and cols at most 2^31 - 256, 2^20 where the gradients sum over them. Types are
+ * moe_ffn.h's MOE_TYPE_*.
  */
 #ifndef MOE_FP8_H
 #define MOE_FP8_H
@@ -104,7 +105,7 @@ typedef struct {
   int32_t top_k;       /* 1 .. MOE_MAX_TOP_K */
 } moe_fp8_experts_problem;
 
-/* Bytes of workspace of moe_fp8_experts_forward (host only). */
+/* Bytes of workspace of moe_fp8_experts_forward (host only). T * H at most 2^31 - 1. */
 int moe_fp8_experts_workspace_size(const moe_fp8_experts_problem *p, size_t *bytes);
 
 /*

@@ -416,9 +416,10 @@ hipError_t launch_backward(const Sizes& z, const float* dloss, const void* score
                            const int32_t* counts, const int32_t* tokens, const uint8_t* mask,
                            const int32_t* offsets, void* dscores, hipStream_t stream) {
   if (z.T == 0) return hipSuccess;
-  // one token a wave until 2048 work-groups, then up to 16
-  const int64_t per = std::min<int64_t>(
-      16, (z.T + 2048 * kBackWaves - 1) / (2048 * kBackWaves)) * kBackWaves;
+  // one token a wave until 2048 work-groups, then up to 16, then 2^22 work-groups
+  const int64_t fair = (z.T + 2048 * kBackWaves - 1) / (2048 * kBackWaves);
+  const int64_t least = (z.T + ((int64_t)kBackWaves << 22) - 1) / ((int64_t)kBackWaves << 22);
+  const int64_t per = std::max(std::min<int64_t>(16, fair), least) * kBackWaves;
   const Backward f{dloss, scores, counts, tokens, mask, offsets, dscores, z.T, per, z.S, z.k, z.B};
   const unsigned n = (unsigned)((z.T + per - 1) / per);
   with_type(z.type, [&](auto type) {

@@ -30,6 +30,12 @@ int check_product(int64_t rows, int32_t cols, int32_t width) {
   if (st != MOE_OK) return st;
   return cols <= 0 || cols > kMaxRows || cols % 8 ? MOE_ERR_SHAPE : MOE_OK;
 }
+// The gradients also sum over rows and over cols
+int check_gradients(int64_t rows, int32_t cols, int32_t width) {
+  const int st = check_product(rows, cols, width);
+  if (st != MOE_OK) return st;
+  return rows > kMaxWidth || cols > kMaxWidth ? MOE_ERR_SHAPE : MOE_OK;
+}
 int check_type(int32_t type) {
   return type < MOE_TYPE_BF16 || type > MOE_TYPE_FP32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
@@ -69,23 +75,25 @@ struct Quantized {
   size_t bytes() const { return codes + scales; }
 };
 
-// Which kernel a product takes: few rows, quantised on the way where they are bf16, or by a
-// launch ahead; or tiles
+// Which kernel a product takes: few rows, quantised on the way where they are bf16 and four at
+// most, or by a launch ahead (kAhead microseconds); or tiles
+constexpr double kAhead = 3.0;
 enum Path { kFew, kFewPrepared, kTiled };
-Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize, bool square) {
-  if (!square) return kTiled;
-  if (fp8::rows_fit(quantize ? fp8::kBf16 : fp8::kCodes, rows, cols, width) && rows <= 16)
-    return kFew;
-  if (!fp8::rows_fit(fp8::kCodes, rows, cols, width)) return kTiled;
-  return fp8::rows_time(rows, cols, width) < fp8::cut_of(false, rows, cols, width).time
-             ? quantize ? kFewPrepared : kFew
-             : kTiled;
+Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize, bool square, bool wide) {
+  if (!square || !fp8::rows_fit(fp8::kCodes, rows, cols, width)) return kTiled;
+  const double few = fp8::rows_time(rows, cols, width);
+  const double tiled = fp8::cut_of(wide, false, rows, cols, width).time;
+  if (quantize && fp8::rows_fit(fp8::kBf16, rows, cols, width))
+    return few < tiled + kAhead ? kFew : kTiled;
+  return few >= tiled ? kTiled : quantize ? kFewPrepared : kFew;
 }
 
-// The shares' sums of a product, of either type of result
+// The shares' sums of a product, of either type of result and either kind of B
 size_t split_of(int64_t rows, int32_t cols, int64_t width) {
-  return region(std::max(fp8::product_workspace(false, rows, cols, width),
-                         fp8::product_workspace(true, rows, cols, width)));
+  size_t most = 0;
+  for (int kind = 0; kind < 4; ++kind)
+    most = std::max(most, fp8::product_workspace(kind & 1, kind & 2, rows, cols, width));
+  return region(most);
 }
 
 // ---- the gradients' workspace ----
@@ -214,7 +222,7 @@ int moe_fp8_matmul(const void* a, const float* a_scales, const uint8_t* b, const
   hipStream_t s = (hipStream_t)stream;
   uint8_t* split = (uint8_t*)workspace;
   const bool square = b_block == MOE_FP8_SQUARE_BLOCKS, quantize = !a_scales;
-  const Path path = path_of(rows, cols, width, quantize, square);
+  const Path path = path_of(rows, cols, width, quantize, square, out_type != MOE_TYPE_BF16);
   if (quantize && path != kFew) {
     const Quantized q(rows, width);
     uint8_t* codes = split;
@@ -243,7 +251,7 @@ int moe_fp8_matmul(const void* a, const float* a_scales, const uint8_t* b, const
 int moe_fp8_matmul_backward_workspace_size(int64_t rows, int32_t cols, int32_t width,
                                            size_t* bytes) {
   if (!bytes) return MOE_ERR_NULL;
-  const int st = check_product(rows, cols, width);
+  const int st = check_gradients(rows, cols, width);
   if (st != MOE_OK) return st;
   const Gradients g(rows, cols, width);
   *bytes = rows ? g.bytes() : 0;

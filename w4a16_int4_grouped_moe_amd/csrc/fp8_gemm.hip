@@ -652,7 +652,7 @@ hipError_t launch_small(Product p, const Cut& c, void* split, hipStream_t stream
 
 template <Mode MODE, Epilogue EPI>
 hipError_t launch(const Product& p, void* split, hipStream_t stream) {
-  const Cut c = cut_of(EPI == kStoreF32, p.M, p.N, p.K);
+  const Cut c = cut_of(EPI == kStoreF32, MODE == kRowScales, p.M, p.N, p.K);
   if constexpr (EPI == kStoreBf16)
     if (c.tile == 2) return launch_big<2, MODE, EPI>(p, stream);
   if (c.tile == 1) return launch_big<1, MODE, EPI, EPI == kStoreF32>(p, stream);

@@ -76,16 +76,16 @@ struct Product {
 };
 // How a product is cut (fp8_plan.cpp): the tile (0: 128 x 128, 1: 128 x 256, 2: 256 x 256, 3: 64
 // x 64), its work-groups, and for tiles 0 and 3 the shares of K, `share` stages each. wide: fp32
-// results, which tile 2 has no registers for.
+// results, which tile 2 has no registers for; rows: B in 1 x 128 blocks.
 struct Cut {
   int tile = 0, shares = 1, share = 1;
   int64_t groups = 0;
   double time = 0;  // estimate, microseconds
 };
-Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K);
+Cut cut_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K);
 double rows_time(int64_t M, int64_t N, int64_t K);  // of the few-row kernel on codes
 // Bytes of the shares' sums (`split`, 16-byte aligned)
-size_t product_workspace(bool wide, int64_t M, int32_t N, int64_t K);
+size_t product_workspace(bool wide, bool rows, int64_t M, int32_t N, int64_t K);
 hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* split,
                           hipStream_t stream);
 // The same for a few rows of A (fp8_rows.hip): codes, or bf16 (experts' h: fp32) rows that are

@@ -6,22 +6,25 @@ namespace fp8 {
 namespace {
 
 // Microseconds a stage of K takes one round of work-groups on 256 CUs, and what a
-// work-group costs besides; by tile (see Cut), narrow and wide.
+// work-group costs besides, its launch among it; by tile (see Cut). Measured on one
+// round of each tile at K of 1024 and 4096: [wide][B in 1 x 128 blocks].
 struct Rate {
   double stage[4], fixed[4];
 };
-constexpr Rate kRates[2] = {{{0.62, 0.88, 1.42, 0.32}, {4.5, 4.5, 7.0, 4.5}},
-                            {{0.90, 1.60, 9.00, 0.40}, {4.5, 5.0, 7.0, 4.5}}};
+constexpr Rate kRates[2][2] = {{{{0.78, 0.89, 1.53, 0.32}, {6.4, 8.6, 13.9, 5.3}},
+                                {{0.91, 1.19, 2.28, 0.31}, {5.7, 7.5, 12.5, 5.4}}},
+                               {{{1.20, 1.66, 9.00, 0.49}, {7.4, 10.7, 20.0, 4.6}},
+                                {{1.27, 1.84, 9.00, 0.49}, {8.2, 10.2, 20.0, 4.4}}}};
 
 }  // namespace
 
 // The cheapest cut. Shares of K cost a launch and the sums' way to memory and
 // back (about 4 TB/s); of equals the larger tile.
-Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K) {
-  const Rate& rate = kRates[wide];
+Cut cut_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K) {
+  const Rate& rate = kRates[wide][rows];
   const int64_t stages = blocks_of(K);
-  const auto tiles = [&](int64_t rows, int64_t cols) {
-    return ((M + rows - 1) / rows) * ((N + cols - 1) / cols);
+  const auto tiles = [&](int64_t high, int64_t across) {
+    return ((M + high - 1) / high) * ((N + across - 1) / across);
   };
   const auto time = [&](int tile, int64_t groups, int64_t st) {
     return (double)((groups + 255) / 256) * (st * rate.stage[tile] + rate.fixed[tile]);
@@ -41,20 +44,18 @@ Cut cut_of(bool wide, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-// Microseconds: a launch and a work-group's start and end, then what a CU spends on its
-// work-groups' loads (a 16 x 64-byte load of A holds its address path 64 cycles, a line of B
-// 18 for 8 rows), or the weights' way from memory.
+// Microseconds of the few-row kernel on codes: rounds of work-groups on 256 CUs, each a launch's
+// or a work-group's start and end and its stages. Measured at 4096 x 7168 and 7168 x 2048 with
+// 16 rows (11.6 and 13.5), 32 (15.0 and 15.0) and 64.
 double rows_time(int64_t M, int64_t N, int64_t K) {
   const int64_t groups = (N + 15) / 16;
-  const int tiles = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  const double busy = (double)((groups + 255) / 256) * blocks_of(K) * (36 + 128 * tiles) / 2400;
-  const double memory = (double)N * K / 4.5e6;
-  return 5.0 + (busy > memory ? busy : memory);
+  const double stage = M <= 16 ? 0.118 : M <= 32 ? 0.179 : 0.30;
+  return (double)((groups + 255) / 256) * (5.0 + stage * blocks_of(K));
 }
 
-size_t product_workspace(bool wide, int64_t M, int32_t N, int64_t K) {
+size_t product_workspace(bool wide, bool rows, int64_t M, int32_t N, int64_t K) {
   if (M == 0) return 0;
-  const Cut c = cut_of(wide, M, N, K);
+  const Cut c = cut_of(wide, rows, M, N, K);
   return c.shares > 1 ? (size_t)c.shares * M * N * 4 : 0;
 }
 
