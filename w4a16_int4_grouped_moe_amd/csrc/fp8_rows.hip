@@ -47,7 +47,8 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
                                                                               const int slices) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu, kExperts = EPI == kSwiglu || EPI == kPairs;
-  constexpr bool kWide = EPI == kStoreF32, kFresh = SRC != kCodes;
+  // the matrix units wait for memory anyway: one tile sums in fp32 (see fp8_gemm.hip)
+  constexpr bool kWide = EPI == kStoreF32 || MT == 1, kFresh = SRC != kCodes;
   // an object a stage: the compiler then sees which copies a read has to wait for
   __shared__ __attribute__((aligned(1024))) uint8_t ring0[kWaves * kSlot], ring1[kWaves * kSlot];
   __shared__ __attribute__((aligned(1024))) uint8_t ring2[kWaves * kSlot];
