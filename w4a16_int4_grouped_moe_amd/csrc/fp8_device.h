@@ -94,6 +94,7 @@ __device__ __forceinline__ u32x2 codes8(const float* v, uint32_t field) {
 }
 
 typedef __attribute__((address_space(3))) float* lds_f32;
+typedef __attribute__((address_space(3))) int32_t* lds_i32;
 typedef const __attribute__((address_space(4))) float* const_f32;
 
 // A wave's fragments of F sub-tiles of 16 rows from `first`

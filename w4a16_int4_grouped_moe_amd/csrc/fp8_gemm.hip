@@ -72,9 +72,14 @@ struct Operand {
     }
   }
   __device__ __forceinline__ void copy(lds_bytes slot, int stage, int wave) const {
+    copy(slot, stage, wave, 0, records);
+  }
+  // the same `shift` bytes further, of `bytes` that may be read
+  __device__ __forceinline__ void copy(lds_bytes slot, int stage, int wave, int64_t shift,
+                                       int32_t bytes) const {
     const lds_bytes dst = slot + wave * (kPer * 1024);
     const __amdgpu_buffer_rsrc_t res =
-        __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, records, kBufferFlags);
+        __builtin_amdgcn_make_buffer_rsrc((void*)(base + shift), 0, bytes, kBufferFlags);
     const int k0 = stage * kRow, left = end - k0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -171,9 +176,6 @@ __device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int6
         if constexpr (EPI == kStoreBf16) {
           *(u32x2*)((uint16_t*)p.out + m * N + n) =
               u32x2{pack2(v[k][0], v[k][1]), pack2(v[k][2], v[k][3])};
-        } else if constexpr (EPI == kPairs) {
-          const int64_t pair = p.sorted[m];
-          if ((uint64_t)pair < (uint64_t)p.pairs) *(f32x4*)((float*)p.out + pair * N + n) = v[k];
         } else {
           *(f32x4*)((float*)p.out + m * N + n) = v[k];
         }
@@ -183,19 +185,6 @@ __device__ __forceinline__ void store_rows(const Product& p, lds_bytes lds, int6
 }
 #endif
 
-// Tile of (AH x 128) x (2 x 128), eight waves (2 x 4), each 64 rows of every A
-// half x 32 columns of both B halves (kSwiglu: gate and up). A phase is one A half
-// against both B halves, 16 MFMAs a wave of 32 cycles each. The two waves of a SIMD run half a phase
-// apart: one reads fragments and issues copies while the other's MFMAs and
-// multiply-adds run, with a barrier after each of the two parts. A half tile is
-// copied into its own place as soon as the phase that read it is over.
-//
-//   AH  buffers  phase  reads      copies                 waits for (at its end)
-//   2   2        0      A0 B0 B1   A1 of stage s + 1      A1 of s
-//                1      A1         A0 B0 B1 of s + 2      A0 B0 B1 of s + 1
-//   1   3        0      A0 B0 B1   all of s + 2           all of s + 1
-//
-// The scales travel with A0: they are read in the first phase.
 // An object a half tile and a stage's scales: the compiler then sees which copies a read has to
 // wait for. x: AH = 2: the second A halves of the two buffers; AH = 1: the third buffer.
 struct BigLds {
@@ -214,10 +203,27 @@ struct BigLds {
 constexpr int kHalf = 128 * kRow;
 
 #if defined(__HIP_DEVICE_COMPILE__)
-// The tile at row tile tm_id, column tile tn_id; idle: this wave's rows are all padding
+// Tile of (AH x 128) x (2 x 128), eight waves (2 x 4), each 64 rows of every A
+// half x 32 columns of both B halves (kSwiglu: gate and up). A phase is one A half
+// against both B halves, 16 MFMAs a wave of 32 cycles each. The two waves of a SIMD run half a phase
+// apart: one reads fragments and issues copies while the other's MFMAs and
+// multiply-adds run, with a barrier after each of the two parts. A half tile is
+// copied into its own place as soon as the phase that read it is over.
+//
+//   AH  buffers  phase  reads      copies                 waits for (at its end)
+//   2   2        0      A0 B0 B1   A1 of stage s + 1      A1 of s
+//                1      A1         A0 B0 B1 of s + 2      A0 B0 B1 of s + 1
+//   1   3        0      A0 B0 B1   all of s + 2           all of s + 1
+//
+// The scales travel with A0: they are read in the first phase.
+//
+// idle: this wave's rows are all padding. kPairs: `tiles` column tiles one after the other, the
+// copies of the next under way while one is stored, straight from the registers to the pairs'
+// rows (`rows`: the pairs of the block's rows).
 template <int AH, Mode MODE, Epilogue EPI, bool WIDE>
 __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m0, int64_t n0,
-                                         bool idle) {
+                                         bool idle, int tiles, lds_i32 rows) {
+  constexpr bool kSpan = EPI == kPairs;
   constexpr int NW = 8, HR = 128, FA = 4, FB = 2;
   constexpr bool kPaired = EPI == kSwiglu, kRows = MODE == kRowScales;
   typedef Operand<HR, NW> Half;
@@ -268,16 +274,42 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
 #pragma unroll
       for (int j = 0; j < FB; ++j) acc[h / 2][h % 2][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // stage s of tile c; `ahead` stages further: its stage and tile (kSpan; past the last tile a
+  // stage past K, whose copies are zeros)
+  int s = 0, c = 0;
+  struct At {
+    int stage, tile;
+  };
+  const auto ahead = [&](int by) {
+    At t{s + by, c};
+    if constexpr (kSpan) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (t.stage >= stages) t.stage -= stages, ++t.tile;
+      if (t.tile >= tiles) t = At{stages, c};
+    }
+    return t;
+  };
+  const auto copy_b = [&](lds_bytes slot0, lds_bytes slot1, const At& t) {
+    if constexpr (kSpan) {
+      const int64_t shift = t.tile * 256 * p.ldb;
+      const int32_t whole = (int32_t)((HR - 1) * p.ldb + p.K);
+      b0.copy(slot0, t.stage, wave, shift, whole);
+      b1.copy(slot1, t.stage, wave, shift, n0 + t.tile * 256 + HR < p.N ? whole : 0);
+    } else {
+      b0.copy(slot0, t.stage, wave);
+      b1.copy(slot1, t.stage, wave);
+    }
+  };
   // stages 0 and 1, in the order in which they are waited for
   scales.copy(ss0, 0);
   a[0].copy(sa0, 0, wave);
-  b0.copy(sb0, 0, wave);
-  b1.copy(sc0, 0, wave);
+  copy_b(sb0, sc0, At{0, 0});
   if constexpr (AH == 2) a[1].copy(sx0, 0, wave);
-  scales.copy(ss1, 1);
-  a[0].copy(sa1, 1, wave);
-  b0.copy(sb1, 1, wave);
-  b1.copy(sc1, 1, wave);
+  const At second = ahead(1);
+  scales.copy(ss1, second.stage);
+  a[0].copy(sa1, second.stage, wave);
+  copy_b(sb1, sc1, second);
   wait_vm<(AH == 2 ? 4 : 3) * kCopies + 1>();
   wait_lgkm0();
   __builtin_amdgcn_s_barrier();
@@ -311,24 +343,51 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
   // B's square scales of the next stage, asked for ahead of a phase's MFMAs: its scalar loads
   // (each stage's from another line) would hold up the wait for the fragments
   float sq_next0 = 0.f, sq_next1 = 0.f;
-  const auto ask = [&](int s) {
+  const auto ask = [&](const At& t) {
     if constexpr (!kRows) {
-      const int64_t at = (s < stages ? s : stages - 1) * p.sb_stage;
+      int64_t at = (t.stage < stages ? t.stage : stages - 1) * p.sb_stage;
+      if constexpr (kSpan) at += 2 * t.tile * p.sb_row;
       sq_next0 = sq0[at];
-      sq_next1 = sq1[at];
+      if constexpr (kSpan)
+        sq_next1 = sq0[n0 + t.tile * 256 + HR < p.N ? at + p.sb_row : at];
+      else
+        sq_next1 = sq1[at];
       __builtin_amdgcn_sched_barrier(0);
     }
   };
-  ask(0);
+  ask(At{0, 0});
+  const auto store_pairs = [&] {
+    const int64_t n = n0 + c * 256 + wn * 32 + 4 * (lane >> 4);
+#pragma unroll
+    for (int h = 0; h < AH; ++h)
+#pragma unroll
+      for (int i = 0; i < FA; ++i) {
+        const int32_t pair = rows[h * HR + wm * 64 + i * 16 + (lane & 15)];
+        float* const out = (float*)p.out + (int64_t)pair * p.N + n;
+        if ((uint32_t)pair < (uint32_t)p.pairs) {
+#pragma unroll
+          for (int hb = 0; hb < 2; ++hb) {
+            if (hb == 1 && n0 + c * 256 + HR >= p.N) continue;
+#pragma unroll
+            for (int j = 0; j < FB; ++j) *(f32x4*)(out + hb * HR + j * 16) = acc[h][hb][i][j];
+          }
+        }
+#pragma unroll
+        for (int hb = 0; hb < 2; ++hb)
+#pragma unroll
+          for (int j = 0; j < FB; ++j) acc[h][hb][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+  };
   // stage s in buffer `buf`; its scales are read in its first phase, so that their place is
   // free for stage s + 2 in the second
-  auto step = [&](int s, auto buffer) {
+  auto step = [&](auto buffer) {
     constexpr int buf = decltype(buffer)::value;
     constexpr int two = (buf + 2) % 3;  // AH = 1: the buffer of stage s + 2
     const lds_bytes a_now = buf == 0 ? sa0 : buf == 1 ? sa1 : sx0;
     const lds_bytes b0_now = buf == 0 ? sb0 : buf == 1 ? sb1 : sx1;
     const lds_bytes b1_now = buf == 0 ? sc0 : buf == 1 ? sc1 : sx2;
     const lds_bytes ss_now = buf == 0 ? ss0 : buf == 1 ? ss1 : ss2;
+    const At one_on = ahead(1), two_on = ahead(2);
     if constexpr (!kRows) cs[0].set(sq_next0), cs[1].set(sq_next1);
     if (!idle) {
       fa.read(a_now, wm * 64, lane);
@@ -344,57 +403,63 @@ __device__ __forceinline__ void big_tile(Product p, const BigLds& lds, int64_t m
     }
     if constexpr (AH == 2) {
       __builtin_amdgcn_sched_barrier(0);  // the reads first: copies wait for their queue
-      a[1].copy(buf ? sx0 : sx1, s + 1, wave);
+      a[1].copy(buf ? sx0 : sx1, one_on.stage, wave);
       wait_vm<4 * kCopies + 1>();
       FP8_MEM_DONE
       FP8_MMA(0)
       FP8_MMA_DONE
       fa.read(buf ? sx1 : sx0, wm * 64, lane);
       __builtin_amdgcn_sched_barrier(0);
-      scales.copy(ss_now, s + 2);
-      a[0].copy(a_now, s + 2, wave);
-      b0.copy(b0_now, s + 2, wave);
-      b1.copy(b1_now, s + 2, wave);
+      scales.copy(ss_now, two_on.stage);
+      a[0].copy(a_now, two_on.stage, wave);
+      copy_b(b0_now, b1_now, two_on);
       wait_vm<4 * kCopies + 1>();
       FP8_MEM_DONE
-      ask(s + 1);
+      ask(one_on);
       FP8_MMA(AH - 1)
-      FP8_MMA_DONE
     } else {
       __builtin_amdgcn_sched_barrier(0);
-      scales.copy(two == 0 ? ss0 : two == 1 ? ss1 : ss2, s + 2);
-      a[0].copy(two == 0 ? sa0 : two == 1 ? sa1 : sx0, s + 2, wave);
-      b0.copy(two == 0 ? sb0 : two == 1 ? sb1 : sx1, s + 2, wave);
-      b1.copy(two == 0 ? sc0 : two == 1 ? sc1 : sx2, s + 2, wave);
+      scales.copy(two == 0 ? ss0 : two == 1 ? ss1 : ss2, two_on.stage);
+      a[0].copy(two == 0 ? sa0 : two == 1 ? sa1 : sx0, two_on.stage, wave);
+      copy_b(two == 0 ? sb0 : two == 1 ? sb1 : sx1, two == 0 ? sc0 : two == 1 ? sc1 : sx2, two_on);
       if constexpr (WIDE) wide[0].set(fb[0]), wide[1].set(fb[1]);
       wait_vm<3 * kCopies + 1>();
       FP8_MEM_DONE
-      ask(s + 1);
+      ask(one_on);
       FP8_MMA(0)
-      FP8_MMA_DONE
     }
+    ++s;
+    if constexpr (kSpan)
+      if (s == stages) {  // the tile's end; what it stores is waited for with the copies after it
+        store_pairs();
+        s = 0;
+        ++c;
+      }
+    FP8_MMA_DONE
   };
-  int s = 0;
+  const int all = kSpan ? stages * tiles : stages;
+  int n = 0;
   if constexpr (AH == 2) {
-    for (; s + 1 < stages; s += 2) {
-      step(s, std::integral_constant<int, 0>{});
-      step(s + 1, std::integral_constant<int, 1>{});
+    for (; n + 1 < all; n += 2) {
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
     }
-    if (s < stages) step(s, std::integral_constant<int, 0>{});
+    if (n < all) step(std::integral_constant<int, 0>{});
   } else {
-    for (; s + 2 < stages; s += 3) {
-      step(s, std::integral_constant<int, 0>{});
-      step(s + 1, std::integral_constant<int, 1>{});
-      step(s + 2, std::integral_constant<int, 2>{});
+    for (; n + 2 < all; n += 3) {
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
+      step(std::integral_constant<int, 2>{});
     }
-    if (s < stages) step(s, std::integral_constant<int, 0>{});
-    if (s + 1 < stages) step(s + 1, std::integral_constant<int, 1>{});
+    if (n < all) step(std::integral_constant<int, 0>{});
+    if (n + 1 < all) step(std::integral_constant<int, 1>{});
   }
 #undef FP8_MEM_DONE
 #undef FP8_MMA_DONE
 #undef FP8_MMA
   if (wave < NW / 2) __builtin_amdgcn_s_barrier();
   wait_vm<0>();  // the copies past the last stage (zeros) land before the LDS is given up
+  if constexpr (kSpan) return;
 
   // an A half at a time: 128 rows of 256 columns, 16 an object
   const int r = lane & 15, q = lane >> 4;
@@ -430,35 +495,48 @@ __global__ __launch_bounds__(512, 2) void big_tile_kernel(const Product p) {
   FP8_BIG_LDS(AH == 1)
   const int64_t tm = (p.m_end - p.m_first + AH * 128 - 1) / (AH * 128), tn = (p.N + 255) / 256;
   const TileId t = tile_of(blockIdx.x, tm, tn);
-  big_tile<AH, MODE, EPI, WIDE>(p, lds, p.m_first + t.m * (AH * 128), t.n * 256, false);
+  big_tile<AH, MODE, EPI, WIDE>(p, lds, p.m_first + t.m * (AH * 128), t.n * 256, false, 1, {});
 #endif
 }
 
 // The experts' products, a work-group a bucket block of 256 rows x 256 columns (kSwiglu: 128
-// gate, 128 up): a block of 128 pairs or fewer as a 128 x 256 tile, of 64 or fewer on half
-// the waves, which leaves the time to the weights' copies.
+// gate, 128 up; kPairs: several such in turn): a block of 128 pairs or fewer as a 128 x 256 tile,
+// of 64 or fewer on half the waves, which leaves the time to the weights' copies.
 template <Mode MODE, Epilogue EPI>
 __global__ __launch_bounds__(512, 2) void experts_kernel(Product p) {
 #if defined(__HIP_DEVICE_COMPILE__)
   FP8_BIG_LDS(true)
+  __shared__ int32_t rows[EPI == kPairs ? kBigRows : 1];
   constexpr int kCols = EPI == kSwiglu ? 128 : 256;
   const int64_t tm = *p.n_padded / kBigRows, tn = (p.N + kCols - 1) / kCols;
-  if ((int64_t)blockIdx.x >= tm * tn) return;  // the grid is sized for the most buckets
-  const TileId t = tile_of(blockIdx.x, tm, tn);
-  const int64_t m0 = t.m * kBigRows, n0 = t.n * kCols;
+  // column tiles of a work-group: as many as cost no round of work-groups more than one does
+  int span = 1;
+  if constexpr (EPI == kPairs) {
+    const int64_t rounds = (tm * tn + 255) / 256;
+#pragma unroll
+    for (int more = 2; more <= 4; more *= 2)
+      if ((tm * ((tn + more - 1) / more) + 255) / 256 * more * 32 <= rounds * 33) span = more;
+  }
+  const int64_t across = (tn + span - 1) / span;
+  if ((int64_t)blockIdx.x >= tm * across) return;  // the grid is sized for the most buckets
+  const TileId t = tile_of(blockIdx.x, tm, across);
+  const int64_t m0 = t.m * kBigRows, n0 = t.n * span * kCols;
+  const int tiles = (int)(tn - t.n * span < span ? tn - t.n * span : span);
   const int64_t b_rows = EPI == kSwiglu ? 2 * (int64_t)p.N : p.N;
   const int64_t e = uniform(p.block_expert[t.m]);
   p.b += e * b_rows * p.ldb;
   p.b_scales += e * (b_rows / kBlock) * p.sb_row;
+  if constexpr (EPI == kPairs)  // (the first barrier comes before its first use)
+    if (threadIdx.x < kBigRows) rows[threadIdx.x] = p.sorted[m0 + threadIdx.x];
   // a block's pairs come first
   const auto filled = [&](int row) {
     return uniform((uint32_t)p.sorted[m0 + row] < (uint32_t)p.pairs) != 0;
   };
   if (filled(128)) {
-    big_tile<2, MODE, EPI, false>(p, lds, m0, n0, false);
+    big_tile<2, MODE, EPI, false>(p, lds, m0, n0, false, tiles, (lds_i32)rows);
   } else {
     const bool idle = (threadIdx.x >> 8) != 0 && !filled(64);
-    big_tile<1, MODE, EPI, false>(p, lds, m0, n0, uniform(idle) != 0);
+    big_tile<1, MODE, EPI, false>(p, lds, m0, n0, uniform(idle) != 0, tiles, (lds_i32)rows);
   }
 #endif
 }
