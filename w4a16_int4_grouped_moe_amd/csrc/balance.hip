@@ -9,6 +9,12 @@
 // gradient is one more pass over the scores:
 //   p_te (c_be - sum_f c_bf p_tf), with c less its mean k n / S: sum_f p_tf = 1, and
 // counts near each other then lose nothing in the difference.
+//
+// 32768 tokens of 384 experts in 24 sequences (50 MB of scores): 17.8 us for the pieces, 2.8 TB/s, a
+// wave waiting in 64% of its cycles, of which about 7 us are a work-group's own start, counts and
+// sums (64 tokens, one work-group, take 7.8 us); 3.9 and 2.1 us for the two launches after it;
+// 21.3 us for the gradient, 4.7 TB/s. More work-groups of half the size, or the next tokens' scores
+// asked for ahead, took as long.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
