@@ -120,7 +120,9 @@ def test_quantize_experts_and_given_outputs():
 PRODUCTS = [(1, 8, 16), (1, 4096, 7168), (2, 264, 1008), (5, 2048, 256), (7, 72, 256), (8, 1000, 4112),
             (9, 520, 144), (16, 512, 1024), (17, 1000, 1008), (33, 136, 64), (48, 264, 704), (64, 128, 2048),
             (65, 4096, 1024), (128, 128, 256), (129, 1000, 480), (300, 264, 7168), (777, 72, 1008),
-            (777, 1000, 1008), (151, 6304, 64), (1030, 4800, 144), (2228, 3648, 272)]
+            (777, 1000, 1008), (151, 6304, 64), (1030, 4800, 144), (2228, 3648, 272),
+            # about the most that the kernels for a few rows hold in LDS: 1 and 4 rows quantised there
+            (1, 4096, 59264), (4, 4096, 15616)]
 
 
 def product_close(got, a, b, n):

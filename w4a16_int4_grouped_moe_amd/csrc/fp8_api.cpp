@@ -125,11 +125,14 @@ int check_experts(const moe_fp8_experts_problem* p) {
   return MOE_OK;
 }
 
-// Rows of a bucket's block: a few where an expert has about one, for the kernels that stream
-// weights; else a tile's (how many pairs are local, only the device knows)
+// Rows of a bucket's block: a few where an expert has two pairs at most on average, for the
+// kernels that stream weights; else a tile's (how many pairs are local, only the device knows).
+// 48 experts at 7168/2048, microseconds with a few and with tiles: 8 tokens (1.3 pairs) 280 and
+// 321, 16 (2.7) 413 and 376; 256 experts at 2048/1024: 64 tokens (2.0) 250 and 319, 128 (4.0)
+// 334 and 369.
 int32_t block_of(const moe_fp8_experts_problem* p) {
   const int64_t P = p->num_tokens * p->top_k;
-  if (P <= 4 * (int64_t)p->num_experts &&
+  if (P <= 2 * (int64_t)p->num_experts &&
       fp8::rows_fit(fp8::kBf16, fp8::kFewRows, 2 * (int64_t)p->inter, p->hidden) &&
       fp8::rows_fit(fp8::kBf16, fp8::kFewRows, p->hidden, p->inter))
     return fp8::kFewRows;

@@ -92,7 +92,7 @@ hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* 
 // quantised on the way; B's scales square, all of B (an expert's) below 2 GiB. rows_fit: whether
 // the kernel takes the sizes (experts: M = kFewRows, N of W13's 2 I rows or W2's).
 enum Source { kCodes = 0, kBf16 = 1, kF32 = 2 };
-constexpr int kMostRows = 64, kFewRows = 4;  // of codes; to quantise, and of an experts' bucket
+constexpr int kMostRows = 16, kFewRows = 4;  // of codes; to quantise, and of an experts' bucket
 bool rows_fit(Source source, int64_t M, int64_t N, int64_t K);
 hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream);
 // kSwiglu: from x bf16 [T, H], h fp32 [bucket rows, I]; kPairs: from that h

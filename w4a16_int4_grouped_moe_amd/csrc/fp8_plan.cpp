@@ -44,13 +44,14 @@ Cut cut_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-// Microseconds of the few-row kernel on codes: rounds of work-groups on 256 CUs, each a launch's
-// or a work-group's start and end and its stages. Measured at 4096 x 7168 and 7168 x 2048 with
-// 16 rows (11.6 and 13.5), 32 (15.0 and 15.0) and 64.
+// Microseconds of the few-row kernel: rounds of work-groups on 256 CUs, each a work-group's start
+// and end and its stages. Measured, and beside it 64 x 64 tiles with shares of K, in whole calls on
+// codes: 4096 x 7168 with 1, 8 and 16 rows 8.9, 9.8, 11.8 (tiles 12 to 12.7), 4096 x 28672 22.3, 24.5,
+// 29.4 (27.5), 7168 x 2048 9.2, 11.1, 13.8 (9.1 to 9.4); with 32 rows, which the kernel does not
+// take, it was 15.0 where tiles were 13.0.
 double rows_time(int64_t M, int64_t N, int64_t K) {
   const int64_t groups = (N + 15) / 16;
-  const double stage = M <= 16 ? 0.118 : M <= 32 ? 0.179 : 0.30;
-  return (double)((groups + 255) / 256) * (5.0 + stage * blocks_of(K));
+  return (double)((groups + 255) / 256) * (4.5 + (0.075 + 0.0035 * M) * blocks_of(K));
 }
 
 size_t product_workspace(bool wide, bool rows, int64_t M, int32_t N, int64_t K) {

@@ -2,8 +2,8 @@
 // (gfx950): decoding, where the time is the weights' way from memory.
 //
 // A work-group owns 16 weight rows (kSwiglu: 8 gate rows and their 8 up rows) and
-// all rows of A: one, two or four 16 x 16 MFMA tiles; of the experts' short rows several such
-// slices, so that a quantised A serves longer streams. Its eight waves take the
+// all rows of A, 16 at most; of the experts' short rows several such slices, so that a
+// quantised A serves longer streams. Its eight waves take the
 // stages of K (128 bytes of a row, one block of scales) in turn. A wave copies its stage's rows into
 // LDS in whole 128-byte lines, kD stages ahead, into a place of its own: it waits
 // for its own copies alone and never for another wave. At the end the waves'
@@ -48,13 +48,11 @@ inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t K, int slices) {
   return sums_at(fresh, rows, K) + (fresh ? slices * kWaves * rows * 64 : 0);
 }
 
-template <Source SRC, Epilogue EPI, int MT, int kD>
-__global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product p,
-                                                                              const int slices) {
+template <Source SRC, Epilogue EPI, int kD>
+__global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int slices) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPaired = EPI == kSwiglu, kExperts = EPI == kSwiglu || EPI == kPairs;
-  // the matrix units wait for memory anyway: one tile sums in fp32 (see fp8_gemm.hip)
-  constexpr bool kWide = EPI == kStoreF32 || MT == 1, kFresh = SRC != kCodes;
+  constexpr bool kFresh = SRC != kCodes;
   // an object a stage: the compiler then sees which copies a read has to wait for
   __shared__ __attribute__((aligned(1024))) uint8_t ring0[kWaves * kSlot], ring1[kWaves * kSlot];
   __shared__ __attribute__((aligned(1024))) uint8_t ring2[kWaves * kSlot];
@@ -98,14 +96,11 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
       (void*)p.b, 0, (int32_t)((b_rows - 1) * p.ldb + K), kBufferFlags);
   const __amdgpu_buffer_rsrc_t xres = __builtin_amdgcn_make_buffer_rsrc(
       (void*)p.a, 0, kFresh ? 0 : (int32_t)((M - 1) * p.lda + K), kBufferFlags);
-  uint32_t xoff[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-    xoff[i] = 16 * i + r < M ? (uint32_t)((16 * i + r) * p.lda) + 16 * q : kOut;
+  const uint32_t xoff = r < M ? (uint32_t)(r * p.lda) + 16 * q : kOut;
 
-  u32x4 x[kFresh ? 1 : kD][MT][2];
+  u32x4 x[kFresh ? 1 : kD][2];
   // a stage's loads, all of them always issued, so that a wave's waits can count them
-  constexpr int kLoads = 2 + (kFresh ? 0 : 2 * MT);
+  constexpr int kLoads = kFresh ? 2 : 4;
   // this wave's stages, slice after slice; the next one to load
   const int per = wave < stages ? (stages - wave + kWaves - 1) / kWaves : 0, total = per * slices;
   int next_s = wave, next_slice = 0;
@@ -124,13 +119,11 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!kFresh) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool in = s * kRow + h * 64 + 16 * q < K;
-          x[d][i][h] = __builtin_amdgcn_raw_buffer_load_b128(
-              xres, in ? xoff[i] + (uint32_t)(s * kRow + h * 64) : kOut, 0, 0);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const bool in = s * kRow + h * 64 + 16 * q < K;
+        x[d][h] = __builtin_amdgcn_raw_buffer_load_b128(
+            xres, in ? xoff + (uint32_t)(s * kRow + h * 64) : kOut, 0, 0);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     next_s += kWaves;
@@ -204,45 +197,34 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   __builtin_amdgcn_s_barrier();  // (no wait for the ring's copies)
   __builtin_amdgcn_sched_barrier(0);
 
-  f32x4 acc[1][MT][1];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[0][i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[1][1][1] = {{{f32x4{0.f, 0.f, 0.f, 0.f}}}};
+  const int row = r < M ? r : 0;  // sums past the last row are not stored
   auto step = [&](auto slot, int s) {
     constexpr int d = decltype(slot)::value;
     const lds_bytes src = ring[d] + wave * kSlot;
-    Frags<1> w[1];
-    Frags<MT> m;
-    float sa[MT];
+    Frags<1> w, m;
+    Wide<1> wide[1];
     ColumnScales<false, 1> cs[1];
     wait_vm<(kD - 1) * kLoads>();  // this stage's copies have landed
     __builtin_amdgcn_sched_barrier(0);
-    w[0].read(src, 0, lane);
+    w.read(src, 0, lane);
     cs[0].set(bs[kPaired && q >= 2 ? stages + s : s]);  // rows 4 q .. 4 q + 3: one square block
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if constexpr (kFresh) {
-        const int row = r < M ? r : 0;  // sums past the last row are not stored
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          m.v[i][h] = *(const u32x4*)(qa + row * stride + s * kRow + h * 64 + 16 * q);
-        sa[i] = as[row * stages + s];
-      } else {
-        m.v[i][0] = x[d][i][0], m.v[i][1] = x[d][i][1];
-        sa[i] = as[(16 * i + r < M ? 16 * i + r : 0) * stages + s];
-      }
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (kFresh)
+        m.v[0][h] = *(const u32x4*)(qa + row * stride + s * kRow + h * 64 + 16 * q);
+      else
+        m.v[0][h] = x[d][h];
     }
-    if constexpr (kWide) {
-      Wide<1> wide[1];
-      wide[0].set(w[0]);
-      mma_wide<false, 1, MT, 1>(acc, wide, m, sa, cs);
-    } else {
-      mma<false, 1, MT, 1>(acc, w, m, sa, cs);
-    }
+    const float sa[1] = {as[row * stages + s]};
+    // the matrix units wait for memory anyway: the sums are fp32 for either result
+    wide[0].set(w);
+    mma_wide<false, 1, 1, 1>(acc, wide, m, sa, cs);
     hold(acc);
     wait_lgkm0();  // the place is read before the next copy into it goes out
     load(slot);
   };
-  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row 16 i + r
+  // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row r
   float* const kept = (float*)(qa + sums_at(kFresh, rows, K));  // fresh: [wave][slice][row][16]
   int s = wave, slice = 0;
   auto keep = [&] {
@@ -266,15 +248,11 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
   __syncthreads();
   const float* sums = kept;  // of wave 0; the others' `pitch` further each
   int pitch = slices * rows * 16;
-  if constexpr (!kFresh) {  // two tiles an object
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      float* const at = i < 2 ? (float*)ring0 : (float*)ring1;
-      *(f32x4*)&at[(wave * 2 + (i & 1)) * 256 + r * 16 + 4 * q] = acc[0][i][0];
-    }
+  if constexpr (!kFresh) {
+    *(f32x4*)&((float*)ring0)[wave * 256 + r * 16 + 4 * q] = acc[0][0][0];
     __syncthreads();
     sums = (const float*)ring0;
-    pitch = 512;
+    pitch = 256;
   }
   const int count = (kFresh ? slices * M : M) * kStep;
   for (int i = threadIdx.x; i < count; i += kThreads) {
@@ -282,8 +260,6 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
     const int n = n0 + sl * kStep + j;
     if (n >= N) continue;
     const float* at = sums + (sl * rows + m) * 16 + j;
-    if constexpr (!kFresh && MT == 4)
-      if (m >= 32) at = (const float*)ring1 + (m - 32) * 16 + j;
     float v = 0.f;
 #pragma unroll
     for (int k = 0; k < kWaves; ++k) v += at[k * pitch];
@@ -303,11 +279,10 @@ __global__ __launch_bounds__(kThreads, MT == 1 ? 4 : 2) void rows_kernel(Product
 #endif
 }
 
-template <Source SRC, Epilogue EPI, int MT>
-hipError_t launch_tiles(const Product& p, int64_t buckets, hipStream_t stream) {
+template <Source SRC, Epilogue EPI>
+hipError_t launch(const Product& p, int64_t buckets, hipStream_t stream) {
   constexpr bool kExperts = EPI == kSwiglu || EPI == kPairs;
-  constexpr int kStep = EPI == kSwiglu ? 8 : 16;
-  constexpr int kD = kExperts ? 3 : MT == 1 ? 6 : MT == 2 ? 4 : 3;
+  constexpr int kStep = EPI == kSwiglu ? 8 : 16, kD = kExperts ? 3 : 6;
   const int64_t rows = kExperts ? kFewRows : p.M, all = (p.N + kStep - 1) / kStep;
   // experts: as many slices as leave two work-groups for every CU, and two on it (N is a
   // multiple of 128, and a work-group's columns lie in one block)
@@ -316,19 +291,11 @@ hipError_t launch_tiles(const Product& p, int64_t buckets, hipStream_t stream) {
     while (slices < 8 && all / (2 * slices) * buckets >= 512 &&
            extra_bytes(true, rows, p.K, 2 * slices) + kD * kWaves * kSlot <= 80 * 1024)
       slices *= 2;
-  hipLaunchKernelGGL((rows_kernel<SRC, EPI, MT, kD>),
+  hipLaunchKernelGGL((rows_kernel<SRC, EPI, kD>),
                      dim3((unsigned)((all + slices - 1) / slices), (unsigned)buckets),
                      dim3(kThreads), extra_bytes(SRC != kCodes, rows, p.K, slices), stream, p,
                      slices);
   return hipGetLastError();
-}
-template <Source SRC, Epilogue EPI>
-hipError_t launch(const Product& p, hipStream_t stream) {
-  if constexpr (SRC == kCodes) {
-    if (p.M > 32) return launch_tiles<SRC, EPI, 4>(p, 1, stream);
-    if (p.M > 16) return launch_tiles<SRC, EPI, 2>(p, 1, stream);
-  }
-  return launch_tiles<SRC, EPI, 1>(p, 1, stream);
 }
 
 }  // namespace
@@ -340,18 +307,18 @@ bool rows_fit(Source source, int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream) {
   if (source == kCodes)
-    return epilogue == kStoreBf16 ? launch<kCodes, kStoreBf16>(p, stream)
-                                  : launch<kCodes, kStoreF32>(p, stream);
+    return epilogue == kStoreBf16 ? launch<kCodes, kStoreBf16>(p, 1, stream)
+                                  : launch<kCodes, kStoreF32>(p, 1, stream);
   if (source == kBf16)
-    return epilogue == kStoreBf16 ? launch<kBf16, kStoreBf16>(p, stream)
-                                  : launch<kBf16, kStoreF32>(p, stream);
+    return epilogue == kStoreBf16 ? launch<kBf16, kStoreBf16>(p, 1, stream)
+                                  : launch<kBf16, kStoreF32>(p, 1, stream);
   return hipErrorInvalidValue;
 }
 
 hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buckets,
                                hipStream_t stream) {
-  if (epilogue == kSwiglu) return launch_tiles<kBf16, kSwiglu, 1>(p, buckets, stream);
-  if (epilogue == kPairs) return launch_tiles<kF32, kPairs, 1>(p, buckets, stream);
+  if (epilogue == kSwiglu) return launch<kBf16, kSwiglu>(p, buckets, stream);
+  if (epilogue == kPairs) return launch<kF32, kPairs>(p, buckets, stream);
   return hipErrorInvalidValue;
 }
 
