@@ -107,15 +107,21 @@ hipError_t launch_product(Mode mode, Epilogue e, const Product& p, void* split, 
   need(p.out, p.M * p.N * (e == kStoreBf16 ? 2 : 4), "out");
   // tiles address their rows by 32-bit offsets
   expect(255 * p.lda + p.K <= 0x7fffffff && 255 * p.ldb + p.K <= 0x7fffffff, "a tile's offsets");
-  const Cut c = cut_of(e == kStoreF32, mode == kRowScales, p.M, p.N, p.K);
+  const Plan plan = plan_of(e == kStoreF32, mode == kRowScales, p.M, p.N, p.K);
+  expect(plan.first >= 0 && plan.first < p.M, "first rows");
   const int64_t high[] = {128, 128, 256, 64}, wide[] = {128, 256, 256, 64};
-  expect(c.tile >= 0 && c.tile <= 3 && !(c.tile == 2 && e == kStoreF32), "tile");
-  expect(c.groups == (p.M + high[c.tile] - 1) / high[c.tile] * ((p.N + wide[c.tile] - 1) / wide[c.tile]), "groups");
   const int64_t stages = blocks_of(p.K);
-  expect(c.shares == 1 ? c.share >= stages : (c.tile == 0 || c.tile == 3), "shares");
-  expect((int64_t)c.shares * c.share >= stages && (int64_t)(c.shares - 1) * c.share < stages, "shares cover K");
-  if (c.tile == 0 || c.tile == 3) expect(c.groups * c.shares <= 1024, "a launch");
-  if (c.shares > 1) need(split, 4 * p.M * p.N * c.shares, "sums");
+  for (int part = 0; part < (plan.first ? 2 : 1); ++part) {
+    const Cut& c = part ? plan.rest : plan.whole;
+    const int64_t rows = part ? p.M - plan.first : plan.first ? plan.first : p.M;
+    expect(c.tile >= 0 && c.tile <= 3 && !(c.tile == 2 && e == kStoreF32), "tile");
+    expect(c.groups == (rows + high[c.tile] - 1) / high[c.tile] * ((p.N + wide[c.tile] - 1) / wide[c.tile]), "groups");
+    expect(c.shares == 1 ? c.share >= stages : (c.tile == 0 || c.tile == 3), "shares");
+    expect((int64_t)c.shares * c.share >= stages && (int64_t)(c.shares - 1) * c.share < stages, "shares cover K");
+    if (c.tile == 0 || c.tile == 3) expect(c.groups * c.shares <= 1024, "a launch");
+    if (c.shares > 1) need(split, 4 * rows * p.N * c.shares, "sums");
+    expect(part || !plan.first || c.shares == 1, "first rows without shares");
+  }
   return hipSuccess;
 }
 bool rows_fit(Source source, int64_t M, int64_t N, int64_t K) {
@@ -316,6 +322,7 @@ int main() {
   for (int64_t M : {0, 1, 2, 4, 5, 16, 17, 33, 64, 65, 129, 777, 4096, 70001, 1 << 20})
     for (int32_t N : {8, 72, 1000, 4096, 100008})
       for (int32_t K : {16, 144, 1008, 7168, 14016, 1 << 20}) products(M, N, K);
+  products(2314, 3456, 1232), products(5390, 2968, 1712), products(8783, 1800, 144);  // in two launches
   products((1ll << 31) - 256, 8, 16);
   products(8, 0x7fffff00, 16);
   for (int64_t M : {0, 1, 15, 127, 128, 129, 4099})

@@ -21,12 +21,15 @@ def test_named_cuts(tmp_path):
     lines = "".join("%d %d %d %d %d\n" % sizes for sizes in CUTS)
     res = subprocess.run([exe], input=lines, capture_output=True, text=True, timeout=120)
     assert res.returncode == 0, res.stderr[-2000:]
-    found = [t + ("s" if s != "1" else "") for t, s in (line.split() for line in res.stdout.splitlines())]
+    found = [("+" if f != "0" else "") + t + ("s" if s != "1" else "")
+             for f, t, s in (line.split() for line in res.stdout.splitlines())]
     assert dict(zip(CUTS, found, strict=True)) == CUTS
     for wide in (0, 1):
         for rows in (0, 1):
             cuts = {c for (w, r, *_), c in CUTS.items() if (w, r) == (wide, rows)}
-            assert cuts == {"0", "0s", "1", "3", "3s"} | (set() if wide else {"2"})
+            two = {"+3", "+3s"} if rows and not wide else {"+0", "+0s", "+3", "+3s"}
+            assert cuts == {"0", "0s", "1", "3", "3s"} | two | (
+                set() if wide else {"2"} if rows else {"2", "+1"})
 
 
 def test_host_code_under_sanitizers(tmp_path):

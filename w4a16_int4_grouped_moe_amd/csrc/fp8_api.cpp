@@ -82,7 +82,7 @@ enum Path { kFew, kFewPrepared, kTiled };
 Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize, bool square, bool wide) {
   if (!square || !fp8::rows_fit(fp8::kCodes, rows, cols, width)) return kTiled;
   const double few = fp8::rows_time(rows, cols, width);
-  const double tiled = fp8::cut_of(wide, false, rows, cols, width).time;
+  const double tiled = fp8::plan_of(wide, false, rows, cols, width).time;
   if (quantize && fp8::rows_fit(fp8::kBf16, rows, cols, width))
     return few < tiled + kAhead ? kFew : kTiled;
   return few >= tiled ? kTiled : quantize ? kFewPrepared : kFew;

@@ -704,13 +704,14 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ sum
     ((f32x4*)out)[u] = v;
 }
 
+// rows [p.m_first, p.m_end), as are launch_small's
 template <int AH, Mode MODE, Epilogue EPI, bool WIDE = false>
 hipError_t launch_big(Product p, hipStream_t stream) {
-  const int64_t tn = (p.N + 255) / 256;
+  const int64_t tn = (p.N + 255) / 256, end = p.m_end;
   const int64_t most = kMaxGroups / tn * (AH * 128);
-  for (int64_t m = 0; m < p.M; m += most) {
+  for (int64_t m = p.m_first; m < end; m += most) {
     p.m_first = m;
-    p.m_end = p.M - m < most ? p.M : m + most;
+    p.m_end = end - m < most ? end : m + most;
     const int64_t tm = (p.m_end - m + AH * 128 - 1) / (AH * 128);
     hipLaunchKernelGGL((big_tile_kernel<AH, MODE, EPI, WIDE>), dim3((unsigned)(tm * tn)),
                        dim3(512), 0, stream, p);
@@ -723,19 +724,18 @@ hipError_t launch_big(Product p, hipStream_t stream) {
 template <int TS, Mode MODE, Epilogue EPI>
 hipError_t launch_small(Product p, const Cut& c, void* split, hipStream_t stream) {
   constexpr bool kWide = EPI == kStoreF32;
-  p.m_end = p.M;
   const dim3 grid((unsigned)c.groups, c.shares);
   if (c.shares == 1) {
     hipLaunchKernelGGL((tile_kernel<TS, MODE, EPI, kWide>), grid, dim3(256), 0, stream, p, c.share);
     return hipGetLastError();
   }
-  void* const out = p.out;
+  void* const out = (char*)p.out + p.m_first * p.N * (EPI == kStoreF32 ? 4 : 2);
   p.out = split;
   hipLaunchKernelGGL((tile_kernel<TS, MODE, kPartial, kWide>), grid, dim3(256), 0, stream, p,
                      c.share);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t quads = p.M * (p.N / 4), groups = (quads + 255) / 256;
+  const int64_t quads = (p.m_end - p.m_first) * (p.N / 4), groups = (quads + 255) / 256;
   const int64_t y = (groups + (1 << 20) - 1) >> 20;
   hipLaunchKernelGGL(join_kernel<EPI>, dim3((unsigned)((groups + y - 1) / y), (unsigned)y),
                      dim3(256), 0, stream, (const float*)split, c.shares, quads, out);
@@ -743,13 +743,23 @@ hipError_t launch_small(Product p, const Cut& c, void* split, hipStream_t stream
 }
 
 template <Mode MODE, Epilogue EPI>
-hipError_t launch(const Product& p, void* split, hipStream_t stream) {
-  const Cut c = cut_of(EPI == kStoreF32, MODE == kRowScales, p.M, p.N, p.K);
+hipError_t launch_cut(const Product& p, const Cut& c, void* split, hipStream_t stream) {
   if constexpr (EPI == kStoreBf16)
     if (c.tile == 2) return launch_big<2, MODE, EPI>(p, stream);
   if (c.tile == 1) return launch_big<1, MODE, EPI, EPI == kStoreF32>(p, stream);
   return c.tile == 0 ? launch_small<128, MODE, EPI>(p, c, split, stream)
                      : launch_small<64, MODE, EPI>(p, c, split, stream);
+}
+
+template <Mode MODE, Epilogue EPI>
+hipError_t launch(Product p, void* split, hipStream_t stream) {
+  const Plan plan = plan_of(EPI == kStoreF32, MODE == kRowScales, p.M, p.N, p.K);
+  p.m_end = plan.first ? plan.first : p.M;
+  const hipError_t e = launch_cut<MODE, EPI>(p, plan.whole, split, stream);
+  if (e != hipSuccess || !plan.first) return e;
+  p.m_first = plan.first;
+  p.m_end = p.M;
+  return launch_cut<MODE, EPI>(p, plan.rest, split, stream);
 }
 
 }  // namespace

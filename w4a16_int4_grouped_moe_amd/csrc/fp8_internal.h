@@ -83,6 +83,14 @@ struct Cut {
   double time = 0;  // estimate, microseconds
 };
 Cut cut_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K);
+// A product is one launch (with its join, for shares) of all rows, or two: the first rows in whole
+// rounds of the largest tile, and the rest.
+struct Plan {
+  int64_t first = 0;  // rows of the first of two launches, 0: there is one
+  Cut whole, rest;    // of the first or all rows, without shares where there are two; of the rest
+  double time = 0;
+};
+Plan plan_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K);
 double rows_time(int64_t M, int64_t N, int64_t K);  // of the few-row kernel on codes
 // Bytes of the shares' sums (`split`, 16-byte aligned)
 size_t product_workspace(bool wide, bool rows, int64_t M, int32_t N, int64_t K);

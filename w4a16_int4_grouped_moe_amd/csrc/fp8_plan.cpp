@@ -44,6 +44,35 @@ Cut cut_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
+// A product whose last round of the largest tiles is nearly empty takes two launches: its first
+// rows in whole rounds, the rest cut on its own. Measured, whole calls on codes, one launch and
+// two: 4352 x 4096 x 4096 93 -> 75 us (fp32 results 169 -> 139), 5120 x 4096 x 7168 157 -> 146
+// (293 -> 267), 2304 x 8192 x 1024 37.8 -> 34.3 (59 -> 57). The second launch counts 3 us, and an
+// estimate less than 5% lower is within the estimates' error and stays one launch. With B in 1 x 128
+// blocks and bf16 results a nearly empty round takes less than it is counted for: two launches that
+// were estimated 13% lower took 62 -> 66 us (2560 x 7168 x 2048), 23% lower 79 -> 63 (2307 x 6840 x
+// 2544).
+Plan plan_of(bool wide, bool rows, int64_t M, int64_t N, int64_t K) {
+  Plan best;
+  best.whole = cut_of(wide, rows, M, N, K);
+  best.time = best.whole.time;
+  const int tile = wide ? 1 : 2;
+  const int64_t high = wide ? 128 : 256, tn = (N + 255) / 256;
+  const int64_t rounds = ((M + high - 1) / high * tn + 255) / 256;
+  if (rounds < 2) return best;
+  const int64_t first = (rounds - 1) * 256 / tn * high;  // of whole rounds
+  if (first <= 0 || first >= M) return best;
+  const Rate& rate = kRates[wide][rows];
+  const int64_t stages = blocks_of(K), groups = first / high * tn;
+  const Cut whole{tile, 1, (int)stages, groups,
+                  (double)((groups + 255) / 256) * (stages * rate.stage[tile] + rate.fixed[tile])};
+  const Cut rest = cut_of(wide, rows, M - first, N, K);
+  const double both = whole.time + rest.time + 3.0;
+  if (both < (rows && !wide ? 0.85 : 0.95) * best.time)
+    best.first = first, best.whole = whole, best.rest = rest, best.time = both;
+  return best;
+}
+
 // Microseconds of the few-row kernel: rounds of work-groups on 256 CUs, each a work-group's start
 // and end and its stages. Measured, and beside it 64 x 64 tiles with shares of K, in whole calls on
 // codes: 4096 x 7168 with 1, 8 and 16 rows 8.9, 9.8, 11.8 (tiles 12 to 12.7), 4096 x 28672 22.3, 24.5,
@@ -56,8 +85,9 @@ double rows_time(int64_t M, int64_t N, int64_t K) {
 
 size_t product_workspace(bool wide, bool rows, int64_t M, int32_t N, int64_t K) {
   if (M == 0) return 0;
-  const Cut c = cut_of(wide, rows, M, N, K);
-  return c.shares > 1 ? (size_t)c.shares * M * N * 4 : 0;
+  const Plan plan = plan_of(wide, rows, M, N, K);
+  const Cut& c = plan.first ? plan.rest : plan.whole;
+  return c.shares > 1 ? (size_t)c.shares * (M - plan.first) * N * 4 : 0;
 }
 
 }  // namespace fp8
