@@ -1,0 +1,52 @@
+"""The host code of the FP8 products for a few rows, by the library's own rules for sizes (no GPU)."""
+import os
+import shutil
+
+import pytest
+
+from .fp8_rows_host import ask, build_check
+from .test_sanitizers import ROCM_INC
+
+pytestmark = pytest.mark.skipif(not shutil.which("g++") or not os.path.isdir(ROCM_INC),
+                                reason="host compiler or HIP headers not found")
+
+
+@pytest.fixture(scope="module")
+def exe(tmp_path_factory):
+    return build_check(tmp_path_factory.mktemp("fp8_rows"))
+
+
+def longest(exe, source, M):
+    """The longest K that the few-row kernels take with M rows of 8 columns."""
+    ks = range(16, (1 << 20) + 1, 16)
+    fits = ask(exe, [f"f {source} {M} 8 {k}" for k in ks])
+    last = max((k for k, f in zip(ks, fits) if f == "1"), default=0)
+    assert all((f == "1") == (k <= last) for k, f in zip(ks, fits))
+    return last
+
+
+# 64 KB hold M quantised rows of K rounded up to 256 and 16 bytes more, 4 (M + 2) bytes of scales for each 128
+# of K, and 512 M bytes of sums; of codes the scales alone
+LONGEST = {(1, 1): 59392, (1, 4): 15104, (0, 1): 699008, (0, 4): 349440, (0, 5): 299520, (0, 16): 116480}
+
+
+@pytest.mark.parametrize("source,M", list(LONGEST))
+def test_longest_rows(exe, source, M):
+    assert longest(exe, source, M) == LONGEST[source, M]
+    assert longest(exe, source, 17 if source == 0 else 5) == 0
+
+
+def test_products_on_both_sides_of_the_limits(exe):
+    """Arrays and workspaces of every path, at the longest K of each and one step more."""
+    lines = [f"m {M} {N} {K} {q} {block} {kind}"
+             for M in (1, 2, 4, 5, 16, 17) for N in (8, 264, 4096)
+             for top in (*LONGEST.values(), 14000, (1 << 20) - 16) for K in (top, top + 16)
+             for q in (0, 1) for block in (1, 128) for kind in (0, 2)]
+    answers = dict(zip(lines, ask(exe, lines)))
+    for (source, M), K in LONGEST.items():
+        if source == 1:  # (codes that long are faster in tiles)
+            assert any(answers[f"m {M} {N} {K} 1 128 0"] == "f" for N in (8, 264, 4096)), M
+            assert not any(answers[f"m {M} {N} {K + 16} 1 128 {kind}"] == "f" for N in (8, 264, 4096) for kind in (0, 2))
+    for line, a in answers.items():
+        q, block = line.split()[4:6]
+        assert a in (("t", "r") if q == "0" else ("qt", "qr", "f")) and (block == "128" or a in ("t", "qt")), line

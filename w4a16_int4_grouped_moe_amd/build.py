@@ -18,8 +18,8 @@ PROBE_LIB = os.path.join(HERE, "libmoe_probe.so")
 PROBE_SOURCES = ["read_probe.hip"]
 SOURCES = ["align.hip", "route.hip", "gemm_small.hip", "gemm_prefill.hip", "prepack.hip", "combine.hip",
            "api.cpp", "ffn_gemm.hip", "ffn_small.hip", "mxfp4.hip", "ffn_plan.cpp",
-           "ffn_api.cpp", "fp8.hip", "fp8_gemm.hip", "fp8_rows.hip", "fp8_plan.cpp", "fp8_api.cpp", "balance.hip",
-           "balance_api.cpp"]
+           "ffn_api.cpp", "fp8.hip", "fp8_gemm.hip", "fp8_rows.hip", "fp8_plan.cpp", "fp8_rows_plan.cpp", "fp8_api.cpp",
+           "balance.hip", "balance_api.cpp"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 # packed fp32 VALU forms are disabled for all device code

@@ -102,6 +102,22 @@ hipError_t launch_product(Mode mode, Epilogue epilogue, const Product& p, void* 
 enum Source { kCodes = 0, kBf16 = 1, kF32 = 2 };
 constexpr int kMostRows = 16, kFewRows = 4;  // of codes; to quantise, and of an experts' bucket
 bool rows_fit(Source source, int64_t M, int64_t N, int64_t K);
+// A work-group of theirs: the waves, the bytes of a wave's stage (16 weight rows), the stages in
+// flight, and the columns of a slice
+constexpr int kRowsWaves = 8, kRowsSlot = 16 * kBlock, kRowsStages = 6, kExpertsStages = 3;
+constexpr int rows_step(Epilogue epilogue) { return epilogue == kSwiglu ? 8 : 16; }
+// Its LDS beside the ring: `rows` quantised rows (fresh; 16 of them at one offset lie in distinct
+// bank groups), the scales of A and of B by stage, and (fresh) at rows_sums_at the waves' sums of
+// each slice
+__host__ __device__ inline int rows_code_stride(int64_t K) {
+  return (int)((K + 255) / 256 * 256 + 16);
+}
+__host__ __device__ inline int64_t rows_sums_at(bool fresh, int64_t rows, int64_t K) {
+  return (fresh ? rows * rows_code_stride(K) : 0) + (4 * (rows + 2) * blocks_of(K) + 15) / 16 * 16;
+}
+int64_t rows_extra(bool fresh, int64_t rows, int64_t K, int slices);
+// Slices of an experts' work-group (N, K: of the product)
+int experts_slices(Epilogue epilogue, int64_t N, int64_t K, int64_t buckets);
 hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream);
 // kSwiglu: from x bf16 [T, H], h fp32 [bucket rows, I]; kPairs: from that h
 hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buckets,

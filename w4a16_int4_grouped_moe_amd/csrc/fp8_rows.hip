@@ -30,23 +30,8 @@
 namespace fp8 {
 namespace {
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kSlot = 16 * kRow;  // bytes of a wave's stage
-constexpr int64_t kMostExtra = 64 * 1024;  // LDS beside the ring
-
-// LDS rows of a quantised A: 16 rows at one offset lie in distinct bank groups
-__host__ __device__ inline int code_stride(int64_t K) {
-  return (int)((K + 255) / 256 * 256 + 16);
-}
-
-// LDS beside the ring: `rows` quantised rows (fresh), the scales of A and of B, by stage, and
-// (fresh) the waves' sums of each slice
-__host__ __device__ inline int64_t sums_at(bool fresh, int64_t rows, int64_t K) {
-  return (fresh ? rows * code_stride(K) : 0) + (4 * (rows + 2) * blocks_of(K) + 15) / 16 * 16;
-}
-inline int64_t extra_bytes(bool fresh, int64_t rows, int64_t K, int slices) {
-  return sums_at(fresh, rows, K) + (fresh ? slices * kWaves * rows * 64 : 0);
-}
+constexpr int kWaves = kRowsWaves, kThreads = 64 * kWaves;
+constexpr int kSlot = kRowsSlot;
 
 template <Source SRC, Epilogue EPI, int kD>
 __global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int slices) {
@@ -68,7 +53,7 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int 
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
   const int K = (int)p.K, stages = (K + kRow - 1) / kRow;
-  constexpr int kStep = kPaired ? 8 : 16;  // columns of a slice
+  constexpr int kStep = rows_step(EPI);  // columns of a slice
   const int N = p.N, n0 = blockIdx.x * kStep * slices;
   const int b_rows = kPaired ? 2 * N : N;
   int M = (int)p.M;
@@ -131,7 +116,7 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int 
   };
   auto fill = [&] { each<kD>([&](auto d) { load(d); }); };
 
-  const int stride = code_stride(K), rows = kExperts ? kFewRows : M;
+  const int stride = rows_code_stride(K), rows = kExperts ? kFewRows : M;
   float* const as = (float*)(qa + (kFresh ? rows * stride : 0));
   float* const bs = as + rows * stages;
   // scales into LDS; the first ones are asked for ahead of the ring's copies
@@ -225,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int 
     load(slot);
   };
   // lane (r, q) holds weight rows 4 q .. 4 q + 3 of A's row r
-  float* const kept = (float*)(qa + sums_at(kFresh, rows, K));  // fresh: [wave][slice][row][16]
+  float* const kept = (float*)(qa + rows_sums_at(kFresh, rows, K));  // fresh: [wave][slice][row][16]
   int s = wave, slice = 0;
   auto keep = [&] {
     if (r < M) *(f32x4*)&kept[((wave * slices + slice) * rows + r) * 16 + 4 * q] = acc[0][0][0];
@@ -282,28 +267,17 @@ __global__ __launch_bounds__(kThreads, 4) void rows_kernel(Product p, const int 
 template <Source SRC, Epilogue EPI>
 hipError_t launch(const Product& p, int64_t buckets, hipStream_t stream) {
   constexpr bool kExperts = EPI == kSwiglu || EPI == kPairs;
-  constexpr int kStep = EPI == kSwiglu ? 8 : 16, kD = kExperts ? 3 : 6;
+  constexpr int kStep = rows_step(EPI), kD = kExperts ? kExpertsStages : kRowsStages;
   const int64_t rows = kExperts ? kFewRows : p.M, all = (p.N + kStep - 1) / kStep;
-  // experts: as many slices as leave two work-groups for every CU, and two on it (N is a
-  // multiple of 128, and a work-group's columns lie in one block)
-  int slices = 1;
-  if (kExperts)
-    while (slices < 8 && all / (2 * slices) * buckets >= 512 &&
-           extra_bytes(true, rows, p.K, 2 * slices) + kD * kWaves * kSlot <= 80 * 1024)
-      slices *= 2;
+  const int slices = kExperts ? experts_slices(EPI, p.N, p.K, buckets) : 1;
   hipLaunchKernelGGL((rows_kernel<SRC, EPI, kD>),
                      dim3((unsigned)((all + slices - 1) / slices), (unsigned)buckets),
-                     dim3(kThreads), extra_bytes(SRC != kCodes, rows, p.K, slices), stream, p,
+                     dim3(kThreads), rows_extra(SRC != kCodes, rows, p.K, slices), stream, p,
                      slices);
   return hipGetLastError();
 }
 
 }  // namespace
-
-bool rows_fit(Source source, int64_t M, int64_t N, int64_t K) {
-  return M >= 1 && M <= (source == kCodes ? kMostRows : kFewRows) && N < (1 << 26) &&
-         N * K <= 0x7fffffff && extra_bytes(source != kCodes, M, K, 1) <= kMostExtra;
-}
 
 hipError_t launch_rows(Source source, Epilogue epilogue, const Product& p, hipStream_t stream) {
   if (source == kCodes)
