@@ -69,7 +69,8 @@ int moe_fp8_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, int
  * result in the 2-norm on common activations (a bf16 rounding: 1.7e-3). B: codes
  * and scales of [cols, width], blocks as b_block says. A [rows, width]: codes
  * and scales in 1 x 128 blocks, or bf16 with a_scales NULL, which is quantised
- * as by moe_fp8_quantize. rows == 0 is a no-op.
+ * as by moe_fp8_quantize: the result is that of its codes, to the bit. rows == 0
+ * is a no-op.
  */
 int moe_fp8_matmul(const void *a, const float *a_scales, const uint8_t *b, const float *b_scales,
                    int32_t b_block, int64_t rows, int32_t cols, int32_t width, int32_t out_type,

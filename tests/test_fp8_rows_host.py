@@ -50,3 +50,15 @@ def test_products_on_both_sides_of_the_limits(exe):
     for line, a in answers.items():
         q, block = line.split()[4:6]
         assert a in (("t", "r") if q == "0" else ("qt", "qr", "f")) and (block == "128" or a in ("t", "qt")), line
+
+
+def test_a_bf16_operand_and_its_codes_take_the_same_kernel(exe):
+    """... few rows or tiles, whose sums differ in their order and, for bf16 results, their accuracy."""
+    sizes = [(M, N, K, kind) for M in (1, 2, 3, 4, 5, 8, 16, 17, 64) for kind in (0, 2)
+             for N in (8, 256, 1024, 2048, 4096, 7168, 8192, 28672)
+             for K in (128, 1024, 2048, 4096, 7168, 8192, 14336, 15104, 15120, 59392)]
+    bf16 = ask(exe, [f"m {M} {N} {K} 1 128 {kind}" for M, N, K, kind in sizes])
+    codes = ask(exe, [f"m {M} {N} {K} 0 128 {kind}" for M, N, K, kind in sizes])
+    differ = [s for s, x, q in zip(sizes, bf16, codes) if q != {"f": "r", "qr": "r", "qt": "t"}[x]]
+    assert not differ, (len(differ), len(sizes), differ[:10])
+    assert {"f", "qr", "qt"} == set(bf16)

@@ -76,16 +76,20 @@ struct Quantized {
 };
 
 // Which kernel a product takes: few rows, quantised on the way where they are bf16 and four at
-// most, or by a launch ahead (kAhead microseconds); or tiles
+// most, or by a launch ahead; or tiles. Sizes alone choose between few rows and tiles, so that a
+// bf16 operand and its codes give the same bits: up to four rows the few-row kernel may be
+// kAhead microseconds longer by the estimates, the launch that tiles of a bf16 operand need. Codes
+// alone, which do not need it, in few rows and in tiles, microseconds: 1 x 256 x 8192 6.9 and 13.1, 4 x
+// 1024 x 8192 7.9 and 12.4, 1 x 7168 x 7168 15.3 and 17.7, 4 x 7168 x 2048 10.0 and 9.7, 4 x 7168 x 1024
+// 8.8 and 6.8; bf16 at the last 9.4 and 8.9.
 constexpr double kAhead = 3.0;
 enum Path { kFew, kFewPrepared, kTiled };
 Path path_of(int64_t rows, int32_t cols, int32_t width, bool quantize, bool square, bool wide) {
   if (!square || !fp8::rows_fit(fp8::kCodes, rows, cols, width)) return kTiled;
-  const double few = fp8::rows_time(rows, cols, width);
+  const bool fresh = fp8::rows_fit(fp8::kBf16, rows, cols, width);
   const double tiled = fp8::plan_of(wide, false, rows, cols, width).time;
-  if (quantize && fp8::rows_fit(fp8::kBf16, rows, cols, width))
-    return few < tiled + kAhead ? kFew : kTiled;
-  return few >= tiled ? kTiled : quantize ? kFewPrepared : kFew;
+  if (fp8::rows_time(rows, cols, width) >= tiled + (fresh ? kAhead : 0)) return kTiled;
+  return quantize && !fresh ? kFewPrepared : kFew;
 }
 
 // The shares' sums of a product, of either type of result and either kind of B
