@@ -23,3 +23,15 @@ def ask(exe, lines):
     answers = res.stdout.splitlines()
     assert len(answers) == len(lines)
     return answers
+
+
+# Experts' calls that take the few-row kernels, and how many slices a work-group has in either product:
+# (tokens, hidden, inter, experts, top_k). 8 waves share the stages of 128: more than 3 stages a wave use a place
+# of its ring again; 7, 9 and 11 stages leave waves without one or with one more than others.
+FEW_EXPERTS = {
+    (1, 7168, 2048, 8, 8): "few 1 4", (2, 7168, 1152, 8, 8): "few 1 8", (4, 2048, 1024, 8, 4): "few 2 2",
+    (5, 1408, 896, 8, 3): "few 1 1", (4, 4096, 256, 8, 4): "few 1 4", (3, 7168, 128, 8, 5): "few 1 4",
+    (2, 1024, 4096, 16, 16): "few 8 2", (16, 2176, 1152, 24, 3): "few 8 4", (8, 2048, 4096, 16, 4): "few 8 4",
+    (1, 15104, 128, 1, 1): "few 1 1", (4, 128, 15104, 4, 2): "few 8 1", (4, 1152, 1024, 16, 4): "few 4 2",
+    (32, 2048, 512, 64, 4): "few 8 8",
+}

@@ -4,7 +4,7 @@ import shutil
 
 import pytest
 
-from .fp8_rows_host import ask, build_check
+from .fp8_rows_host import FEW_EXPERTS, ask, build_check
 from .test_sanitizers import ROCM_INC
 
 pytestmark = pytest.mark.skipif(not shutil.which("g++") or not os.path.isdir(ROCM_INC),
@@ -62,3 +62,11 @@ def test_a_bf16_operand_and_its_codes_take_the_same_kernel(exe):
     differ = [s for s, x, q in zip(sizes, bf16, codes) if q != {"f": "r", "qr": "r", "qt": "t"}[x]]
     assert not differ, (len(differ), len(sizes), differ[:10])
     assert {"f", "qr", "qt"} == set(bf16)
+
+
+def test_named_experts_take_the_few_row_kernels(exe):
+    """... with the slices that they are named for, so that a change of the rules cannot empty the GPU tests."""
+    found = ask(exe, ["e %d %d %d %d %d" % size for size in FEW_EXPERTS])
+    assert dict(zip(FEW_EXPERTS, found)) == FEW_EXPERTS
+    assert {int(s) for a in found for s in a.split()[1:]} == {1, 2, 4, 8}
+    assert ask(exe, ["e 5 256 128 2 1"]) == ["tiles"]

@@ -5,6 +5,7 @@ import torch
 
 import w4a16_int4_grouped_moe_amd as moe
 from tests import fp8_experts_oracle as x
+from tests.fp8_rows_host import FEW_EXPERTS
 from tests.test_fp8_experts_oracle import SIZES
 
 pytestmark = pytest.mark.gpu
@@ -53,3 +54,16 @@ def test_a_run_and_a_shared_expert():
     weights = torch.cat([weights, torch.ones_like(weights[:, :1])], dim=1)
     q13, q2 = (moe.fp8_quantize((w * w.shape[2] ** -0.5).bfloat16(), block=128) for w in (w13, w2))
     check((act.bfloat16(), ids, weights, (q13.codes, q13.scales), (q2.codes, q2.scales), 0))
+
+
+@pytest.mark.parametrize("size", list(FEW_EXPERTS), ids=lambda s: "-".join(map(str, s)) + " " + FEW_EXPERTS[s])
+def test_few_rows_deep_and_in_slices(size):
+    """The few-row kernels as decoding uses them: several stages a wave, several slices a work-group, one to four
+    pairs a bucket."""
+    T, H, I, E, k = size
+    args = [*x.inputs(T, H, I, E, E, k, 0, seed=T, device="cuda"), 0]
+    check(args)
+    pair = torch.arange(T * k, device="cuda").reshape(T, k)
+    for full in (2, 3, 4, 5):  # pairs of an expert; of five, one is in a bucket of its own
+        args[1] = (pair // full % E).int()
+        check(args)
