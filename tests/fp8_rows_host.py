@@ -35,3 +35,10 @@ FEW_EXPERTS = {
     (1, 15104, 128, 1, 1): "few 1 1", (4, 128, 15104, 4, 2): "few 8 1", (4, 1152, 1024, 16, 4): "few 4 2",
     (32, 2048, 512, 64, 4): "few 8 8",
 }
+
+# Experts of these many pairs each (in buckets of 256 rows: blocks that are full, of at most 128 and of at most 64
+# pairs), 64 blocks, and sizes (hidden, inter) at which the second product takes so many column tiles of
+# 256 a work-group in turn: the last tile half or whole, the last group short, stages of 128 odd and even
+PAIRS = [1, 64, 65, 128, 129, 256, 257, 300, 0, 40, 90, 200] * 4 + [1, 64, 65, 128, 129, 256, 257, 300, 0, 40, 90]
+SPANS = {(1152, 128): 2, (1152, 256): 2, (1408, 384): 2, (2048, 640): 2, (896, 384): 1,
+         (3200, 128): 4, (3456, 384): 4, (3712, 256): 4, (3968, 640): 4}

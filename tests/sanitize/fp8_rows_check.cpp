@@ -8,6 +8,7 @@
 //   e T H I E k                   moe_fp8_experts_forward: "few" and the slices of a work-group of both products,
 //                                 or "tiles"
 //   f source M N K                rows_fit
+//   s tm tn                       experts_span
 #include <cstdio>
 #include <string>
 #include <vector>
@@ -125,7 +126,7 @@ int main() {
   char op;
   long long v[6];
   while (std::scanf(" %c", &op) == 1) {
-    const int n = op == 'm' ? 6 : op == 'e' ? 5 : 4;
+    const int n = op == 'm' ? 6 : op == 'e' ? 5 : op == 's' ? 2 : 4;
     for (int i = 0; i < n; ++i)
       if (std::scanf("%lld", &v[i]) != 1) return 2;
     buffers.clear();
@@ -154,6 +155,8 @@ int main() {
       float *s13 = (float*)buffer(E * square_scales(2 * I, H)), *s2 = (float*)buffer(E * square_scales(H, I));
       expect(moe_fp8_experts_forward(x, ids, w, w13, s13, w2, s2, buffer(2 * T * H), &p, buffer(bytes), bytes,
                                      nullptr) == MOE_OK, "experts");
+    } else if (op == 's') {
+      launched = std::to_string(fp8::experts_span(v[0], v[1]));
     } else {
       launched = fp8::rows_fit((fp8::Source)v[0], v[1], v[2], v[3]) ? "1" : "0";
     }

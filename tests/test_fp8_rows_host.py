@@ -4,7 +4,7 @@ import shutil
 
 import pytest
 
-from .fp8_rows_host import FEW_EXPERTS, ask, build_check
+from .fp8_rows_host import FEW_EXPERTS, PAIRS, SPANS, ask, build_check
 from .test_sanitizers import ROCM_INC
 
 pytestmark = pytest.mark.skipif(not shutil.which("g++") or not os.path.isdir(ROCM_INC),
@@ -70,3 +70,17 @@ def test_named_experts_take_the_few_row_kernels(exe):
     assert dict(zip(FEW_EXPERTS, found)) == FEW_EXPERTS
     assert {int(s) for a in found for s in a.split()[1:]} == {1, 2, 4, 8}
     assert ask(exe, ["e 5 256 128 2 1"]) == ["tiles"]
+
+
+def test_named_sizes_take_their_column_tiles_in_turn(exe):
+    blocks = sum(-(-n // 256) for n in PAIRS)
+    found = ask(exe, [f"s {blocks} {-(-hidden // 256)}" for hidden, _ in SPANS])
+    assert dict(zip(SPANS, map(int, found))) == SPANS
+    for hidden, inter in SPANS:  # tiles, not the few-row kernels
+        assert ask(exe, [f"e {sum(PAIRS) // 2} {hidden} {inter} {len(PAIRS)} 2"]) == ["tiles"]
+    # never a round of work-groups more than 1/32 over one tile each
+    sizes = [(tm, tn) for tm in range(1, 200, 3) for tn in range(1, 40)]
+    for (tm, tn), a in zip(sizes, ask(exe, [f"s {tm} {tn}" for tm, tn in sizes])):
+        rounds = lambda span: -(-tm * -(-tn // span) // 256) * span  # noqa: E731
+        best = max(s for s in (1, 2, 4) if rounds(s) * 32 <= rounds(1) * 33)
+        assert int(a) == best

@@ -5,7 +5,7 @@ import torch
 
 import w4a16_int4_grouped_moe_amd as moe
 from tests import fp8_experts_oracle as x
-from tests.fp8_rows_host import FEW_EXPERTS
+from tests.fp8_rows_host import FEW_EXPERTS, PAIRS, SPANS
 from tests.test_fp8_experts_oracle import SIZES
 
 pytestmark = pytest.mark.gpu
@@ -67,3 +67,19 @@ def test_few_rows_deep_and_in_slices(size):
     for full in (2, 3, 4, 5):  # pairs of an expert; of five, one is in a bucket of its own
         args[1] = (pair // full % E).int()
         check(args)
+
+
+@pytest.mark.parametrize("size", list(SPANS), ids=lambda s: "%d-%d" % s + " %d in turn" % SPANS[s])
+def test_column_tiles_in_turn(size):
+    """The second product with one, two and four column tiles a work-group, over blocks of every filling."""
+    (H, I), E, T = size, len(PAIRS), sum(PAIRS) // 2
+    args = [*x.inputs(T, H, I, E, E, 2, 0, seed=H + I, device="cuda"), 0]
+    owner = torch.repeat_interleave(torch.arange(E), torch.tensor(PAIRS))
+    order = torch.randperm(len(owner), generator=torch.Generator().manual_seed(1))
+    args[1] = owner[order].reshape(T, 2).int().cuda()
+    out = check(args)
+    # in a workspace of exactly the size asked for, full of NaN, with guards around it
+    need = moe.fp8_experts_workspace_size(T, H, I, E, 2)
+    room = torch.full((need + 512,), 0xff, dtype=torch.uint8, device="cuda")
+    assert torch.equal(run(*args, workspace=room[256:256 + need]), out)
+    assert (room[:256] == 0xff).all() and (room[256 + need:] == 0xff).all()

@@ -520,14 +520,7 @@ __global__ __launch_bounds__(512, 2) void experts_kernel(Product p) {
   __shared__ int32_t rows[EPI == kPairs ? kBigRows : 1];
   constexpr int kCols = EPI == kSwiglu ? 128 : 256;
   const int64_t tm = *p.n_padded / kBigRows, tn = (p.N + kCols - 1) / kCols;
-  // column tiles of a work-group: as many as cost no round of work-groups more than one does
-  int span = 1;
-  if constexpr (EPI == kPairs) {
-    const int64_t rounds = (tm * tn + 255) / 256;
-#pragma unroll
-    for (int more = 2; more <= 4; more *= 2)
-      if ((tm * ((tn + more - 1) / more) + 255) / 256 * more * 32 <= rounds * 33) span = more;
-  }
+  const int span = EPI == kPairs ? experts_span(tm, tn) : 1;
   const int64_t across = (tn + span - 1) / span;
   if ((int64_t)blockIdx.x >= tm * across) return;  // the grid is sized for the most buckets
   const TileId t = tile_of(blockIdx.x, tm, across);

@@ -126,5 +126,14 @@ hipError_t launch_experts_rows(Epilogue epilogue, const Product& p, int64_t buck
 // rows, a launch's of at most kMaxGroups tiles
 constexpr int kBigRows = 256;
 hipError_t launch_experts(Epilogue epilogue, const Product& p, hipStream_t stream);
+// kPairs: column tiles that a work-group takes in turn, tm blocks by tn tiles (the device knows the
+// blocks): as many as cost no round of work-groups on 256 CUs more than one does
+__host__ __device__ inline int experts_span(int64_t tm, int64_t tn) {
+  const int64_t rounds = (tm * tn + 255) / 256;
+  int span = 1;
+  for (int more = 2; more <= 4; more *= 2)
+    if ((tm * ((tn + more - 1) / more) + 255) / 256 * more * 32 <= rounds * 33) span = more;
+  return span;
+}
 
 }  // namespace fp8
