@@ -51,7 +51,8 @@ extern "C" {
 int moe_fp8_quantize(const void *x, int32_t type, int64_t rows, int32_t width, int32_t block,
                      uint8_t *codes, float *scales, void *stream);
 
-/* The values of codes and scales, rounded once to `type`: out [rows, width]. */
+/* The values of codes and scales, each its code times its scale in fp32, rounded to `type`: out
+ * [rows, width]. */
 int moe_fp8_dequantize(const uint8_t *codes, const float *scales, int64_t rows, int32_t width,
                        int32_t block, int32_t type, void *out, void *stream);
 
@@ -62,7 +63,9 @@ int moe_fp8_matmul_workspace_size(int64_t rows, int32_t cols, int32_t width, int
 /*
  * out [rows, cols] = A B^T, rounded once to out_type (MOE_TYPE_BF16 or
  * MOE_TYPE_FP32). The products of a block of 128 are summed, multiplied by the
- * product of the two scales, and added to the others' in fp32. For fp32 results
+ * product of the two scales, and added to the others' in fp32; where that product
+ * of scales is below 2^-126 or past fp32's largest, results lose digits or are 0,
+ * infinite or NaN. For fp32 results
  * a block's sum is fp32 throughout; for bf16 results the FP8 matrix units form
  * it, which cut each of eight products off 2^13 below the power of two of the
  * largest's exponents: at most 2^-10 of the sum of magnitudes, 2.6e-5 of a

@@ -95,3 +95,27 @@ def test_nan_codes_in_experts(T, E, k):
     assert out[mine, 260].isnan().all()
     out[mine, 260] = clean[mine, 260]
     assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 70, 1500])
+@pytest.mark.parametrize("powers", [(-126, 0), (-126, 126), (0, -126), (120, -100), (-100, 127), (60, 40), (-60, -66)])
+def test_scales_to_the_ends_of_fp32(M, powers):
+    """Scales of any power whose product is a normal number: the result is that of scales of 1, moved."""
+    N, K, (pa, pb) = 264, 400, powers
+    a, w = moe.fp8_quantize(rand(M, K, seed=M)), published(N, K, seed=N)
+    ones = lambda s, p: torch.full_like(s, 2.0 ** p)  # noqa: E731
+    for block, sb in ((128, w.scales), (1, torch.ones(-(-K // 128), N, device="cuda"))):
+        for dtype in (torch.bfloat16, torch.float32):
+            base = moe.fp8_matmul(moe.Fp8(a.codes, ones(a.scales, 0), 1), moe.Fp8(w.codes, ones(sb, 0), block), dtype=dtype)
+            out = moe.fp8_matmul(moe.Fp8(a.codes, ones(a.scales, pa), 1), moe.Fp8(w.codes, ones(sb, pb), block), dtype=dtype)
+            assert torch.equal(out.double(), base.double() * 2.0 ** (pa + pb)), (block, dtype)
+
+
+def test_dequantised_values_are_fp32_products_rounded():
+    """Scales that are no powers of two: the product of code and scale in fp32, then the type."""
+    w = published(130, 144, seed=3)
+    want = moe.fp8_dequantize(w, dtype=torch.float32)
+    s = w.scales.repeat_interleave(128, 0)[:130].repeat_interleave(128, 1)[:, :144]
+    assert torch.equal(want, w.codes.float() * s)
+    assert torch.equal(moe.fp8_dequantize(w), want.bfloat16())
+    assert torch.equal(moe.fp8_dequantize(w, dtype=torch.float16), want.half())
