@@ -69,7 +69,10 @@ def test_named_experts_take_the_few_row_kernels(exe):
     found = ask(exe, ["e %d %d %d %d %d" % size for size in FEW_EXPERTS])
     assert dict(zip(FEW_EXPERTS, found)) == FEW_EXPERTS
     assert {int(s) for a in found for s in a.split()[1:]} == {1, 2, 4, 8}
-    assert ask(exe, ["e 5 256 128 2 1"]) == ["tiles"]
+    # at most two pairs an expert on average, hidden and inter up to 15104
+    few = ["e 4 256 128 2 1", "e 12 256 128 48 8", "e 1 15104 128 1 1", "e 1 128 15104 1 1", "e 1 15104 15104 1 1"]
+    tiles = ["e 5 256 128 2 1", "e 13 256 128 48 8", "e 1 15232 128 1 1", "e 1 128 15232 1 1"]
+    assert all(a.startswith("few") for a in ask(exe, few)) and ask(exe, tiles) == ["tiles"] * len(tiles)
 
 
 def test_named_sizes_take_their_column_tiles_in_turn(exe):

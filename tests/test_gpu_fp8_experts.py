@@ -16,10 +16,10 @@ def run(act, ids, weights, w13, w2, base, **given):
                                    expert_base=base, **given)
 
 
-def check(args):
+def check(args, bound=x.BOUND):
     out = run(*args)
     whole, each = x.distance(out, *args)
-    assert whole <= 1 and each <= 1, (whole, each)
+    assert whole <= bound / x.BOUND and each <= 1, (whole, each)
     assert torch.equal(out, run(*args))
     return out
 
@@ -59,14 +59,14 @@ def test_a_run_and_a_shared_expert():
 @pytest.mark.parametrize("size", list(FEW_EXPERTS), ids=lambda s: "-".join(map(str, s)) + " " + FEW_EXPERTS[s])
 def test_few_rows_deep_and_in_slices(size):
     """The few-row kernels as decoding uses them: several stages a wave, several slices a work-group, one to four
-    pairs a bucket."""
+    pairs a bucket. They sum in fp32."""
     T, H, I, E, k = size
     args = [*x.inputs(T, H, I, E, E, k, 0, seed=T, device="cuda"), 0]
-    check(args)
+    check(args, x.FP32_SUMS)
     pair = torch.arange(T * k, device="cuda").reshape(T, k)
     for full in (2, 3, 4, 5):  # pairs of an expert; of five, one is in a bucket of its own
         args[1] = (pair // full % E).int()
-        check(args)
+        check(args, x.FP32_SUMS)
 
 
 @pytest.mark.parametrize("size", list(SPANS), ids=lambda s: "%d-%d" % s + " %d in turn" % SPANS[s])

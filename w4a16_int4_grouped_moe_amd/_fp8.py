@@ -169,7 +169,9 @@ def _out_type(dtype, default_of=None):
 def fp8_matmul(a, b: Fp8, out=None, dtype=None, workspace=None):
     """a [M, K] times the transpose of b [N, K] (moe_fp8_matmul) -> [M, N] in dtype (bfloat16,
     the default, or float32). a: an Fp8 with block=1, or a bf16 tensor that is quantised as by
-    fp8_quantize; b: an Fp8 of either block. Autograd records nothing."""
+    fp8_quantize, with the same result; b: an Fp8 of either block. float32 results are summed in
+    fp32 throughout, bfloat16 ones of more than a few rows in the FP8 matrix units, which cut
+    small products off (moe_fp8.h). Autograd records nothing."""
     if isinstance(a, Fp8):
         _is_fp8(a, "a", 1, 2)
         dev, (M, K), codes, scales = a.device, a.shape, a.codes, a.scales.data_ptr()
@@ -202,8 +204,9 @@ def fp8_matmul_backward_workspace_size(rows: int, cols: int, width: int) -> int:
 def fp8_matmul_backward(dout, a, b: Fp8, da=None, db=None, dtype=None, workspace=None):
     """Gradients of fp8_matmul(a, b) for a and b's matrix (moe_fp8_matmul_backward): dout bf16
     [M, N], a bf16 [M, K], b an Fp8 with block=128 of [N, K] -> (da [M, K], db [N, K]) in dtype
-    (bfloat16, the default, or float32). Both operands of each product are quantised in blocks
-    of 128 along the axis that it sums over. Given output tensors are overwritten."""
+    (bfloat16, the default, or float32, which also sums in fp32 throughout). Both operands of
+    each product are quantised in blocks of 128 along the axis that it sums over. Given output
+    tensors are overwritten."""
     dev = _gpu(a, "a")
     torch = _ffn.torch
     _need(a, "a", torch.bfloat16, 2, dev)

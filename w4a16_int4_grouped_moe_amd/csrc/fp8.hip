@@ -148,8 +148,10 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
 }
 
 // A tile of 128 rows on its way to being 128 bytes of a column: 32 words of four
-// rows, columns 33 words apart, so that 64 lanes that write or read one word each of
-// eight columns meet 64 banks.
+// rows, columns 33 words apart. The eight columns that a wave writes are 16 apart, 528
+// words, 16 banks of 64: the eight words of columns 64 apart meet, two ways; so do some of the
+// eight neighbouring columns that it reads. Conflicts are 56% of the LDS's busy cycles in
+// prepare_kernel, where the LDS is busy in 14 to 39%, and memory is what bounds it.
 [[maybe_unused]] constexpr int kPitch = 33;
 
 #if defined(__HIP_DEVICE_COMPILE__)

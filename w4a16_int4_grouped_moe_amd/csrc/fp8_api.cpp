@@ -130,10 +130,12 @@ int check_experts(const moe_fp8_experts_problem* p) {
 }
 
 // Rows of a bucket's block: a few where an expert has two pairs at most on average, for the
-// kernels that stream weights; else a tile's (how many pairs are local, only the device knows).
-// 48 experts at 7168/2048, microseconds with a few and with tiles: 8 tokens (1.3 pairs) 280 and
-// 321, 16 (2.7) 413 and 376; 256 experts at 2048/1024: 64 tokens (2.0) 250 and 319, 128 (4.0)
-// 334 and 369.
+// kernels that stream weights; else a tile's. Measured with all experts local, microseconds with
+// a few and with tiles: 48 experts at 7168/2048, 8 tokens (1.3 pairs) 280 and 321, 16 (2.7) 413
+// and 376; 256 experts at 2048/1024, 64 tokens (2.0) 250 and 319, 128 (4.0) 334 and 369. How many
+// pairs are local only the device knows, so that the rule counts them all, and takes tiles too
+// early where few are: 48 of 384 experts here, 16 tokens (19 local pairs) 150 with a few rows and
+// 176 with tiles, 64 (75) 325 and 352, 96 (102) 369 and 364.
 int32_t block_of(const moe_fp8_experts_problem* p) {
   const int64_t P = p->num_tokens * p->top_k;
   if (P <= 2 * (int64_t)p->num_experts &&
