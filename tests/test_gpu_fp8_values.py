@@ -119,3 +119,23 @@ def test_dequantised_values_are_fp32_products_rounded():
     assert torch.equal(want, w.codes.float() * s)
     assert torch.equal(moe.fp8_dequantize(w), want.bfloat16())
     assert torch.equal(moe.fp8_dequantize(w, dtype=torch.float16), want.half())
+
+
+@pytest.mark.parametrize("M", [3, 12, 70, 1500])
+def test_small_products_beside_large_ones(M):
+    """448 448 - 448 448 and one product more, in every place of a block of 128: fp32 results keep it whatever its
+    size, and so do bf16 ones of few rows; the FP8 matrix unit from 2^-13 of 2^16 on, the power of two of the
+    large ones' exponents, or in another eight of the block than theirs."""
+    K, N, last = 128, 8504 if M == 1500 else 264, 127
+    for s in (2.0 ** -6, 1.0, 8.0, 64.0):
+        a = torch.zeros((M, K), device="cuda")
+        b = torch.ones((N, K), device="cuda")
+        place = torch.arange(M, device="cuda") % 126 + 1
+        a[torch.arange(M), place] = s
+        a[:, 0], a[:, last], b[:, 0], b[:, last] = 448, -448, 448, 448
+        args = (moe.Fp8(a.to(E4M3), torch.ones(1, M, device="cuda"), 1),
+                moe.Fp8(b.to(E4M3), torch.ones(-(-N // 128), 1, device="cuda"), 128))
+        assert (moe.fp8_matmul(*args, dtype=torch.float32) == s).all()
+        keeps = (place >= 8) & (place < 120) | (s >= 8) | (M <= 16)
+        out = moe.fp8_matmul(*args)
+        assert (out[keeps] == s).all() and (out[~keeps].float().abs() <= 8).all()
